@@ -16,12 +16,15 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIBPATH = os.path.join(_HERE, "libdecodegemm.so")
 
-DG_OP_GEMV_BF16, DG_OP_GATE_UP_SILU, DG_OP_HEAD_FP8_ARGMAX, DG_OP_MOE_W1, DG_OP_MOE_W2, DG_OP_GEMV_A8W8 = range(6)
+DG_OP_GEMV_BF16, DG_OP_GATE_UP_SILU, DG_OP_HEAD_FP8_ARGMAX, DG_OP_MOE_W1, DG_OP_MOE_W2, DG_OP_GEMV_A8W8, DG_OP_GEMV_A4W4 = range(7)
 DG_VAR_DEFAULT, DG_VAR_CC_WARP, DG_VAR_CC_BULK, DG_VAR_TC, DG_VAR_MMA = range(5)
 (DG_OK, DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT, DG_ERR_UNSUPPORTED_SHAPE, DG_ERR_WORKSPACE_TOO_SMALL, DG_ERR_CUDA,
  DG_ERR_TABLE_REFUSED, DG_ERR_NO_DEVICE, DG_ERR_BAD_VARIANT) = range(9)
 DG_DEVERR_BAD_TOPK_ID = 0x1
 DG_DEVERR_WAIT_TIMEOUT = 0x2
+DG_FP4_MX, DG_FP4_NV = range(2)
+DG_LOGITS_BF16, DG_LOGITS_F32 = range(2)
+DG_SCORE_SOFTMAX, DG_SCORE_SIGMOID = range(2)
 
 
 def _rows_buckets():
@@ -56,6 +59,12 @@ class Choice(ctypes.Structure):
 class Shape(ctypes.Structure):
     _fields_ = [("op", ctypes.c_int32), ("M", ctypes.c_int32), ("N", ctypes.c_int32),
                 ("K", ctypes.c_int32), ("topk", ctypes.c_int32), ("E", ctypes.c_int32)]
+
+
+class RouteParams(ctypes.Structure):
+    _fields_ = [("topk", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("score", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class DGError(RuntimeError):
@@ -109,6 +118,13 @@ def lib():
     L.dg_moe_w2.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, Z, P, P]
     L.dg_gemv_a8w8_blockscale.argtypes = [P, P, P, P, I, I, I, P, Z, P, P]
     L.dg_quant_a8_blockscale.argtypes = [P, P, P, I, I, P]
+    L.dg_fp4_scale_bytes.argtypes = [I, I, I]
+    L.dg_fp4_scale_bytes.restype = Z
+    L.dg_quant_fp4_blockscale.argtypes = [P, P, P, P, I, I, I, P]
+    L.dg_dequant_fp4_blockscale.argtypes = [P, P, P, P, I, I, I, P]
+    L.dg_gemv_a4w4_blockscale.argtypes = [P, P, P, P, P, P, I, I, I, I, P, Z, P, P]
+    L.dg_moe_route.argtypes = [P, I, ctypes.c_int64, P, ctypes.POINTER(RouteParams), P, P, I, I, P]
+    L.dg_logprobs.argtypes = [P, I, ctypes.c_int64, P, ctypes.c_float, I, P, P, P, P, P, I, I, P]
     L.dg_select.argtypes = [I, I, I, I, ctypes.POINTER(Choice)]
     L.dg_table_load.argtypes = [ctypes.c_char_p]
     L.dg_table_clear.argtypes = []
@@ -124,7 +140,8 @@ def lib():
                  "dg_gate_up_silu", "dg_head_fp8_argmax", "dg_head_fp8_argmax_noalloc",
                  "dg_head_fp8_argmax_noalloc_status", "dg_head_fp8_argmax_noalloc_scratch", "dg_moe_w1_silu",
                  "dg_moe_w2", "dg_select",
-                 "dg_gemv_a8w8_blockscale", "dg_quant_a8_blockscale",
+                 "dg_gemv_a8w8_blockscale", "dg_quant_a8_blockscale", "dg_quant_fp4_blockscale",
+                 "dg_dequant_fp4_blockscale", "dg_gemv_a4w4_blockscale", "dg_moe_route", "dg_logprobs",
                  "dg_table_load", "dg_table_check", "dg_sweep"):
         getattr(L, name).restype = S
     _lib = L
@@ -312,6 +329,171 @@ def dg_quant_a8_blockscale(x, q=None, sx=None, stream=None):
     return q, sx
 
 
+# The calls below are small enough that marshalling them shows in a decode step: pointers go
+# to ctypes as plain integers, and the stream is read without making a Stream object.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream_of is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream_of(_current_device())
+
+
+def _tensor(t, name, dtype, shape):
+    """Address of a dense CUDA tensor of this dtype and shape, or ValueError."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name}: tensors must be contiguous CUDA tensors")
+    return t.data_ptr()
+
+
+def _scalar(t, name):
+    """Address of one fp32 on the device (None: none)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() != 1:
+        raise ValueError(f"{name}: expected one torch.float32 value")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensors must be contiguous CUDA tensors")
+    return t.data_ptr()
+
+
+def fp4_scale_shape(rows: int, K: int, fmt: int):
+    """Shape of the tiled block scales: [ceil(rows / 128), ceil(blocks / 4), 512] bytes."""
+    block = 16 if fmt == DG_FP4_NV else 32
+    return (rows + 127) // 128, (K // block + 3) // 4, 512
+
+
+def _fp4_fmt(fmt):
+    if fmt not in (DG_FP4_MX, DG_FP4_NV):
+        raise ValueError(f"fmt: {fmt}, expected DG_FP4_MX or DG_FP4_NV")
+
+
+def dg_fp4_scale_bytes(rows: int, K: int, fmt: int) -> int:
+    return int(lib().dg_fp4_scale_bytes(int(rows), int(K), int(fmt)))
+
+
+def dg_quant_fp4_blockscale(x, fmt, g=None, q=None, s=None, stream=None):
+    """(q [M, K/2] uint8 code pairs, s uint8 tiled block scales) of x [M, K] bf16 in the MX or
+    NV 4-bit format; g: the NV tensor scale (one fp32 on the device), None for 1."""
+    M, K = x.shape
+    _fp4_fmt(fmt)
+    if q is None:
+        q = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+    if s is None:
+        s = torch.empty(fp4_scale_shape(M, K, fmt), dtype=torch.uint8, device=x.device)
+    _ok(lib().dg_quant_fp4_blockscale(_tensor(x, "x", torch.bfloat16, (M, K)), _tensor(q, "q", torch.uint8, (M, K // 2)),
+                                      _tensor(s, "s", torch.uint8, fp4_scale_shape(M, K, fmt)), _scalar(g, "g"), M, K,
+                                      fmt, _raw_stream(stream)), "dg_quant_fp4_blockscale")
+    return q, s
+
+
+def dg_dequant_fp4_blockscale(q, s, fmt, g=None, y=None, stream=None):
+    """y [M, K] bf16: the values that the codes and scales of dg_quant_fp4_blockscale stand for."""
+    M, K = q.shape[0], 2 * q.shape[1]
+    _fp4_fmt(fmt)
+    if y is None:
+        y = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
+    _ok(lib().dg_dequant_fp4_blockscale(_tensor(q, "q", torch.uint8, (M, K // 2)),
+                                        _tensor(s, "s", torch.uint8, fp4_scale_shape(M, K, fmt)), _scalar(g, "g"),
+                                        _tensor(y, "y", torch.bfloat16, (M, K)), M, K, fmt, _raw_stream(stream)),
+        "dg_dequant_fp4_blockscale")
+    return y
+
+
+def dg_gemv_a4w4_blockscale(x, Wq, sw, fmt, gx=None, gw=None, y=None, ws=None, choice=None, stream=None):
+    """y [M, N] bf16 = microscaled 4-bit product of x [M, K] (bf16, quantised inside the call with
+    tensor scale gx) and the weights Wq [N, K/2], sw, gw as dg_quant_fp4_blockscale makes them."""
+    M, K = x.shape
+    N = Wq.shape[0]
+    _fp4_fmt(fmt)
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    if ws is None:
+        ws = workspace(DG_OP_GEMV_A4W4, M, N, K, device=x.device)
+    _ok(lib().dg_gemv_a4w4_blockscale(_tensor(x, "x", torch.bfloat16, (M, K)),
+                                      _tensor(Wq, "Wq", torch.uint8, (N, K // 2)),
+                                      _tensor(sw, "sw", torch.uint8, fp4_scale_shape(N, K, fmt)), _scalar(gx, "gx"),
+                                      _scalar(gw, "gw"), _tensor(y, "y", torch.bfloat16, (M, N)), M, N, K, fmt,
+                                      _tensor(ws, "ws", torch.uint8, ws.shape), ws.numel(), _raw_stream(stream),
+                                      _choice(choice)), "dg_gemv_a4w4_blockscale")
+    return y
+
+
+def _logits(t):
+    """(address, element type, row stride) of [M, n] logits: bf16 or fp32, rows dense, any row stride."""
+    if t.dtype is torch.bfloat16:
+        kind = DG_LOGITS_BF16
+    elif t.dtype is torch.float32:
+        kind = DG_LOGITS_F32
+    else:
+        raise ValueError(f"logits: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
+    if t.dim() != 2:
+        raise ValueError(f"logits: shape {tuple(t.shape)}, expected two dimensions")
+    M, n = t.shape
+    ld, one = t.stride()
+    if not t.is_cuda or (one != 1 and n > 1) or (ld < n and M > 1):
+        raise ValueError("logits: rows must be dense and apart, on a CUDA device")
+    return t.data_ptr(), kind, max(ld, n)
+
+
+def dg_moe_route(logits, topk, score=DG_SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1, group_top=1, renorm=True,
+                 scale=1.0, ids=None, w=None, stream=None):
+    """(ids [M, topk] int32, w [M, topk] fp32): the experts and gate weights of each token, as
+    dg_moe_w1_silu and dg_moe_w2 take them, from router logits [M, E]."""
+    p, kind, ld = _logits(logits)
+    M, E = logits.shape
+    if ids is None:
+        ids = torch.empty((M, topk), dtype=torch.int32, device=logits.device)
+    if w is None:
+        w = torch.empty((M, topk), dtype=torch.float32, device=logits.device)
+    prm = RouteParams(topk, n_group, topk_group, group_top, score, 1 if renorm else 0, scale)
+    _ok(lib().dg_moe_route(p, kind, ld, None if bias is None else _tensor(bias, "bias", torch.float32, (E,)), prm,
+                           _tensor(ids, "ids", torch.int32, (M, topk)), _tensor(w, "w", torch.float32, (M, topk)), M, E,
+                           _raw_stream(stream)), "dg_moe_route")
+    return ids, w
+
+
+def dg_logprobs(logits, tokens=None, n_top=0, scale=1.0, logprob=None, rank=None, entropy=None, top_ids=None,
+                top_logprobs=None, stream=None):
+    """Log-probabilities over logits [M, V]: a dict of logprob [M], rank [M] (of tokens [M] int64;
+    None without them), entropy [M], top_ids and top_logprobs [M, n_top] (None at 0)."""
+    p, kind, ld = _logits(logits)
+    M, V = logits.shape
+    dev = logits.device
+    if tokens is not None:
+        if logprob is None:
+            logprob = torch.empty((M,), dtype=torch.float32, device=dev)
+        if rank is None:
+            rank = torch.empty((M,), dtype=torch.int32, device=dev)
+    elif logprob is not None or rank is not None:
+        raise ValueError("tokens: logprob and rank need them")
+    if entropy is None:
+        entropy = torch.empty((M,), dtype=torch.float32, device=dev)
+    if n_top > 0:
+        if top_ids is None:
+            top_ids = torch.empty((M, n_top), dtype=torch.int32, device=dev)
+        if top_logprobs is None:
+            top_logprobs = torch.empty((M, n_top), dtype=torch.float32, device=dev)
+    elif top_ids is not None or top_logprobs is not None:
+        raise ValueError("n_top: top_ids and top_logprobs need it")
+    _ok(lib().dg_logprobs(p, kind, ld, None if tokens is None else _tensor(tokens, "tokens", torch.int64, (M,)), scale,
+                          n_top, None if logprob is None else _tensor(logprob, "logprob", torch.float32, (M,)),
+                          None if rank is None else _tensor(rank, "rank", torch.int32, (M,)),
+                          _tensor(entropy, "entropy", torch.float32, (M,)),
+                          None if n_top <= 0 else _tensor(top_ids, "top_ids", torch.int32, (M, n_top)),
+                          None if n_top <= 0 else _tensor(top_logprobs, "top_logprobs", torch.float32, (M, n_top)),
+                          M, V, _raw_stream(stream)), "dg_logprobs")
+    return {"logprob": logprob, "rank": rank, "entropy": entropy, "top_ids": top_ids, "top_logprobs": top_logprobs}
+
+
 def dg_gate_up_silu(x, W_gu, out=None, ws=None, choice=None, stream=None):
     """out[M,N_half] = silu(x . W_gu[0::2]^T) * (x . W_gu[1::2]^T)."""
     M, K = x.shape
@@ -463,7 +645,7 @@ def dg_table_check(path: str, arch: str, driver_version: int, runtime_version: i
     return int(s), int(n.value), buf.value.decode()
 
 
-_OP_NAMES = ("gemv_bf16", "gate_up_silu", "head_fp8_argmax", "moe_w1_silu", "moe_w2", "gemv_a8w8")
+_OP_NAMES = ("gemv_bf16", "gate_up_silu", "head_fp8_argmax", "moe_w1_silu", "moe_w2", "gemv_a8w8", "gemv_a4w4")
 
 
 def _bucket(M: int) -> int:

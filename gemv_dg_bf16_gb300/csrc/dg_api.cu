@@ -13,6 +13,7 @@
 
 #include "dg_cc_bulk.cuh"
 #include "dg_cc_dense.cuh"
+#include "dg_fp4.cuh"
 #include "dg_internal.h"
 #include "dg_moe.cuh"
 
@@ -226,6 +227,9 @@ void default_choice(dg_op op, int M, int N, int K, dg_choice* out)
         // all rows costs more than one extra launch (12.7 -> 9.7 us at 32 rows).
         out->params[1] = M > 16 ? 1 : 0;
         break;
+    case DG_OP_GEMV_A4W4:
+        out->variant = DG_VAR_TC;          // block-scaled e2m1 MMA
+        break;
     default:
         break;
     }
@@ -319,6 +323,9 @@ size_t dg_workspace_bytes(dg_op op, int M, int N, int K, int topk)
         break;
     case DG_OP_GEMV_A8W8:
         if (M > 0 && K > 0) b = a8_workspace_bytes(M, K);
+        break;
+    case DG_OP_GEMV_A4W4:
+        if (M > 0 && K > 0) b = a4_workspace_bytes(M, K);
         break;
     default:
         break;
@@ -681,6 +688,112 @@ dg_status dg_quant_a8_blockscale(const void* x, void* q, float* sx, int M, int K
     dg_status s;
     if (!current_device(&s)) return s;
     return launch_a8_quant(x, q, sx, M, K, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dg_fp4_scale_bytes(int rows, int K, int fmt)
+{
+    if (rows < 1 || K < 1 || K % 32 != 0 || (fmt != DG_FP4_MX && fmt != DG_FP4_NV)) return 0;
+    return fp4::scale_bytes(rows, K, fmt == DG_FP4_NV);
+}
+
+static dg_status check_fp4(const void* const* ptrs, int n, const float* g, const float* g2, int M, int K, int fmt)
+{
+    for (int i = 0; i < n; ++i)
+        if (!ptrs[i]) return DG_ERR_INVALID_ARG;
+    if (M < 1 || K < 1 || (fmt != DG_FP4_MX && fmt != DG_FP4_NV)) return DG_ERR_INVALID_ARG;
+    if (fmt == DG_FP4_MX && (g || g2)) return DG_ERR_INVALID_ARG;
+    if (K % 32 != 0) return DG_ERR_UNSUPPORTED_SHAPE;
+    for (int i = 0; i < n; ++i)
+        if (!aligned16(ptrs[i])) return DG_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(g2)) & 3u) return DG_ERR_ALIGNMENT;
+    return DG_OK;
+}
+
+dg_status dg_quant_fp4_blockscale(const void* x, void* q, void* s, const float* g, int M, int K, int fmt,
+                                  dg_stream_t stream)
+{
+    const void* ptrs[] = {x, q, s};
+    dg_status st = check_fp4(ptrs, 3, g, nullptr, M, K, fmt);
+    if (st != DG_OK) return st;
+    if (!current_device(&st)) return st;
+    return launch_fp4_quant(fmt == DG_FP4_NV, x, q, s, g, M, K, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dg_status dg_dequant_fp4_blockscale(const void* q, const void* s, const float* g, void* y, int M, int K, int fmt,
+                                    dg_stream_t stream)
+{
+    const void* ptrs[] = {q, s, y};
+    dg_status st = check_fp4(ptrs, 3, g, nullptr, M, K, fmt);
+    if (st != DG_OK) return st;
+    if (!current_device(&st)) return st;
+    return launch_fp4_dequant(fmt == DG_FP4_NV, q, s, g, y, M, K, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw, const float* gx, const float* gw,
+                                  void* y, int M, int N, int K, int fmt, void* ws, size_t ws_bytes,
+                                  dg_stream_t stream, const dg_choice* choice)
+{
+    if (M < 1 || M > kMaxDenseRows || N < 1) return DG_ERR_INVALID_ARG;
+    const void* ptrs[] = {x, Wq, sw, y};
+    dg_status s = check_fp4(ptrs, 4, gx, gw, M, K, fmt);
+    if (s != DG_OK) return s;
+    s = check_common(ptrs, 4, ws, ws_bytes, dg_workspace_bytes(DG_OP_GEMV_A4W4, M, N, K, 0));
+    if (s != DG_OK) return s;
+    const DeviceInfo* dev = current_device(&s);
+    if (!dev) return s;
+    dg_choice c;
+    if ((s = resolve_choice(DG_OP_GEMV_A4W4, M, N, K, choice, &c)) != DG_OK) return s;
+    if (c.variant != DG_VAR_TC) return DG_ERR_BAD_VARIANT;
+    return launch_tc_a4(dev, c, fmt == DG_FP4_NV, x, Wq, sw, gx, gw, y, M, N, K, ws, ws_bytes,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Logits of either type: a pointer on its element's boundary, rows ld >= n elements apart.
+static dg_status check_logits(const void* logits, int type, int64_t ld, int M, int n)
+{
+    if (!logits || M < 1 || n < 1 || ld < n || (type != DG_LOGITS_BF16 && type != DG_LOGITS_F32))
+        return DG_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) & (type == DG_LOGITS_F32 ? 3u : 1u)) return DG_ERR_ALIGNMENT;
+    return DG_OK;
+}
+
+static bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+dg_status dg_moe_route(const void* logits, int logits_type, int64_t ld, const float* bias, const dg_route_params* p,
+                       int32_t* ids, float* w, int M, int E, dg_stream_t stream)
+{
+    dg_status s = check_logits(logits, logits_type, ld, M, E);
+    if (s != DG_OK) return s;
+    if (!p || !ids || !w) return DG_ERR_INVALID_ARG;
+    if (p->n_group < 1 || p->topk_group < 1 || p->topk_group > p->n_group || p->topk < 1 ||
+        (p->group_top != 1 && p->group_top != 2) || (p->renorm != 0 && p->renorm != 1) ||
+        (p->score != DG_SCORE_SOFTMAX && p->score != DG_SCORE_SIGMOID))
+        return DG_ERR_INVALID_ARG;
+    if (E > 1024 || p->topk > 32 || p->n_group > 32 || E % p->n_group != 0 ||
+        p->topk > p->topk_group * (E / p->n_group))
+        return DG_ERR_UNSUPPORTED_SHAPE;
+    if (misaligned(bias, 4) || misaligned(ids, 4) || misaligned(w, 4)) return DG_ERR_ALIGNMENT;
+    if (!current_device(&s)) return s;
+    return launch_route(*p, logits, bias, ids, w, M, E, ld, logits_type == DG_LOGITS_F32,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+dg_status dg_logprobs(const void* logits, int logits_type, int64_t ld, const int64_t* tokens, float scale, int n_top,
+                      float* logprob, int32_t* rank, float* entropy, int32_t* top_ids, float* top_logprobs, int M,
+                      int V, dg_stream_t stream)
+{
+    dg_status s = check_logits(logits, logits_type, ld, M, V);
+    if (s != DG_OK) return s;
+    if (!(scale >= 1e-6f && scale <= 1e6f) || n_top < 0 || (n_top > 0) != (top_ids != nullptr) ||
+        (n_top > 0) != (top_logprobs != nullptr) || (!tokens && (logprob || rank)))
+        return DG_ERR_INVALID_ARG;
+    if (n_top > 32 || M > (1 << 28)) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (misaligned(tokens, 8) || misaligned(logprob, 4) || misaligned(rank, 4) || misaligned(entropy, 4) ||
+        misaligned(top_ids, 4) || misaligned(top_logprobs, 4))
+        return DG_ERR_ALIGNMENT;
+    if (!current_device(&s)) return s;
+    return launch_logprobs(logits, logits_type == DG_LOGITS_F32, ld, tokens, scale, n_top, logprob, rank, entropy,
+                           top_ids, top_logprobs, M, V, reinterpret_cast<cudaStream_t>(stream));
 }
 
 dg_status dg_moe_w1_silu(const void* x, const int32_t* topk_ids, const void* W1, const float* s1,

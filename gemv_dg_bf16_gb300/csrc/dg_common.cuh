@@ -49,6 +49,16 @@ __device__ __forceinline__ uint4 ld_stream(const void* p)
     return v;
 }
 
+// The same for data that a preceding launch may have written: stays behind pdl_wait().
+__device__ __forceinline__ uint4 ld_stream_after(const void* p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // 16-byte load that bypasses L1 (data written by other CTAs of this launch).
 __device__ __forceinline__ uint4 ld_cg16(const void* p)
 {

@@ -55,6 +55,27 @@ dg_status launch_tc_a8(const DeviceInfo* dev, const dg_choice& c, const void* x,
                        void* y, int M, int N, int K, void* ws, size_t ws_bytes, cudaStream_t stream);
 dg_status launch_a8_quant(const void* x, void* q, float* sx, int M, int K, cudaStream_t stream);
 
+// Microscaled 4-bit formats (dg_fp4.cu): quantisation and its inverse; nv: 16-element
+// blocks with e4m3 scales, else 32-element blocks with e8m0 scales.  `early` lets the next
+// launch begin before the codes are written (only where that launch waits for them).
+dg_status launch_fp4_quant(bool nv, const void* x, void* q, void* s, const float* g, int M, int K, bool early,
+                           cudaStream_t stream);
+dg_status launch_fp4_dequant(bool nv, const void* q, const void* s, const float* g, void* y, int M, int K,
+                             cudaStream_t stream);
+// A4W4 block-scaled linear on the tcgen05 family (dg_tc_dense.cu).
+int tc_a4_nsplit(const DeviceInfo* dev, int N, int K, int M, bool fixed);
+size_t a4_workspace_bytes(int M, int K);
+dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const void* x, const void* Wq,
+                       const void* sw, const float* gx, const float* gw, void* y, int M, int N, int K, void* ws,
+                       size_t ws_bytes, cudaStream_t stream);
+
+// Routing of tokens to experts (dg_route.cu) and log-probabilities (dg_logprobs.cu).
+dg_status launch_route(const dg_route_params& p, const void* logits, const float* bias, int32_t* ids, float* w,
+                       int M, int E, long long ld, bool f32, cudaStream_t stream);
+dg_status launch_logprobs(const void* logits, bool f32, long long ld, const int64_t* tokens, float scale, int n_top,
+                          float* logprob, int32_t* rank, float* entropy, int32_t* top_ids, float* top_logprobs, int M,
+                          int V, cudaStream_t stream);
+
 // tcgen05 fp8 head (dg_tc_head.cu): shared memory for (K, stages) and the launcher.
 size_t tc_head_smem(int K, int stages);
 dg_status launch_tc_head(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq,

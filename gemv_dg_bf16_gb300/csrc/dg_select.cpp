@@ -164,6 +164,7 @@ const char* op_name(int op)
     case DG_OP_MOE_W1: return "moe_w1_silu";
     case DG_OP_MOE_W2: return "moe_w2";
     case DG_OP_GEMV_A8W8: return "gemv_a8w8";
+    case DG_OP_GEMV_A4W4: return "gemv_a4w4";
     default: return nullptr;
     }
 }
@@ -187,9 +188,11 @@ bool valid_bucket(int m)
 std::string check_choice(int op, const dg_choice& c)
 {
     if (op == DG_OP_GEMV_A8W8 && c.variant != DG_VAR_TC) return "the A8W8 linear runs on the tensor cores only";
+    if (op == DG_OP_GEMV_A4W4 && c.variant != DG_VAR_TC) return "the A4W4 linear runs on the tensor cores only";
     if (c.variant == DG_VAR_TC) {
         if (c.params[0] != 0 && (c.params[0] < 2 || c.params[0] > 8)) return "pipeline stages must be 2..8";
-        const bool dense = op == DG_OP_GEMV_BF16 || op == DG_OP_GATE_UP_SILU || op == DG_OP_GEMV_A8W8;
+        const bool dense = op == DG_OP_GEMV_BF16 || op == DG_OP_GATE_UP_SILU || op == DG_OP_GEMV_A8W8 ||
+                           op == DG_OP_GEMV_A4W4;
         if (dense && c.params[1] != 0 && c.params[1] != 1)
             return op == DG_OP_GEMV_A8W8 ? "A8W8 quantisation launch flag must be 0 or 1"
                                          : "tensor-core K-split rule must be 0 or 1";
@@ -415,7 +418,8 @@ bool same_family(int a, int b) { return a == b || (cuda_core_family(a) && cuda_c
 // rows; params[1] = 1 fixes it to the shape alone.
 void fix_split(int op, dg_choice* c)
 {
-    if (c->variant == DG_VAR_TC && (op == DG_OP_GEMV_BF16 || op == DG_OP_GATE_UP_SILU)) c->params[1] = 1;
+    if (c->variant == DG_VAR_TC && (op == DG_OP_GEMV_BF16 || op == DG_OP_GATE_UP_SILU || op == DG_OP_GEMV_A4W4))
+        c->params[1] = 1;
 }
 
 }  // namespace
@@ -426,7 +430,7 @@ using namespace dg;
 
 extern "C" {
 
-int dg_selection_space(void) { return 11; }
+int dg_selection_space(void) { return 12; }
 
 const char* dg_build_id(void) { return build_id(); }
 

@@ -189,6 +189,8 @@ struct Problem {
         case DG_OP_GEMV_A8W8:
             return dg_gemv_a8w8_blockscale(x.p, w, static_cast<const float*>(s.p), out.p, M, N, K, ws.p, ws_bytes,
                                            s_, &c);
+        case DG_OP_GEMV_A4W4:
+            return dg_gemv_a4w4_blockscale(x.p, w, s.p, nullptr, nullptr, out.p, M, N, K, topk, ws.p, ws_bytes, s_, &c);
         default:
             return DG_ERR_INVALID_ARG;
         }
@@ -218,6 +220,7 @@ dg_status setup(Problem& P, const DeviceInfo* dev)
         wbytes = size_t(P.E) * 2 * N * K; xbytes = size_t(M) * K * 2; P.out_bytes = size_t(M) * P.topk * N * 2; break;
     case DG_OP_MOE_W2:
         wbytes = size_t(P.E) * N * K; xbytes = size_t(M) * P.topk * K * 2; P.out_bytes = size_t(M) * N * 2; break;
+    case DG_OP_GEMV_A4W4: wbytes = size_t(N) * K / 2; xbytes = size_t(M) * K * 2; P.out_bytes = size_t(M) * N * 2; break;
     case DG_OP_GEMV_A8W8: wbytes = size_t(N) * K; xbytes = size_t(M) * K * 2; P.out_bytes = size_t(M) * N * 2; break;
     default: return DG_ERR_INVALID_ARG;
     }
@@ -242,6 +245,12 @@ dg_status setup(Problem& P, const DeviceInfo* dev)
         const size_t nsc = size_t((N + 127) / 128) * ((K + 127) / 128);
         if (!P.s.alloc(nsc * 4)) return DG_ERR_CUDA;
         fill_f32<<<64, 256>>>(static_cast<float*>(P.s.p), nsc, 31, 1e-4f, 3e-4f);
+    }
+    if (P.op == DG_OP_GEMV_A4W4) {                  // (random code bytes above: any byte is two codes)
+        const size_t n = dg_fp4_scale_bytes(N, K, P.topk);
+        if (n == 0) return DG_ERR_INVALID_ARG;
+        if (!P.s.alloc(n)) return DG_ERR_CUDA;
+        if (cudaMemset(P.s.p, P.topk == DG_FP4_NV ? 0x20 : 0x78, n) != cudaSuccess) return DG_ERR_CUDA;   // 2^-3, 2^-7
     }
     if (P.op == DG_OP_HEAD_FP8_ARGMAX) {
         if (!P.scale.alloc(4)) return DG_ERR_CUDA;

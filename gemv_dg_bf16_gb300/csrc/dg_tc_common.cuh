@@ -136,6 +136,54 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
+// Block-scaled kind::mxf4nvf4 with e2m1 A and B, fp32 accumulate, K-major, M = 128, N = n:
+// block scales as e4m3 (nv, 16 elements each) or e8m0 (32 elements); the scale-factor ids
+// (bits 4-5 for B, 29-30 for A) are added per MMA.
+__host__ __device__ constexpr uint32_t idesc_fp4(int n, bool nv)
+{
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | ((nv ? 0u : 1u) << 23) |
+           (static_cast<uint32_t>(128 >> 4) << 24);
+}
+
+// 64 K elements; sa, sb: tensor-memory columns of the scales (NV: 4 a row, MX: 2).
+template <bool NV>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                        uint32_t acc)
+{
+    if constexpr (NV)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sa), "r"(sb)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sa), "r"(sb)
+            : "memory");
+}
+
+// One 512-byte scale tile (32 rows of 16 bytes, 8-row groups 128 bytes apart, no swizzle)
+// from shared memory to four tensor-memory columns, the same in every lane quarter.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem)
+{
+    const uint64_t desc = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+                          (static_cast<uint64_t>(1) << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Untiled bulk copy to shared memory (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");

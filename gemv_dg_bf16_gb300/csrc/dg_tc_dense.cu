@@ -34,6 +34,7 @@
 #include <mutex>
 
 #include "dg_a8.cuh"
+#include "dg_fp4.cuh"
 #include "dg_internal.h"
 #include "dg_tc_common.cuh"
 
@@ -69,6 +70,13 @@ struct TcArgs {
     // (tmX over q [M, K]) and the activation scales from sxg [M, kbs].
     int preq;
     const float* sxg;
+    // A4W4 (EPI 3, 4): the tiled block scales of the weights and of the activations, scale
+    // tiles along K, and the tensor scales (NULL: 1).
+    const uint8_t* sfw;
+    const uint8_t* sfx;
+    int nkt;
+    const float* gx;
+    const float* gw;
 };
 
 constexpr int kA8Bufs = 4;                        // A8W8: per-block accumulators in flight
@@ -79,6 +87,11 @@ constexpr int kA8Bufs = 4;                        // A8W8: per-block accumulator
 constexpr int kA8MaxBlocks = 16;
 constexpr int kA8Bars = 2 * kA8Bufs + kA8MaxBlocks;
 static_assert(kA8Bars % 2 == 0, "keep the barrier block 16-byte aligned");
+
+// A4W4: K elements per stage (128 bytes of codes a row) and the bytes of a stage's block
+// scales for 128 rows (NV: 4 tiles of 64 elements, MX: 2 of 128).
+constexpr int kA4Block = 256;
+__host__ __device__ constexpr int a4_scale_box(bool nv) { return kA4Block / fp4::tile_k(nv) * fp4::kTileBytes; }
 
 // A8W8: bytes after the ring for the quantised activations [block][MP rows x 128 B] and
 // the combined scales sx * sw [block][MP].
@@ -146,10 +159,18 @@ __device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr)
     return v;
 }
 
-// Four consecutive rows n..n+3 of token t held by one thread (n a multiple of 4).
-template <int EPI>
-__device__ __forceinline__ void emit4(const TcArgs& a, int t, int n, float4 v)
+// A4W4: the product of the tensor scales (read after the kernels before this one).
+__device__ __forceinline__ float tensor_scale(const TcArgs& a)
 {
+    return __fmul_rn(a.gx ? *a.gx : 1.0f, a.gw ? *a.gw : 1.0f);
+}
+
+// Four consecutive rows n..n+3 of token t held by one thread (n a multiple of 4).
+// (A4W4: the tensor scales' product alpha first.)
+template <int EPI>
+__device__ __forceinline__ void emit4(const TcArgs& a, int t, int n, float4 v, float alpha = 1.0f)
+{
+    if constexpr (EPI >= 3) v = make_float4(v.x * alpha, v.y * alpha, v.z * alpha, v.w * alpha);
     if constexpr (EPI != 1) {
         uint16_t* dst = a.out + static_cast<size_t>(t) * a.ld_out + n;
         if (n + 3 < a.N && (a.ld_out % 4) == 0) {
@@ -179,7 +200,7 @@ __device__ __forceinline__ void emit4(const TcArgs& a, int t, int n, float4 v)
 // warp store is contiguous.
 template <int EPI>
 __device__ __forceinline__ void store_staged(const TcArgs& a, const float* S, int rs, int tile, int r0, int r1,
-                                             int etid)
+                                             int etid, float alpha)
 {
     // 16-byte pieces need the range to start on an 8-row boundary (rank slices may
     // start at any multiple of 4) and to hold whole 8-row pieces.
@@ -188,7 +209,8 @@ __device__ __forceinline__ void store_staged(const TcArgs& a, const float* S, in
 #pragma unroll 1
         for (int i = etid; i < a.M * q4; i += 128) {
             const int t = i / q4, c = i - t * q4;
-            emit4<EPI>(a, t, tile * kTileRows + r0 + c * 4, *reinterpret_cast<const float4*>(S + t * rs + c * 4));
+            emit4<EPI>(a, t, tile * kTileRows + r0 + c * 4, *reinterpret_cast<const float4*>(S + t * rs + c * 4),
+                       alpha);
         }
         return;
     }
@@ -199,9 +221,13 @@ __device__ __forceinline__ void store_staged(const TcArgs& a, const float* S, in
     for (int i = etid; i < a.M * q; i += 128) {
         const int t = i / q, c = i - t * q;
         const float* src = S + t * rs + c * 8;
-        const float4 lo = *reinterpret_cast<const float4*>(src);
-        const float4 hi = *reinterpret_cast<const float4*>(src + 4);
+        float4 lo = *reinterpret_cast<const float4*>(src);
+        float4 hi = *reinterpret_cast<const float4*>(src + 4);
         const int n = n0 + c * 8;
+        if constexpr (EPI >= 3) {
+            lo = make_float4(lo.x * alpha, lo.y * alpha, lo.z * alpha, lo.w * alpha);
+            hi = make_float4(hi.x * alpha, hi.y * alpha, hi.z * alpha, hi.w * alpha);
+        }
         if constexpr (EPI != 1) {
             if (vec && n + 7 < a.N) {
                 uint4 w;
@@ -211,7 +237,7 @@ __device__ __forceinline__ void store_staged(const TcArgs& a, const float* S, in
                 w.w = f32_to_bf16_bits(hi.z) | (static_cast<uint32_t>(f32_to_bf16_bits(hi.w)) << 16);
                 *reinterpret_cast<uint4*>(a.out + static_cast<size_t>(t) * a.ld_out + n) = w;
             } else {
-                emit4<EPI>(a, t, n, lo);
+                emit4<EPI>(a, t, n, lo);           // (already scaled)
                 emit4<EPI>(a, t, n + 4, hi);
             }
         } else {
@@ -241,14 +267,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // box they share, and two TMEM accumulators take the two MMA chains -- one wave of
     // CTAs, each activation box loaded once for 256 weight rows.  Every tile's chain is
     // the same as a CTA of its own would run, so the bits do not change.
+    // EPI 3, 4 (A4W4, MX and NV): e2m1 codes of weights and activations, 256 K elements per
+    // stage; the stage also holds both sides' block scales, which tcgen05.cp takes to tensor
+    // memory in front of the MMAs that use them (two buffers, so a copy need not wait for
+    // the previous stage's MMAs).
     constexpr bool A8 = EPI == 2;
-    static_assert(!PAIR || (MP == 256 && !A8), "paired tiles are the 256-token bf16 path");
-    constexpr int KBE = A8 ? kA8Block : kKB;      // K elements per stage
-    constexpr int kXBox = A8 ? 0 : MP * kKB * 2;
+    constexpr bool A4 = EPI >= 3, NV = EPI == 4;
+    static_assert(!PAIR || (MP == 256 && !A8 && !A4), "paired tiles are the 256-token bf16 path");
+    constexpr int KBE = A4 ? kA4Block : (A8 ? kA8Block : kKB);      // K elements per stage
+    constexpr int kXBox = A8 ? 0 : MP * kKB * 2;                    // 128 bytes a row, bf16 or e2m1
+    constexpr int kSfBox = A4 ? a4_scale_box(NV) : 0;
+    constexpr int kXTiles = MP > 128 ? 2 : 1;                       // scale tiles over the tokens
     constexpr int kWBoxes = PAIR ? 2 : 1;
-    constexpr int kStage = kWBox * kWBoxes + kXBox;
-    constexpr uint32_t kCols = A8 ? static_cast<uint32_t>(kA8Bufs * MP) : (PAIR ? 2 * MP : (MP < 32 ? 32 : MP));
-    constexpr uint32_t kIdesc = A8 ? tc::idesc_f8(MP) : tc::idesc_bf16(MP);
+    constexpr int kStage = kWBox * kWBoxes + kXBox + kSfBox * (1 + kXTiles);
+    // A4: accumulator, then two buffers each of the weights' and the activations' scales
+    // (4 columns per 128 rows and MMA).
+    constexpr uint32_t kSfCols = 4u * (kA4Block / fp4::tile_k(NV));
+    constexpr uint32_t kSfw = MP < 32 ? 32 : MP, kSfx = kSfw + 2 * kSfCols;
+    constexpr uint32_t kCols = A4   ? (kSfx + 2 * kSfCols * kXTiles <= 128   ? 128
+                                       : kSfx + 2 * kSfCols * kXTiles <= 256 ? 256
+                                                                             : 512)
+                               : A8 ? static_cast<uint32_t>(kA8Bufs * MP)
+                                    : (PAIR ? 2 * MP : (MP < 32 ? 32 : MP));
+    constexpr uint32_t kIdesc = A4 ? tc::idesc_fp4(MP, NV) : A8 ? tc::idesc_f8(MP) : tc::idesc_bf16(MP);
+    constexpr int kKX = A4 ? KBE / 2 : KBE;       // a stage's width in elements of the tensor maps (A4: bytes)
     constexpr int kExtraBars = A8 ? kA8Bars : 0;
 
     extern __shared__ uint8_t smem_raw[];
@@ -318,17 +360,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Weights are read once: they are the first lines evicted from L2.
             const uint64_t once = tc::policy_evict_first();
             const int pre = nkb < S ? nkb : S;
+            // A4: scale tiles of K-block kb, at most kSfBox bytes a side (the last block may have fewer)
+            constexpr int kSfTiles = A4 ? kSfBox / fp4::kTileBytes : 1;
+            auto sf_bytes = [&](int kb) {
+                const int left = a.nkt - kb * kSfTiles;
+                return static_cast<uint32_t>((left < kSfTiles ? left : kSfTiles) * fp4::kTileBytes);
+            };
+            auto stage_tx = [&](int kb) {
+                if constexpr (A4) return static_cast<uint32_t>(kWBox + kXBox) + sf_bytes(kb) * (1 + kXTiles);
+                return static_cast<uint32_t>(kStage);
+            };
+            auto load_sfw = [&](uint32_t dst, int kb, uint32_t bar) {
+                tc::bulk_load(dst + kWBox + kXBox,
+                              a.sfw + (static_cast<size_t>(tile) * a.nkt + kb * kSfTiles) * fp4::kTileBytes, sf_bytes(kb),
+                              bar);
+            };
+            auto load_sfx = [&](uint32_t dst, int kb, uint32_t bar) {
+#pragma unroll
+                for (int r = 0; r < kXTiles; ++r)
+                    tc::bulk_load(dst + kWBox + kXBox + kSfBox * (1 + r),
+                                  a.sfx + (static_cast<size_t>(r) * a.nkt + kb * kSfTiles) * fp4::kTileBytes,
+                                  sf_bytes(kb), bar);
+            };
             for (int i = 0; i < pre; ++i) {
                 const uint32_t dst = tc::su32(smem + i * kStage);
-                tc::bar_expect_tx(full0 + 8 * i, kStage);
-                tc::tma_2d_hint(dst, &tmW, (kb0 + i) * KBE, tile * kTileRows, full0 + 8 * i, once);
+                tc::bar_expect_tx(full0 + 8 * i, stage_tx(kb0 + i));
+                if constexpr (A4) load_sfw(dst, kb0 + i, full0 + 8 * i);
+                tc::tma_2d_hint(dst, &tmW, (kb0 + i) * kKX, tile * kTileRows, full0 + 8 * i, once);
                 if constexpr (PAIR)        // (rows past N read as zeros when the tile is the last, odd one)
                     tc::tma_2d_hint(dst + kWBox, &tmW, (kb0 + i) * KBE, (tile + 1) * kTileRows, full0 + 8 * i, once);
             }
             pdl_wait();
             if constexpr (!A8)
-                for (int i = 0; i < pre; ++i)
-                    tc::tma_2d(tc::su32(smem + i * kStage) + kWBox * kWBoxes, &tmX, (kb0 + i) * kKB, 0, full0 + 8 * i);
+                for (int i = 0; i < pre; ++i) {
+                    const uint32_t dst = tc::su32(smem + i * kStage);
+                    tc::tma_2d(dst + kWBox * kWBoxes, &tmX, (kb0 + i) * kKX, 0, full0 + 8 * i);
+                    if constexpr (A4) load_sfx(dst, kb0 + i, full0 + 8 * i);
+                }
             if constexpr (A8)
                 if (a.preq)
                     // every block's codes at once (rows M..MP-1 read as zeros), each
@@ -343,8 +411,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t round = static_cast<uint32_t>(i / S);
                 if (!tc::bar_wait(empty0 + 8 * s, (round & 1u) ^ 1u, abort_flag)) break;
                 const uint32_t dst = tc::su32(smem + s * kStage);
-                tc::bar_expect_tx(full0 + 8 * s, kStage);
-                const int k = (kb0 + i) * KBE;
+                tc::bar_expect_tx(full0 + 8 * s, stage_tx(kb0 + i));
+                const int k = (kb0 + i) * kKX;
+                if constexpr (A4) {
+                    load_sfw(dst, kb0 + i, full0 + 8 * s);
+                    load_sfx(dst, kb0 + i, full0 + 8 * s);
+                }
                 tc::tma_2d_hint(dst, &tmW, k, tile * kTileRows, full0 + 8 * s, once);
                 if constexpr (PAIR) tc::tma_2d_hint(dst + kWBox, &tmW, k, (tile + 1) * kTileRows, full0 + 8 * s, once);
                 if constexpr (!A8) tc::tma_2d(dst + kWBox * kWBoxes, &tmX, k, 0, full0 + 8 * s);
@@ -376,6 +448,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    tc::sw128_desc(xa + kk * 32), kIdesc, kk > 0 ? 1u : 0u);
                     tc::commit(empty0 + 8 * s);
                     tc::commit(accf0 + 8 * b);
+                } else if constexpr (A4) {
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t xa = wa + kWBox, sw = xa + kXBox, sx = sw + kSfBox;
+                    const uint32_t cw = tmem + kSfw + (i & 1) * kSfCols;
+                    const uint32_t cx = tmem + kSfx + (i & 1) * kSfCols * kXTiles;
+                    const int kleft = a.K - (kb0 + i) * kA4Block;
+                    const int steps = kleft >= kA4Block ? kA4Block / 64 : (kleft + 63) / 64;      // 64 elements an MMA
+                    constexpr int kPer = fp4::tile_k(NV) / 64;                                    // MMAs per scale tile
+                    // tcgen05.cp and tcgen05.mma of one thread run in order
+                    for (int j = 0; j < (steps + kPer - 1) / kPer; ++j) {
+                        tc::copy_scales(cw + 4 * j, sw + j * fp4::kTileBytes);
+#pragma unroll
+                        for (int r = 0; r < kXTiles; ++r)
+                            tc::copy_scales(cx + 4 * (j * kXTiles + r), sx + r * kSfBox + j * fp4::kTileBytes);
+                    }
+                    for (int kk = 0; kk < steps; ++kk) {
+                        const int j = kk / kPer;
+                        const uint32_t id = static_cast<uint32_t>(kk % kPer) * 2;                 // MX: byte pair 0 or 2
+                        tc::mma_fp4<NV>(tmem, tc::sw128_desc(wa + kk * 32), tc::sw128_desc(xa + kk * 32),
+                                        kIdesc | (id << 4) | (id << 29), cw + 4 * j, cx + 4 * j * kXTiles,
+                                        (i > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc::commit(empty0 + 8 * s);
                 } else {
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t xa = wa + kWBox * kWBoxes;
@@ -533,6 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool ok = tc::bar_wait(accum, 0, abort_flag);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const float alpha = A4 ? tensor_scale(a) : 1.0f;
         // `good` may differ between threads when a wait ran out; every named barrier
         // below is still reached by all 128 epilogue threads.
         const bool good = ok && !*abort_flag;
@@ -555,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (good) store_staged<EPI>(a, S, kTileRows, tile + pt, 0, kTileRows, threadIdx.x - 64);
+                if (good) store_staged<EPI>(a, S, kTileRows, tile + pt, 0, kTileRows, threadIdx.x - 64, alpha);
             }
         } else if (a.push) {
             // Push row `row` of this rank's partial tile (tokens 0..mq-1) into the
@@ -605,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (got && !*abort_flag) store_staged<EPI>(a, S, rs, tile, lo, hi, r);
+            if (got && !*abort_flag) store_staged<EPI>(a, S, rs, tile, lo, hi, r, alpha);
         } else if (good) {
             // Park this rank's partial tile P[t][row] (fp32) in the now idle stage memory.
             float* P = reinterpret_cast<float*>(smem);
@@ -630,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int hi = ((split + 1) * (kTileRows / 4) / a.nsplit) * 4;
             const int w4 = (hi - lo) / 4;
             const int count = w4 * a.M;
+            const float alpha = A4 ? tensor_scale(a) : 1.0f;
             const uint32_t pbase = tc::su32(smem);
             uint32_t peer[kMaxCluster];
 #pragma unroll
@@ -671,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
-                        if (vv[u]) emit4<EPI>(a, tt[u], tile * kTileRows + rr[u], acc[u]);
+                        if (vv[u]) emit4<EPI>(a, tt[u], tile * kTileRows + rr[u], acc[u], alpha);
                 }
             }
         }
@@ -745,6 +842,20 @@ const void* tc_lookup_pair(int epi)
 {
     return epi == 0 ? reinterpret_cast<const void*>(&tc_dense_kernel<256, 0, true>)
                     : reinterpret_cast<const void*>(&tc_dense_kernel<256, 1, true>);
+}
+
+// The A4W4 kernels.
+template <int EPI>
+const void* tc_lookup_a4(int mp)
+{
+    switch (mp) {
+    case 16: return tc_fn<16, EPI>();
+    case 32: return tc_fn<32, EPI>();
+    case 64: return tc_fn<64, EPI>();
+    case 128: return tc_fn<128, EPI>();
+    case 256: return tc_fn<256, EPI>();
+    default: return nullptr;
+    }
 }
 
 size_t stage_bytes_pair() { return 2 * static_cast<size_t>(kWBox) + static_cast<size_t>(256) * kKB * 2; }
@@ -1122,6 +1233,136 @@ dg_status launch_tc_a8(const DeviceInfo* dev, const dg_choice& c, const void* x,
     if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
+    }
+    return DG_OK;
+}
+
+// ------------------------------------------------------------------ A4W4 blockscale
+
+int tc_a4_nsplit(const DeviceInfo* dev, int N, int K, int M, bool fixed)
+{
+    const int tiles = (N + kTileRows - 1) / kTileRows;
+    const int nkb = (K + kA4Block - 1) / kA4Block;
+    // Both CTA slots of every SM up to 128 tokens (a function of the shape alone, so a row's
+    // bits do not depend on how many rows share the call), one above; in one wave of
+    // clusters, and at least 2 K-blocks (512 elements) per rank.
+    const bool two = fixed || tc_mp(M) <= 128;
+    int ns = (two ? 2 : 1) * dev->sm_count / tiles;
+    if (ns > kMaxCluster) ns = kMaxCluster;
+    if (ns > nkb / 2) ns = nkb / 2;
+    while (ns > 1 && tiles > cluster_capacity(dev, two, ns)) --ns;
+    return ns < 1 ? 1 : ns;
+}
+
+size_t a4_workspace_bytes(int M, int K)
+{
+    const size_t q = (static_cast<size_t>(M) * K / 2 + 255) / 256 * 256;
+    // the wider of the two formats' scales
+    return kWsData + q + fp4::scale_bytes(M, K, true);
+}
+
+namespace {
+
+size_t stage_bytes_a4(int mp, bool nv)
+{
+    return kWBox + static_cast<size_t>(mp) * 128 + static_cast<size_t>(a4_scale_box(nv)) * (mp > 128 ? 3 : 2);
+}
+
+size_t smem_bytes_a4(int mp, bool nv, int stages, size_t recv)
+{
+    return 1024 + stages * stage_bytes_a4(mp, nv) + (2 * stages + 2) * 8 + 16 + recv;
+}
+
+}  // namespace
+
+dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const void* x, const void* Wq,
+                       const void* sw, const float* gx, const float* gw, void* y, int M, int N, int K, void* ws,
+                       size_t ws_bytes, cudaStream_t stream)
+{
+    if (M < 1 || M > kMaxDenseRows || K % 32 != 0) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (c.params[1] != 0 && c.params[1] != 1) return DG_ERR_BAD_VARIANT;
+    for (int i = 2; i < 6; ++i)
+        if (c.params[i] != 0) return DG_ERR_BAD_VARIANT;
+    if (ws_bytes < a4_workspace_bytes(M, K)) return DG_ERR_WORKSPACE_TOO_SMALL;
+    const bool fixed = c.params[1] == 1;
+    const int chunk = fixed ? 128 : 256;                 // token rows per launch
+    uint8_t* qws = static_cast<uint8_t*>(ws) + kWsData;
+    uint8_t* sws = qws + (static_cast<size_t>(M) * K / 2 + 255) / 256 * 256;
+    // Every launch is checked before the first is queued.
+    for (int pass = 0; pass < 2; ++pass) {
+        if (pass == 1) {
+            const dg_status st = launch_fp4_quant(nv, x, qws, sws, gx, M, K, true, stream);
+            if (st != DG_OK) return st;
+        }
+        for (int t0 = 0; t0 < M; t0 += chunk) {
+            const int mc = M - t0 < chunk ? M - t0 : chunk;
+            const int mp = tc_mp(mc);
+            const void* fn = nv ? tc_lookup_a4<4>(mp) : tc_lookup_a4<3>(mp);
+            if (!fn) return DG_ERR_BAD_VARIANT;
+            const int ns = tc_a4_nsplit(dev, N, K, mc, fixed);
+            const int mq = (mc + 3) & ~3;
+            size_t recv = mq <= kPushMaxTokens ? recv_bytes(ns, mq) : 0;
+            int stages = c.params[0];
+            if (stages == 0) {
+                stages = mp <= 128 ? 5 : 3;
+                while (stages > 2 && smem_bytes_a4(mp, nv, stages, recv) > (mp <= 128 ? kCoResidentSmem : kMaxDynSmem))
+                    --stages;
+            }
+            if (stages < 2 || stages > 8) return DG_ERR_BAD_VARIANT;
+            // The epilogue stages the tile (or parks the K-split partial) in the ring.
+            if (stages * stage_bytes_a4(mp, nv) < static_cast<size_t>(mp) * kTileRows * 4) return DG_ERR_BAD_VARIANT;
+            size_t smem = smem_bytes_a4(mp, nv, stages, recv);
+            if (smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
+            // Never more co-resident CTAs than their TMEM columns fit in the SM's 512.
+            const size_t cols = mp <= 16 ? 128 : (mp <= 128 ? 256 : 512);
+            const size_t min_smem = 228 * 1024 / (512 / cols + 1) + 1024;
+            if (smem < min_smem) smem = min_smem;
+            if (occupancy(fn, kThreads, smem) < 1) return DG_ERR_UNSUPPORTED_SHAPE;
+            TcArgs a{};
+            a.N = N;
+            a.K = K;
+            a.M = mc;
+            a.tiles = (N + kTileRows - 1) / kTileRows;
+            a.nkb = (K + kA4Block - 1) / kA4Block;
+            a.nsplit = ns;
+            a.push = recv > 0 ? 1 : 0;
+            a.mq = mq;
+            a.slice_max = slice_max(ns);
+            a.stages = stages;
+            a.out = static_cast<uint16_t*>(y) + static_cast<size_t>(t0) * N;
+            a.ld_out = N;
+            a.ws = static_cast<uint8_t*>(ws);
+            a.nkt = fp4::scale_tiles(K, nv);
+            a.sfw = static_cast<const uint8_t*>(sw);
+            a.sfx = sws + static_cast<size_t>(t0 / fp4::kTileRows) * a.nkt * fp4::kTileBytes;
+            a.gx = gx;
+            a.gw = gw;
+            CUtensorMap tmW, tmX;
+            const uint64_t kb = static_cast<uint64_t>(K) / 2;
+            if (!encode_2d(&tmW, Wq, kb, static_cast<uint64_t>(N), 128, kTileRows, true) ||
+                !encode_2d(&tmX, qws + t0 * kb, kb, static_cast<uint64_t>(mc), 128, static_cast<uint32_t>(mp), true))
+                return DG_ERR_CUDA;
+            if (pass == 0) continue;
+            void* args[] = {&tmW, &tmX, &a};
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(a.tiles * a.nsplit));
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = smem;
+            cfg.stream = stream;
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = static_cast<unsigned>(a.nsplit);
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+                cudaGetLastError();
+                return DG_ERR_CUDA;
+            }
+        }
     }
     return DG_OK;
 }

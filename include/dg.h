@@ -14,6 +14,12 @@
  *   dg_gemv_a8w8_blockscale
  *                       e4m3 weights with 128 x 128 block scales, the per-(token,
  *                       128-block) activation quantisation fused in (M <= 64)
+ *   dg_gemv_a4w4_blockscale
+ *                       microscaled 4-bit (e2m1) weights and activations, MX or NV block
+ *                       scales, the activation quantisation inside the call (M <= 512);
+ *                       dg_quant_fp4_blockscale / dg_dequant_fp4_blockscale convert
+ *   dg_moe_route        router logits to the expert ids and gate weights of the MoE calls
+ *   dg_logprobs         log-probability, rank, entropy and top alternatives over logits
  *
  * plus dg_select, which maps (op, M, N, K) to a kernel variant through a
  * per-device shape table written by an on-device sweep (dg_sweep), and a
@@ -79,7 +85,8 @@ typedef enum {
     DG_OP_MOE_W1 = 3,
     DG_OP_MOE_W2 = 4,
     DG_OP_GEMV_A8W8 = 5,
-    DG_OP_COUNT = 6
+    DG_OP_GEMV_A4W4 = 6,
+    DG_OP_COUNT = 7
 } dg_op;
 
 /* Kernel families.  One family serves one (op, M) bucket; variants inside a
@@ -109,7 +116,9 @@ typedef enum {
  *                   batch-invariant mode's choice;
  *                   the two agree up to 128 rows); A8W8: [1] 1 = quantise the activations
  *                   in a launch of its own into the workspace and stream the codes by TMA
- *                   (0 = the quantisation fused into the tensor-core kernel; same bits)
+ *                   (0 = the quantisation fused into the tensor-core kernel; same bits);
+ *                   A4W4: [1] 1 = the K-split by the shape alone at every row count, as
+ *                   for the bf16 linear
  * For the MoE ops (DG_VAR_CC_WARP), params[5] is the work order: 0 or 1 = persistent
  * CTAs walk (active expert, N-tile) units, params[3] the N-tile width in rows (0 =
  * derived); 2 = each CTA owns one contiguous row range of every active expert (W2:
@@ -149,6 +158,7 @@ const char* dg_status_str(dg_status s);
  *   HEAD_FP8_ARGMAX: N = vocabulary rows, K
  *   MOE_W1:          N = I (expert intermediate), K = hidden, topk
  *   MOE_W2:          N = Nout (hidden), K = I, topk
+ *   GEMV_A4W4:       N rows of W, K (either format)
  * Always >= 16 (the device status word). */
 size_t dg_workspace_bytes(dg_op op, int M, int N, int K, int topk);
 
@@ -338,6 +348,101 @@ dg_status dg_gemv_a8w8_blockscale(const void* x, const void* Wq, const float* sw
  * K % 16 == 0; asynchronous on `stream`; argument errors return before any launch. */
 dg_status dg_quant_a8_blockscale(const void* x, void* q, float* sx, int M, int K, dg_stream_t stream);
 
+/* Microscaled 4-bit formats.  A row of K elements is cut into blocks along K, each held as
+ * e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) under one 8-bit scale.  All
+ * steps in binary32, correctly rounded; e2m1() and e4m3() round to nearest even, saturating:
+ *   DG_FP4_MX  32 elements, scale 2^e stored as the byte e + 127 (OCP Microscaling Formats
+ *              v1.0): e = max(floor(log2 amax) - 2, -127), code = e2m1(x * 2^-e)
+ *   DG_FP4_NV  16 elements, scale s stored as e4m3, under one fp32 scale g > 0 of the whole
+ *              tensor (a device pointer; NULL: g = 1):
+ *              s = e4m3(amax / (6 g)), code = e2m1(x / (s g)), 0 where s is 0
+ * A block that holds an infinity or a NaN gets the format's NaN scale (0xFF, 0x7F) and zero
+ * codes.  An all-zero block has zero codes.
+ * Codes: [rows, K / 2] bytes, the element of lower index in the low nibble, the sign in the
+ * nibble's high bit.  Scales: [ceil(rows / 128)][ceil(blocks / 4)] tiles of 512 bytes, the
+ * scale of row r, block b at byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of tile
+ * (r / 128, b / 4); bytes of rows and blocks past the end are zero (a linear reads the
+ * blocks past the end: they must not be NaN).  dg_fp4_scale_bytes gives the size. */
+#define DG_FP4_MX 0
+#define DG_FP4_NV 1
+size_t dg_fp4_scale_bytes(int rows, int K, int fmt);   /* 0 for a bad argument */
+
+/* q, s = the codes and tiled scales of x [M, K] bf16 (activations, or weights with M = N).
+ * M >= 1, K % 32 == 0; g NULL with DG_FP4_MX.  Asynchronous on `stream`; a linear launched
+ * after it may read q and s as its weights. */
+dg_status dg_quant_fp4_blockscale(const void* x, void* q, void* s, const float* g, int M, int K, int fmt,
+                                  dg_stream_t stream);
+
+/* y [M, K] bf16 = the values that q and s stand for: bf16_rn(code * (scale * g)), products in
+ * binary32 (MX: exact unless the value leaves bf16's range).  A NaN scale gives NaN. */
+dg_status dg_dequant_fp4_blockscale(const void* q, const void* s, const float* g, void* y, int M, int K, int fmt,
+                                    dg_stream_t stream);
+
+/* Decode linear on microscaled 4-bit operands:
+ *   qx, sx  = dg_quant_fp4_blockscale(x, gx)                       (inside the call)
+ *   y[m, n] = bf16_rn( (gx * gw) * sum_k (qx[m,k] sx[m,k]) * (Wq[n,k] sw[n,k]) )   fp32 sum
+ * x [M, K] bf16, Wq [N, K / 2] codes and sw tiled scales of the weights in the same format,
+ * gx, gw: device pointers to the tensor scales of the activations (calibrated ahead) and of
+ * the weights (NULL: 1; both NULL with DG_FP4_MX), y [M, N] bf16.
+ * 1 <= M <= 512, K % 32 == 0.  Tensor cores only (DG_VAR_TC; params[0] pipeline stages,
+ * params[1] the K-split rule).  Up to 128 rows the K-split is fixed by (N, K) on a given
+ * device, so output row m depends on input row m alone; with DG_NUMERICS_BATCH_INVARIANT (or
+ * params[1] = 1) at every M.  Non-finite activations give NaN outputs for their token.  ws:
+ * the status word, and the codes and scales of the activations. */
+dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw, const float* gx, const float* gw,
+                                  void* y, int M, int N, int K, int fmt, void* ws, size_t ws_bytes,
+                                  dg_stream_t stream, const dg_choice* choice);
+
+/* Element type of the logits that dg_moe_route and dg_logprobs read.  For these two calls the
+ * pointers need their element's alignment only, and row m of the logits starts at
+ * logits + m * ld elements (ld >= the row's length). */
+#define DG_LOGITS_BF16 0
+#define DG_LOGITS_F32 1
+
+/* Routing of tokens to experts: the topk_ids and gate weights of dg_moe_w1_silu / dg_moe_w2
+ * from router logits.  Per token, in binary32 (expf, divisions correctly rounded):
+ *   p[e]   = 1 / (1 + exp(-x[e]))                                DG_SCORE_SIGMOID
+ *          = exp(x[e] - max x) / sum exp(x - max x)              DG_SCORE_SOFTMAX
+ *   key[e] = p[e] + bias[e]       (bias NULL: p[e]); experts whose logit is -inf or NaN have
+ *            no key: they are never picked and add nothing to the sum
+ *   with n_group > 1 the experts are n_group equal runs; a run's score is its largest key
+ *            (group_top 1) or the sum of its two largest (group_top 2; of one if it has one),
+ *            and only the topk_group best runs keep their keys
+ *   ids    = the topk largest keys in descending order; equal keys (and equal runs) go to the
+ *            lower index; a slot that finds none holds -1 with weight 0
+ *   w      = p[ids], divided by their sum if renorm (0 where the sum is 0), times scale
+ * logits [M, E] (ld), bias [E] fp32 or NULL, ids [M, topk] int32, w [M, topk] fp32.
+ * M >= 1, 1 <= E <= 1024, 1 <= topk <= 32 and topk <= topk_group * E / n_group,
+ * 1 <= n_group <= 32 dividing E, 1 <= topk_group <= n_group. */
+#define DG_SCORE_SOFTMAX 0
+#define DG_SCORE_SIGMOID 1
+typedef struct {
+    int32_t topk, n_group, topk_group, group_top;
+    int32_t score;           /* DG_SCORE_* */
+    int32_t renorm;          /* 0 or 1 */
+    float scale;
+} dg_route_params;
+dg_status dg_moe_route(const void* logits, int logits_type, int64_t ld, const float* bias, const dg_route_params* p,
+                       int32_t* ids, float* w, int M, int E, dg_stream_t stream);
+
+/* Log-probabilities over logits (those of dg_head_fp8_argmax, or a prompt's).  With
+ * z = scale * x (scale > 0: one over the temperature) and lse = log sum exp z:
+ *   logprob[m] = z[m, tokens[m]] - lse[m]
+ *   rank[m]    = how many logits of the row are larger than the token's
+ *   entropy[m] = lse[m] - sum softmax(z) z                          (nats)
+ *   top_ids, top_logprobs [M, n_top]: the n_top largest logits in descending order, equal
+ *                ones by the lower index, and their log-probabilities
+ * Logits of -inf are masked: probability 0, never an alternative.  A row with nothing else
+ * gives logprob -inf and entropy 0; alternatives that a row lacks are id -1, -inf.  A NaN or
+ * +inf in a row makes its logprob, entropy and top_logprobs NaN; NaN is never an alternative.
+ * A token outside [0, V) gives logprob NaN and rank -1.
+ * logits [M, V] (ld), tokens [M] int64 or NULL (then logprob and rank are NULL too); each of
+ * logprob [M] fp32, rank [M] int32, entropy [M] fp32 may be NULL; 0 <= n_top <= 32 (both top
+ * pointers NULL at 0).  M >= 1, V >= 1, 1e-6 <= scale <= 1e6. */
+dg_status dg_logprobs(const void* logits, int logits_type, int64_t ld, const int64_t* tokens, float scale, int n_top,
+                      float* logprob, int32_t* rank, float* entropy, int32_t* top_ids, float* top_logprobs, int M,
+                      int V, dg_stream_t stream);
+
 /* ---------------------------------------------------------------- selection */
 
 /* Kernel choice for (op, M, N, K): the loaded table's entry for M padded up to
@@ -386,7 +491,8 @@ dg_status dg_table_check(const char* path, const char* arch, int driver_version,
  * "Rejected paths" (re-measure every row against the incumbent in context).
  * Each record names the op and its sizes as dg_workspace_bytes does (N = N_half
  * for gate/up, N = I and K = hidden for MoE W1, N = Nout and K = I for MoE W2);
- * E is the expert count (0 = 128).  The table is written to out_path as JSON with
+ * E is the expert count (0 = 128); for A4W4 topk names the format (DG_FP4_*) that is
+ * measured, and the pick serves both.  The table is written to out_path as JSON with
  * this build's identity.  The sweep allocates and frees its own device buffers
  * (it is an offline tool, not a decode-loop call) and synchronises the device.
  * Returns the first error met; shapes after it are not measured. */
