@@ -702,7 +702,7 @@ static dg_status check_fp4(const void* const* ptrs, int n, const float* g, const
         if (!ptrs[i]) return DG_ERR_INVALID_ARG;
     if (M < 1 || K < 1 || (fmt != DG_FP4_MX && fmt != DG_FP4_NV)) return DG_ERR_INVALID_ARG;
     if (fmt == DG_FP4_MX && (g || g2)) return DG_ERR_INVALID_ARG;
-    if (K % 32 != 0) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (K % 32 != 0 || M > 0x7fffff00) return DG_ERR_UNSUPPORTED_SHAPE;
     for (int i = 0; i < n; ++i)
         if (!aligned16(ptrs[i])) return DG_ERR_ALIGNMENT;
     if ((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(g2)) & 3u) return DG_ERR_ALIGNMENT;
@@ -716,7 +716,7 @@ dg_status dg_quant_fp4_blockscale(const void* x, void* q, void* s, const float* 
     dg_status st = check_fp4(ptrs, 3, g, nullptr, M, K, fmt);
     if (st != DG_OK) return st;
     if (!current_device(&st)) return st;
-    return launch_fp4_quant(fmt == DG_FP4_NV, x, q, s, g, M, K, false, reinterpret_cast<cudaStream_t>(stream));
+    return launch_fp4_quant(fmt == DG_FP4_NV, x, q, s, g, M, K, fp4::kTileRows, false, reinterpret_cast<cudaStream_t>(stream));
 }
 
 dg_status dg_dequant_fp4_blockscale(const void* q, const void* s, const float* g, void* y, int M, int K, int fmt,

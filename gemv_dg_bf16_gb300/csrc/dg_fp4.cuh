@@ -50,6 +50,7 @@ struct Scale {
     uint32_t byte;
     float f;           // MX: 2^-e; NV: s g
     bool live;
+    bool plain;        // NV: operands or quotients leave the range that encode8's division is for
 };
 
 // amax_bits: the largest |x| of the block, as bits (an integer maximum keeps NaN on top).
@@ -61,11 +62,13 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax_bits, float g6, float
         r.byte = NV ? 0x7fu : 0xffu;
         r.f = 1.0f;
         r.live = false;
+        r.plain = false;
     } else if constexpr (NV) {
         const uint32_t c = tc::to_e4m3x2(__fdiv_rn(__uint_as_float(amax_bits), g6), 0.0f) & 0xffu;
         r.byte = c;
         r.f = __fmul_rn(e4m3_value(c), g);
         r.live = c != 0;
+        r.plain = !(r.f >= 0x1p-100f && r.f <= 0x1p100f && __uint_as_float(amax_bits) <= r.f * 0x1p20f);
     } else {
         // bf16 magnitudes: the exponent field, or the leading bit of a subnormal
         int e = static_cast<int>(amax_bits >> 23) - 127 - 2;
@@ -73,15 +76,9 @@ __device__ __forceinline__ Scale block_scale(uint32_t amax_bits, float g6, float
         r.byte = static_cast<uint32_t>(e + 127);
         r.f = pow2(-e);
         r.live = amax_bits != 0;
+        r.plain = false;
     }
     return r;
-}
-
-template <bool NV>
-__device__ __forceinline__ float scaled(float x, const Scale& s)
-{
-    if constexpr (NV) return __fdiv_rn(x, s.f);
-    return __fmul_rn(x, s.f);
 }
 
 // Eight values -> eight codes (element i in nibble i).
@@ -97,6 +94,35 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float (&v)[8])
         : "=r"(r)
         : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
+}
+
+// Codes of eight elements of a block.  NV divides by s g: with r the correctly rounded
+// reciprocal and q within an ulp of x / f, q + r (x - q f) in fused steps is the correctly
+// rounded quotient (P. W. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990) -- three instructions an element for a division's dozen.
+// Where the remainder or the quotient could leave the normal range (divisors outside
+// 2^-100 .. 2^100, a scale that saturated far below its block): plain division.
+template <bool NV>
+__device__ __forceinline__ uint32_t encode8(float (&v)[8], const Scale& s)
+{
+    if constexpr (NV) {
+        if (!s.plain) {
+            const float r = __frcp_rn(s.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float q = __fmul_rn(v[i], r);
+                v[i] = __fmaf_rn(__fmaf_rn(-q, s.f, v[i]), r, q);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], s.f);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], s.f);
+    }
+    const uint32_t c = to_e2m1x8(v);
+    return s.live ? c : 0u;
 }
 
 // Two codes of byte j of `codes` -> fp32 (exact).
@@ -124,17 +150,13 @@ __device__ __forceinline__ void unpack8(const uint4& a, float (&v)[8])
     }
 }
 
-// Largest magnitude of eight bf16 values, as fp32 bits.
+// Largest magnitude of eight bf16 values, as fp32 bits: bf16 magnitudes order as 16-bit
+// integers, two a word.
 __device__ __forceinline__ uint32_t amax8(const uint4& a)
 {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m = max(m, (w[i] << 16) & 0x7fff0000u);
-        m = max(m, w[i] & 0x7fff0000u);
-    }
-    return m;
+    const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu),
+                                __vmaxu2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu));
+    return max(m & 0xffff0000u, m << 16);
 }
 
 }  // namespace fp4

@@ -58,12 +58,12 @@ dg_status launch_a8_quant(const void* x, void* q, float* sx, int M, int K, cudaS
 // Microscaled 4-bit formats (dg_fp4.cu): quantisation and its inverse; nv: 16-element
 // blocks with e4m3 scales, else 32-element blocks with e8m0 scales.  `early` lets the next
 // launch begin before the codes are written (only where that launch waits for them).
-dg_status launch_fp4_quant(bool nv, const void* x, void* q, void* s, const float* g, int M, int K, bool early,
-                           cudaStream_t stream);
+// tile_rows: rows that share a scale tile, 128 but for the linear's groups of fewer tokens.
+dg_status launch_fp4_quant(bool nv, const void* x, void* q, void* s, const float* g, int M, int K, int tile_rows,
+                           bool early, cudaStream_t stream);
 dg_status launch_fp4_dequant(bool nv, const void* q, const void* s, const float* g, void* y, int M, int K,
                              cudaStream_t stream);
 // A4W4 block-scaled linear on the tcgen05 family (dg_tc_dense.cu).
-int tc_a4_nsplit(const DeviceInfo* dev, int N, int K, int M, bool fixed);
 size_t a4_workspace_bytes(int M, int K);
 dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const void* x, const void* Wq,
                        const void* sw, const float* gx, const float* gw, void* y, int M, int N, int K, void* ws,

@@ -75,6 +75,7 @@ struct TcArgs {
     const uint8_t* sfw;
     const uint8_t* sfx;
     int nkt;
+    int groups, tg;        // token groups of tg rows (one CTA or cluster each), M rows in all
     const float* gx;
     const float* gw;
 };
@@ -88,6 +89,8 @@ constexpr int kA8MaxBlocks = 16;
 constexpr int kA8Bars = 2 * kA8Bufs + kA8MaxBlocks;
 static_assert(kA8Bars % 2 == 0, "keep the barrier block 16-byte aligned");
 
+// A4W4: the "activations quantised" barrier (and one to keep the block a multiple of 16 bytes).
+constexpr int kA4Bars = 2;
 // A4W4: K elements per stage (128 bytes of codes a row) and the bytes of a stage's block
 // scales for 128 rows (NV: 4 tiles of 64 elements, MX: 2 of 128).
 constexpr int kA4Block = 256;
@@ -256,6 +259,39 @@ __device__ __forceinline__ void store_staged(const TcArgs& a, const float* S, in
     }
 }
 
+// A4W4: this rank's share of the tokens (contiguous), folded over the ranks in rank order: a
+// warp takes a token's 128 rows, 4 a lane, with the loads of U tokens from all ranks (at
+// most R) in flight, and writes 256 bytes of its output row.
+template <int EPI, int R, int U>
+__device__ __forceinline__ void fold_tokens(const TcArgs& a, uint32_t parked, int rank, int tile, int t0, int rows,
+                                            int w, int lane)
+{
+    const float alpha = tensor_scale(a);
+    const int lo = rows * rank / a.nsplit, hi = rows * (rank + 1) / a.nsplit;
+    uint32_t peer[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) peer[r] = r < a.nsplit ? map_to_rank(parked, r) : 0u;
+#pragma unroll 1
+    for (int t = lo + w; t < hi; t += 4 * U) {
+        float4 p[U][R];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < a.nsplit && t + 4 * u < hi)
+                    p[u][r] = ld_dsmem_f32x4(peer[r] + static_cast<uint32_t>(((t + 4 * u) * kTileRows + lane * 4) * 4));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + 4 * u >= hi) break;
+            float4 s = p[u][0];
+#pragma unroll
+            for (int r = 1; r < R; ++r)
+                if (r < a.nsplit) s = make_float4(s.x + p[u][r].x, s.y + p[u][r].y, s.z + p[u][r].z, s.w + p[u][r].w);
+            emit4<EPI>(a, t0 + t + 4 * u, tile * kTileRows + lane * 4, s, alpha);
+        }
+    }
+}
+
 template <int MP, int EPI, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     tc_dense_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, TcArgs a)
@@ -268,37 +304,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     // CTAs, each activation box loaded once for 256 weight rows.  Every tile's chain is
     // the same as a CTA of its own would run, so the bits do not change.
     // EPI 3, 4 (A4W4, MX and NV): e2m1 codes of weights and activations, 256 K elements per
-    // stage; the stage also holds both sides' block scales, which tcgen05.cp takes to tensor
-    // memory in front of the MMAs that use them (two buffers, so a copy need not wait for
-    // the previous stage's MMAs).
+    // stage, and the weights' block scales; tcgen05.cp takes the scales to tensor memory in
+    // front of the MMAs that use them (two buffers, so a copy need not wait for the previous
+    // stage's MMAs).  The activations' codes and scales come with each stage from a launch
+    // ahead (preq), or the epilogue warps quantise the rank's whole K range into shared
+    // memory beside the ring (few rows), and a stage holds the weights' part only.
     constexpr bool A8 = EPI == 2;
     constexpr bool A4 = EPI >= 3, NV = EPI == 4;
     static_assert(!PAIR || (MP == 256 && !A8 && !A4), "paired tiles are the 256-token bf16 path");
     constexpr int KBE = A4 ? kA4Block : (A8 ? kA8Block : kKB);      // K elements per stage
     constexpr int kXBox = A8 ? 0 : MP * kKB * 2;                    // 128 bytes a row, bf16 or e2m1
     constexpr int kSfBox = A4 ? a4_scale_box(NV) : 0;
-    constexpr int kXTiles = MP > 128 ? 2 : 1;                       // scale tiles over the tokens
+    constexpr int kSfTiles = A4 ? kSfBox / fp4::kTileBytes : 1;     // scale tiles along a stage's K
+    static_assert(!A4 || MP <= fp4::kTileRows, "one scale tile over a token group");
     constexpr int kWBoxes = PAIR ? 2 : 1;
-    constexpr int kStage = kWBox * kWBoxes + kXBox + kSfBox * (1 + kXTiles);
+    constexpr int kXOff = kWBox * kWBoxes + kSfBox;                 // weights, their scales, activations, their scales
+    constexpr int kXSf = kXOff + kXBox;
+    constexpr int kFullStage = kXSf + kSfBox;
+    const int kStage = (A4 && !a.preq) ? kXOff : kFullStage;
+    constexpr int kXBlock = kXBox + kSfBox;                         // A4 without preq: one K-block beside the ring
     // A4: accumulator, then two buffers each of the weights' and the activations' scales
     // (4 columns per 128 rows and MMA).
     constexpr uint32_t kSfCols = 4u * (kA4Block / fp4::tile_k(NV));
     constexpr uint32_t kSfw = MP < 32 ? 32 : MP, kSfx = kSfw + 2 * kSfCols;
-    constexpr uint32_t kCols = A4   ? (kSfx + 2 * kSfCols * kXTiles <= 128   ? 128
-                                       : kSfx + 2 * kSfCols * kXTiles <= 256 ? 256
-                                                                             : 512)
+    constexpr uint32_t kCols = A4   ? (kSfx + 2 * kSfCols <= 128 ? 128 : 256)
                                : A8 ? static_cast<uint32_t>(kA8Bufs * MP)
                                     : (PAIR ? 2 * MP : (MP < 32 ? 32 : MP));
     constexpr uint32_t kIdesc = A4 ? tc::idesc_fp4(MP, NV) : A8 ? tc::idesc_f8(MP) : tc::idesc_bf16(MP);
     constexpr int kKX = A4 ? KBE / 2 : KBE;       // a stage's width in elements of the tensor maps (A4: bytes)
-    constexpr int kExtraBars = A8 ? kA8Bars : 0;
+    constexpr int kExtraBars = A8 ? kA8Bars : A4 ? kA4Bars : 0;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int S = a.stages;
     uint8_t* xq = smem + S * kStage;                                            // A8: [block][MP x 128 B]
     float* sxs = reinterpret_cast<float*>(xq + static_cast<size_t>(a.xq_blocks) * MP * kA8Block);   // A8: [block][MP]
-    const size_t xtra = A8 ? a8_extra_bytes(a.xq_blocks, MP) : 0;
+    const size_t xtra = A8 ? a8_extra_bytes(a.xq_blocks, MP) : A4 ? static_cast<size_t>(a.xq_blocks) * kXBlock : 0;
     // full[S], empty[S], accum, recv (+ A8: acc_full[4], acc_empty[4], x_ready)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S * kStage + xtra);
     const int nbars = 2 * S + 2 + kExtraBars;
@@ -310,8 +351,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool clustered = a.nsplit > 1;
     // the parked partial tile takes the padded stride when the idle ring holds it
-    const int pstride = static_cast<size_t>(S) * kStage >= static_cast<size_t>(MP) * kPStride * 4 ? kPStride : kTileRows;
-    const int tile = PAIR ? 2 * static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) / a.nsplit;
+    const int pstride = A4 ? kTileRows : static_cast<size_t>(S) * kStage >= static_cast<size_t>(MP) * kPStride * 4 ? kPStride : kTileRows;
+    int tile = PAIR ? 2 * static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) / a.nsplit;
+    // A4: token rows [t0, t0 + rows_here) of the call; groups of one tile run side by side, so
+    // the tile's weights come from HBM once.
+    int group = 0, t0 = 0, rows_here = a.M;
+    if constexpr (A4) {
+        group = tile % a.groups;
+        tile /= a.groups;
+        t0 = group * a.tg;
+        rows_here = a.M - t0 < a.tg ? a.M - t0 : a.tg;
+    }
     const int ntiles_here = PAIR ? (tile + 1 < a.tiles ? 2 : 1) : 1;
     const int split = clustered ? static_cast<int>(cluster_rank()) : 0;
     const int kb0 = static_cast<int>((static_cast<long long>(split) * a.nkb) / a.nsplit);
@@ -327,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int i = 0; i < kA8MaxBlocks; ++i) tc::bar_init(tc::su32(bars + 2 * S + 2 + 2 * kA8Bufs + i), 1);
         }
+        if constexpr (A4) tc::bar_init(tc::su32(bars + 2 * S + 2), 4);       // one per epilogue warp
         if (clustered && a.push) {
             // every rank pushes this rank's slice of rows, mq tokens each
             const int rows = slice_lo(split + 1, a.nsplit) - slice_lo(split, a.nsplit);
@@ -354,33 +405,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     pdl_launch_dependents();
     if (warp == 0) {
-        if (lane == 0) {
+        if (tc::elect_one()) {
             // Weight boxes of the first ring fill do not depend on earlier kernels:
             // issue them before waiting, the activation boxes after.
             // Weights are read once: they are the first lines evicted from L2.
             const uint64_t once = tc::policy_evict_first();
             const int pre = nkb < S ? nkb : S;
             // A4: scale tiles of K-block kb, at most kSfBox bytes a side (the last block may have fewer)
-            constexpr int kSfTiles = A4 ? kSfBox / fp4::kTileBytes : 1;
             auto sf_bytes = [&](int kb) {
                 const int left = a.nkt - kb * kSfTiles;
                 return static_cast<uint32_t>((left < kSfTiles ? left : kSfTiles) * fp4::kTileBytes);
             };
             auto stage_tx = [&](int kb) {
-                if constexpr (A4) return static_cast<uint32_t>(kWBox + kXBox) + sf_bytes(kb) * (1 + kXTiles);
-                return static_cast<uint32_t>(kStage);
+                if constexpr (A4)
+                    return a.preq ? static_cast<uint32_t>(kWBox + kXBox) + sf_bytes(kb) * 2
+                                  : static_cast<uint32_t>(kWBox) + sf_bytes(kb);
+                return static_cast<uint32_t>(kFullStage);
             };
             auto load_sfw = [&](uint32_t dst, int kb, uint32_t bar) {
-                tc::bulk_load(dst + kWBox + kXBox,
+                tc::bulk_load(dst + kWBox,
                               a.sfw + (static_cast<size_t>(tile) * a.nkt + kb * kSfTiles) * fp4::kTileBytes, sf_bytes(kb),
                               bar);
             };
             auto load_sfx = [&](uint32_t dst, int kb, uint32_t bar) {
-#pragma unroll
-                for (int r = 0; r < kXTiles; ++r)
-                    tc::bulk_load(dst + kWBox + kXBox + kSfBox * (1 + r),
-                                  a.sfx + (static_cast<size_t>(r) * a.nkt + kb * kSfTiles) * fp4::kTileBytes,
-                                  sf_bytes(kb), bar);
+                // A group's scales start a tile row of their own: the MMA reads them from the first
+                // of four tensor-memory columns, which has to be a multiple of four.
+                tc::bulk_load(dst + kXSf, a.sfx + (static_cast<size_t>(group) * a.nkt + kb * kSfTiles) * fp4::kTileBytes,
+                              sf_bytes(kb), bar);
             };
             for (int i = 0; i < pre; ++i) {
                 const uint32_t dst = tc::su32(smem + i * kStage);
@@ -391,12 +442,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tma_2d_hint(dst + kWBox, &tmW, (kb0 + i) * KBE, (tile + 1) * kTileRows, full0 + 8 * i, once);
             }
             pdl_wait();
-            if constexpr (!A8)
-                for (int i = 0; i < pre; ++i) {
-                    const uint32_t dst = tc::su32(smem + i * kStage);
-                    tc::tma_2d(dst + kWBox * kWBoxes, &tmX, (kb0 + i) * kKX, 0, full0 + 8 * i);
-                    if constexpr (A4) load_sfx(dst, kb0 + i, full0 + 8 * i);
-                }
+            const bool with_x = !A8 && (!A4 || a.preq);
+            auto load_x = [&](uint32_t dst, int kb, uint32_t bar) {
+                tc::tma_2d(dst + kXOff, &tmX, kb * kKX, t0, bar);
+                if constexpr (A4) load_sfx(dst, kb, bar);
+            };
+            if (with_x)
+                for (int i = 0; i < pre; ++i) load_x(tc::su32(smem + i * kStage), kb0 + i, full0 + 8 * i);
             if constexpr (A8)
                 if (a.preq)
                     // every block's codes at once (rows M..MP-1 read as zeros), each
@@ -406,30 +458,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc::tma_2d(tc::su32(xq + static_cast<size_t>(i) * MP * kA8Block), &tmX, (kb0 + i) * kA8Block,
                                    0, xfull0 + 8 * i);
                     }
+            int s = 0;                       // stage and round of K-block i (pre is S where there is a second round)
+            uint32_t round = 1;
             for (int i = pre; i < nkb; ++i) {
-                const int s = i % S;
-                const uint32_t round = static_cast<uint32_t>(i / S);
                 if (!tc::bar_wait(empty0 + 8 * s, (round & 1u) ^ 1u, abort_flag)) break;
                 const uint32_t dst = tc::su32(smem + s * kStage);
                 tc::bar_expect_tx(full0 + 8 * s, stage_tx(kb0 + i));
                 const int k = (kb0 + i) * kKX;
-                if constexpr (A4) {
-                    load_sfw(dst, kb0 + i, full0 + 8 * s);
-                    load_sfx(dst, kb0 + i, full0 + 8 * s);
-                }
+                if constexpr (A4) load_sfw(dst, kb0 + i, full0 + 8 * s);
                 tc::tma_2d_hint(dst, &tmW, k, tile * kTileRows, full0 + 8 * s, once);
                 if constexpr (PAIR) tc::tma_2d_hint(dst + kWBox, &tmW, k, (tile + 1) * kTileRows, full0 + 8 * s, once);
-                if constexpr (!A8) tc::tma_2d(dst + kWBox * kWBoxes, &tmX, k, 0, full0 + 8 * s);
+                if (with_x) load_x(dst, kb0 + i, full0 + 8 * s);
+                if (++s == S) {
+                    s = 0;
+                    ++round;
+                }
             }
         } else {
             pdl_wait();
         }
     } else if (warp == 1) {
         pdl_wait();
-        if (lane == 0) {
+        if (tc::elect_one()) {
+            int s = -1;
+            uint32_t round = 0;
             for (int i = 0; i < nkb; ++i) {
-                const int s = i % S;
-                const uint32_t round = static_cast<uint32_t>(i / S);
+                if (++s == S) {
+                    s = 0;
+                    ++round;
+                }
                 if (!tc::bar_wait(full0 + 8 * s, round & 1u, abort_flag)) break;
                 const uint32_t wa = tc::su32(smem + s * kStage);
                 if constexpr (A8) {
@@ -449,25 +506,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::commit(empty0 + 8 * s);
                     tc::commit(accf0 + 8 * b);
                 } else if constexpr (A4) {
+                    if (!a.preq && i == 0 && !tc::bar_wait(accf0, 0, abort_flag)) break;     // activations quantised
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t xa = wa + kWBox, sw = xa + kXBox, sx = sw + kSfBox;
+                    const uint32_t sw = wa + kWBox;
+                    const uint32_t xa = a.preq ? wa + kXOff : tc::su32(xq + static_cast<size_t>(i) * kXBlock);
+                    const uint32_t sx = xa + kXBox;
                     const uint32_t cw = tmem + kSfw + (i & 1) * kSfCols;
-                    const uint32_t cx = tmem + kSfx + (i & 1) * kSfCols * kXTiles;
+                    const uint32_t cx = tmem + kSfx + (i & 1) * kSfCols;
                     const int kleft = a.K - (kb0 + i) * kA4Block;
                     const int steps = kleft >= kA4Block ? kA4Block / 64 : (kleft + 63) / 64;      // 64 elements an MMA
                     constexpr int kPer = fp4::tile_k(NV) / 64;                                    // MMAs per scale tile
                     // tcgen05.cp and tcgen05.mma of one thread run in order
-                    for (int j = 0; j < (steps + kPer - 1) / kPer; ++j) {
-                        tc::copy_scales(cw + 4 * j, sw + j * fp4::kTileBytes);
 #pragma unroll
-                        for (int r = 0; r < kXTiles; ++r)
-                            tc::copy_scales(cx + 4 * (j * kXTiles + r), sx + r * kSfBox + j * fp4::kTileBytes);
+                    for (int j = 0; j < kSfTiles; ++j) {
+                        if (j * kPer >= steps) break;
+                        tc::copy_scales(cw + 4 * j, sw + j * fp4::kTileBytes);
+                        tc::copy_scales(cx + 4 * j, sx + j * fp4::kTileBytes);
                     }
-                    for (int kk = 0; kk < steps; ++kk) {
+#pragma unroll
+                    for (int kk = 0; kk < kA4Block / 64; ++kk) {
+                        if (kk >= steps) break;
                         const int j = kk / kPer;
                         const uint32_t id = static_cast<uint32_t>(kk % kPer) * 2;                 // MX: byte pair 0 or 2
                         tc::mma_fp4<NV>(tmem, tc::sw128_desc(wa + kk * 32), tc::sw128_desc(xa + kk * 32),
-                                        kIdesc | (id << 4) | (id << 29), cw + 4 * j, cx + 4 * j * kXTiles,
+                                        kIdesc | (id << 4) | (id << 29), cw + 4 * j, cx + 4 * j,
                                         (i > 0 || kk > 0) ? 1u : 0u);
                     }
                     tc::commit(empty0 + 8 * s);
@@ -493,6 +555,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Epilogue warps 2..5 -> TMEM lane quarter (warp % 4).
         const int q = warp & 3;
         const int row = q * 32 + lane;
+        if constexpr (A4) {
+            if (!a.preq) {
+                // A warp takes one token's 256 elements of a K-block at a time, 8 a lane: the
+                // arithmetic of fp4_quant_kernel, codes into the swizzled rows that the MMA
+                // reads, scale words into the scale tile.  Rows M.. stay unset: an MMA column
+                // depends on its own row only, and theirs are not stored.
+                constexpr int kShare = fp4::block_len(NV) / 8, kWord = 4 * kShare, kU = 4;
+                const float g = a.gx ? *a.gx : 1.0f, g6 = __fmul_rn(6.0f, g);
+                const int items = nkb * a.M, step_i = 4 / a.M, step_t = 4 - step_i * a.M;
+                int gi = q / a.M, gt = q - gi * a.M;                 // (K-block, token) of the warp's next item
+#pragma unroll 1
+                for (int z0 = q; z0 < items; z0 += 4 * kU) {
+                    uint4 raw[kU];
+                    int ii[kU], tt[kU];
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        const int z = z0 + 4 * u;
+                        ii[u] = gi;
+                        tt[u] = gt;
+                        gi += step_i;
+                        gt += step_t;
+                        if (gt >= a.M) {
+                            gt -= a.M;
+                            ++gi;
+                        }
+                        const int k = (kb0 + ii[u]) * kA4Block + lane * 8;
+                        raw[u] = make_uint4(0, 0, 0, 0);
+                        if (z < items && k < a.K) raw[u] = ld_stream_after(a.x + static_cast<size_t>(tt[u]) * a.K + k);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        if (z0 + 4 * u >= items) break;
+                        uint32_t m = fp4::amax8(raw[u]);
+#pragma unroll
+                        for (int o = 1; o < kShare; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+                        const fp4::Scale bs = fp4::block_scale<NV>(m, g6, g);
+                        float v[8];
+                        fp4::unpack8(raw[u], v);
+                        uint8_t* blk = xq + static_cast<size_t>(ii[u]) * kXBlock;
+                        *reinterpret_cast<uint32_t*>(blk + tc::sw128_offset(tt[u], lane / 4) + (lane & 3) * 4) =
+                            fp4::encode8<NV>(v, bs);
+                        const bool in = (kb0 + ii[u]) * kA4Block + lane * 8 < a.K;      // scales past K are zero
+                        uint32_t w = in ? bs.byte << (8 * ((lane / kShare) & 3)) : 0u;
+#pragma unroll
+                        for (int o = kShare; o < kWord; o <<= 1) w |= __shfl_xor_sync(kFull, w, o);
+                        if (lane % kWord == 0)
+                            *reinterpret_cast<uint32_t*>(blk + kXBox + (lane / kWord) * fp4::kTileBytes +
+                                                         fp4::tile_offset(tt[u], 0)) = w;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(accf0);
+            }
+        }
         if constexpr (A8) {
             const int et = threadIdx.x - 64;
             if (a.preq) {
@@ -633,7 +750,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         // below is still reached by all 128 epilogue threads.
         const bool good = ok && !*abort_flag;
         if (!good && row == 0) set_status(a.ws, DG_DEVERR_WAIT_TIMEOUT);
-        if (!clustered) {
+        if (A4 && !clustered) {
+            // A lane holds one weight row, a warp 32 of them: 64 bytes of one token's output
+            // per store, straight from tensor memory.
+            const int n = tile * kTileRows + row;
+            if (good) {
+                constexpr int kC = MP < 32 ? 16 : 32;
+                uint16_t* dst = a.out + static_cast<size_t>(t0) * a.ld_out + n;
+#pragma unroll 1
+                for (int c = 0; c < rows_here; c += kC) {
+                    uint32_t v[kC];
+                    const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c);
+                    if constexpr (kC == 16)
+                        tc::tmem_ld16(at, v);
+                    else
+                        tc::tmem_ld32(at, v);
+                    const int left = n < a.N ? rows_here - c : 0;
+#pragma unroll
+                    for (int j = 0; j < kC; ++j) {
+                        if (j < left) *dst = f32_to_bf16_bits(__uint_as_float(v[j]) * alpha);
+                        dst += a.ld_out;
+                    }
+                }
+            }
+        } else if (!clustered) {
             // Stage the tile S[t][row] (fp32) in the now idle stage memory, then write
             // it out in coalesced 16-byte pieces (paired tiles: one after the other).
             float* S = reinterpret_cast<float*>(smem);
@@ -705,8 +845,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (good) {
             // Park this rank's partial tile P[t][row] (fp32) in the now idle stage memory.
             float* P = reinterpret_cast<float*>(smem);
-#pragma unroll 1
-            for (int c = 0; c < MP / 16; ++c) {
+#pragma unroll(A4 ? 2 : 1)
+            for (int c = 0; c < MP / 16 && (!A4 || c * 16 < rows_here); ++c) {
                 uint32_t v[16];
                 tc::tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c * 16, v);
 #pragma unroll
@@ -718,7 +858,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (clustered && !a.push) {
         cluster_wait();                      // (the arrival at the start)
         cluster_sync_all();                  // every rank's partial tile is in place
-        if (warp >= 2) {
+        if (A4 && warp >= 2) {
+            if (!*abort_flag) {
+                if (a.nsplit <= 4)
+                    fold_tokens<EPI, 4, 4>(a, tc::su32(smem), split, tile, t0, rows_here, warp - 2, lane);
+                else
+                    fold_tokens<EPI, 8, 2>(a, tc::su32(smem), split, tile, t0, rows_here, warp - 2, lane);
+            }
+        } else if (warp >= 2) {
             // This rank folds rows [lo, hi) (multiples of 4) for all tokens: P_0 + P_1 + ...
             // in rank order, four rows per thread, read through DSMEM.
             const int etid = threadIdx.x - 64;
@@ -853,7 +1000,6 @@ const void* tc_lookup_a4(int mp)
     case 32: return tc_fn<32, EPI>();
     case 64: return tc_fn<64, EPI>();
     case 128: return tc_fn<128, EPI>();
-    case 256: return tc_fn<256, EPI>();
     default: return nullptr;
     }
 }
@@ -1239,39 +1385,83 @@ dg_status launch_tc_a8(const DeviceInfo* dev, const dg_choice& c, const void* x,
 
 // ------------------------------------------------------------------ A4W4 blockscale
 
-int tc_a4_nsplit(const DeviceInfo* dev, int N, int K, int M, bool fixed)
+// How a call is cut: token groups of up to tg rows (the MMA's N) and ns K ranges.
+struct A4Plan {
+    int tg, ns;
+};
+
+// The cheapest cut by a model of what a CTA does, in units of 10 ns, measured on GB300 (graphs of
+// calls, 1 to 512 rows over 14 weight shapes; the cut it takes is within 0.4 % of the best one on
+// average, 4 % at worst): 33 a K-block of 256 elements, whatever the token group (issue and
+// scale copies, not bytes, set the pace); kEnd the epilogue of a group; with a K-split the
+// fold, kFold + kFoldRank per rank (partials through distributed shared memory at about 25
+// GB/s a CTA).  One wave: at most 264 of the 304 CTA slots -- fuller grids leave no room for
+// the next launch's CTAs to start under this one's tail (12288 x 4096 at 16 rows: 192 CTAs
+// 7.6 us, 288 9.8).  Few rows take few, small groups and a K-split; many rows split tokens
+// instead, and the tile's weights come from L2 to each group (128 x 4096 x 4096: one group of
+// 128 and 4 ranks 12.1 us, 4 groups of 32 and 2 ranks 9.6).
+static A4Plan a4_plan(const DeviceInfo* dev, int N, int K, int M, bool fixed)
 {
+    constexpr int kTg[4] = {16, 32, 64, 128};
+    constexpr int kEnd[4] = {0, 20, 180, 260}, kFold[4] = {80, 120, 160, 320}, kFoldRank[4] = {24, 17, 25, 23};
     const int tiles = (N + kTileRows - 1) / kTileRows;
     const int nkb = (K + kA4Block - 1) / kA4Block;
-    // Both CTA slots of every SM up to 128 tokens (a function of the shape alone, so a row's
-    // bits do not depend on how many rows share the call), one above; in one wave of
-    // clusters, and at least 2 K-blocks (512 elements) per rank.
-    const bool two = fixed || tc_mp(M) <= 128;
-    int ns = (two ? 2 : 1) * dev->sm_count / tiles;
-    if (ns > kMaxCluster) ns = kMaxCluster;
-    if (ns > nkb / 2) ns = nkb / 2;
-    while (ns > 1 && tiles > cluster_capacity(dev, two, ns)) --ns;
-    return ns < 1 ? 1 : ns;
+    const long long slots = 2 * dev->sm_count * 13 / 15;
+    // the fixed rule: the K ranges that one row would take
+    const int ns_fixed = fixed && M > 1 ? a4_plan(dev, N, K, 1, false).ns : 0;
+    A4Plan best{128, 1};
+    long long best_cost = -1;
+    for (int g = 0; g < 4; ++g) {
+        const int tg = kTg[g];
+        if ((tg == 16 && M > 16) || (tg > 16 && tg / 2 >= M)) continue;
+        for (int ns = 1; ns <= kMaxCluster && ns <= nkb; ++ns) {
+            if (ns_fixed && ns != ns_fixed) continue;
+            const long long ctas = static_cast<long long>(tiles) * ((M + tg - 1) / tg) * ns;
+            if (ns > 1 && !ns_fixed && (ctas > slots || ctas / ns > cluster_capacity(dev, true, ns))) continue;
+            const long long waves = (ctas + slots - 1) / slots;
+            const long long cost = waves * 33 * ((nkb + ns - 1) / ns) + kEnd[g] + (ns > 1 ? kFold[g] + kFoldRank[g] * ns : 0);
+            if (best_cost < 0 || cost < best_cost) {
+                best_cost = cost;
+                best = A4Plan{tg, ns};
+            }
+        }
+    }
+    return best;
 }
 
 size_t a4_workspace_bytes(int M, int K)
 {
     const size_t q = (static_cast<size_t>(M) * K / 2 + 255) / 256 * 256;
-    // the wider of the two formats' scales
-    return kWsData + q + fp4::scale_bytes(M, K, true);
+    // the wider of the two formats' scales, a tile row for each 32 tokens (the smallest group)
+    return kWsData + q +
+           static_cast<size_t>((M + 31) / 32) * fp4::scale_tiles(K, true) * fp4::kTileBytes;
 }
 
 namespace {
 
-size_t stage_bytes_a4(int mp, bool nv)
+// One K-block of activations: codes and scale tiles.
+size_t xblock_bytes_a4(int mp, bool nv)
 {
-    return kWBox + static_cast<size_t>(mp) * 128 + static_cast<size_t>(a4_scale_box(nv)) * (mp > 128 ? 3 : 2);
+    return static_cast<size_t>(mp) * 128 + static_cast<size_t>(a4_scale_box(nv));
 }
 
-size_t smem_bytes_a4(int mp, bool nv, int stages, size_t recv)
+// xq_blocks: K-blocks of activations kept beside the ring (0: they come with each stage).
+size_t stage_bytes_a4(int mp, bool nv, int xq_blocks)
 {
-    return 1024 + stages * stage_bytes_a4(mp, nv) + (2 * stages + 2) * 8 + 16 + recv;
+    return kWBox + static_cast<size_t>(a4_scale_box(nv)) + (xq_blocks ? 0 : xblock_bytes_a4(mp, nv));
 }
+
+size_t smem_bytes_a4(int mp, bool nv, int stages, size_t recv, int xq_blocks)
+{
+    return 1024 + stages * stage_bytes_a4(mp, nv, xq_blocks) + xq_blocks * xblock_bytes_a4(mp, nv) +
+           (2 * stages + 2 + kA4Bars) * 8 + 16 + recv;
+}
+
+// The linear's own CTAs quantise the activations where a rank has at most this many
+// (row, K-block) pieces: every row tile repeats the work, about 0.14 us a piece and warp, against
+// a launch of its own (4096 x 4096, us fused / apart: 1 row 5.1 / 6.1, 4 rows 6.2 / 6.2, 8 rows
+// 8.1 / 6.6; 12288 x 4096, twice the K-blocks a rank: 4 rows 9.7 / 8.1).
+constexpr int kA4FusePieces = 16;
 
 }  // namespace
 
@@ -1284,85 +1474,86 @@ dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const
     for (int i = 2; i < 6; ++i)
         if (c.params[i] != 0) return DG_ERR_BAD_VARIANT;
     if (ws_bytes < a4_workspace_bytes(M, K)) return DG_ERR_WORKSPACE_TOO_SMALL;
-    const bool fixed = c.params[1] == 1;
-    const int chunk = fixed ? 128 : 256;                 // token rows per launch
+    const A4Plan plan = a4_plan(dev, N, K, M, c.params[1] == 1);
+    const int mp = plan.tg, ns = plan.ns, groups = (M + mp - 1) / mp;
+    const void* fn = nv ? tc_lookup_a4<4>(mp) : tc_lookup_a4<3>(mp);
+    if (!fn) return DG_ERR_BAD_VARIANT;
+    const int nkb = (K + kA4Block - 1) / kA4Block;
+    const bool fuse = static_cast<long long>(M) * ((nkb + ns - 1) / ns) <= kA4FusePieces;
+    const int mq = (M + 3) & ~3;
+    const int xq = fuse ? (nkb + ns - 1) / ns : 0;
+    const size_t recv = mq <= kPushMaxTokens ? recv_bytes(ns, mq) : 0;
+    int stages = c.params[0];
+    if (stages == 0) {
+        stages = 5;
+        while (stages > 2 && smem_bytes_a4(mp, nv, stages, recv, xq) > kCoResidentSmem) --stages;
+    }
+    if (stages < 2 || stages > 8) return DG_ERR_BAD_VARIANT;
+    // A K-split parks its partial tile in the ring.
+    if (ns > 1 && !recv && stages * stage_bytes_a4(mp, nv, xq) < static_cast<size_t>(mp) * kTileRows * 4)
+        return DG_ERR_BAD_VARIANT;
+    size_t smem = smem_bytes_a4(mp, nv, stages, recv, xq);
+    if (smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
+    // Never more co-resident CTAs than their TMEM columns fit in the SM's 512.
+    const size_t cols = mp <= 64 ? 128 : 256;
+    const size_t min_smem = 228 * 1024 / (512 / cols + 1) + 1024;
+    if (smem < min_smem) smem = min_smem;
+    if (occupancy(fn, kThreads, smem) < 1) return DG_ERR_UNSUPPORTED_SHAPE;
     uint8_t* qws = static_cast<uint8_t*>(ws) + kWsData;
     uint8_t* sws = qws + (static_cast<size_t>(M) * K / 2 + 255) / 256 * 256;
-    // Every launch is checked before the first is queued.
-    for (int pass = 0; pass < 2; ++pass) {
-        if (pass == 1) {
-            const dg_status st = launch_fp4_quant(nv, x, qws, sws, gx, M, K, true, stream);
-            if (st != DG_OK) return st;
-        }
-        for (int t0 = 0; t0 < M; t0 += chunk) {
-            const int mc = M - t0 < chunk ? M - t0 : chunk;
-            const int mp = tc_mp(mc);
-            const void* fn = nv ? tc_lookup_a4<4>(mp) : tc_lookup_a4<3>(mp);
-            if (!fn) return DG_ERR_BAD_VARIANT;
-            const int ns = tc_a4_nsplit(dev, N, K, mc, fixed);
-            const int mq = (mc + 3) & ~3;
-            size_t recv = mq <= kPushMaxTokens ? recv_bytes(ns, mq) : 0;
-            int stages = c.params[0];
-            if (stages == 0) {
-                stages = mp <= 128 ? 5 : 3;
-                while (stages > 2 && smem_bytes_a4(mp, nv, stages, recv) > (mp <= 128 ? kCoResidentSmem : kMaxDynSmem))
-                    --stages;
-            }
-            if (stages < 2 || stages > 8) return DG_ERR_BAD_VARIANT;
-            // The epilogue stages the tile (or parks the K-split partial) in the ring.
-            if (stages * stage_bytes_a4(mp, nv) < static_cast<size_t>(mp) * kTileRows * 4) return DG_ERR_BAD_VARIANT;
-            size_t smem = smem_bytes_a4(mp, nv, stages, recv);
-            if (smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
-            // Never more co-resident CTAs than their TMEM columns fit in the SM's 512.
-            const size_t cols = mp <= 16 ? 128 : (mp <= 128 ? 256 : 512);
-            const size_t min_smem = 228 * 1024 / (512 / cols + 1) + 1024;
-            if (smem < min_smem) smem = min_smem;
-            if (occupancy(fn, kThreads, smem) < 1) return DG_ERR_UNSUPPORTED_SHAPE;
-            TcArgs a{};
-            a.N = N;
-            a.K = K;
-            a.M = mc;
-            a.tiles = (N + kTileRows - 1) / kTileRows;
-            a.nkb = (K + kA4Block - 1) / kA4Block;
-            a.nsplit = ns;
-            a.push = recv > 0 ? 1 : 0;
-            a.mq = mq;
-            a.slice_max = slice_max(ns);
-            a.stages = stages;
-            a.out = static_cast<uint16_t*>(y) + static_cast<size_t>(t0) * N;
-            a.ld_out = N;
-            a.ws = static_cast<uint8_t*>(ws);
-            a.nkt = fp4::scale_tiles(K, nv);
-            a.sfw = static_cast<const uint8_t*>(sw);
-            a.sfx = sws + static_cast<size_t>(t0 / fp4::kTileRows) * a.nkt * fp4::kTileBytes;
-            a.gx = gx;
-            a.gw = gw;
-            CUtensorMap tmW, tmX;
-            const uint64_t kb = static_cast<uint64_t>(K) / 2;
-            if (!encode_2d(&tmW, Wq, kb, static_cast<uint64_t>(N), 128, kTileRows, true) ||
-                !encode_2d(&tmX, qws + t0 * kb, kb, static_cast<uint64_t>(mc), 128, static_cast<uint32_t>(mp), true))
-                return DG_ERR_CUDA;
-            if (pass == 0) continue;
-            void* args[] = {&tmW, &tmX, &a};
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(static_cast<unsigned>(a.tiles * a.nsplit));
-            cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = smem;
-            cfg.stream = stream;
-            cudaLaunchAttribute attr[2];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = static_cast<unsigned>(a.nsplit);
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-            cfg.attrs = attr;
-            cfg.numAttrs = 2;
-            if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
-                cudaGetLastError();
-                return DG_ERR_CUDA;
-            }
-        }
+    TcArgs a{};
+    a.N = N;
+    a.K = K;
+    a.M = M;
+    a.tiles = (N + kTileRows - 1) / kTileRows;
+    a.nkb = nkb;
+    a.nsplit = ns;
+    a.push = recv > 0 ? 1 : 0;
+    a.mq = mq;
+    a.slice_max = slice_max(ns);
+    a.stages = stages;
+    a.out = static_cast<uint16_t*>(y);
+    a.ld_out = N;
+    a.ws = static_cast<uint8_t*>(ws);
+    a.x = static_cast<const uint16_t*>(x);
+    a.preq = fuse ? 0 : 1;
+    a.xq_blocks = xq;
+    a.nkt = fp4::scale_tiles(K, nv);
+    a.sfw = static_cast<const uint8_t*>(sw);
+    a.sfx = sws;
+    a.groups = groups;
+    a.tg = mp;
+    a.gx = gx;
+    a.gw = gw;
+    CUtensorMap tmW, tmX;
+    const uint64_t kb = static_cast<uint64_t>(K) / 2;
+    if (!encode_2d(&tmW, Wq, kb, static_cast<uint64_t>(N), 128, kTileRows, true)) return DG_ERR_CUDA;
+    if (fuse)
+        tmX = tmW;                                   // (not read)
+    else if (!encode_2d(&tmX, qws, kb, static_cast<uint64_t>(M), 128, static_cast<uint32_t>(mp), true))
+        return DG_ERR_CUDA;
+    if (!fuse) {
+        const dg_status st = launch_fp4_quant(nv, x, qws, sws, gx, M, K, mp < fp4::kTileRows ? mp : fp4::kTileRows, true, stream);
+        if (st != DG_OK) return st;
+    }
+    void* args[] = {&tmW, &tmX, &a};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.tiles * groups * ns));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ns);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+        cudaGetLastError();
+        return DG_ERR_CUDA;
     }
     return DG_OK;
 }

@@ -385,9 +385,9 @@ dg_status dg_dequant_fp4_blockscale(const void* q, const void* s, const float* g
  * gx, gw: device pointers to the tensor scales of the activations (calibrated ahead) and of
  * the weights (NULL: 1; both NULL with DG_FP4_MX), y [M, N] bf16.
  * 1 <= M <= 512, K % 32 == 0.  Tensor cores only (DG_VAR_TC; params[0] pipeline stages,
- * params[1] the K-split rule).  Up to 128 rows the K-split is fixed by (N, K) on a given
- * device, so output row m depends on input row m alone; with DG_NUMERICS_BATCH_INVARIANT (or
- * params[1] = 1) at every M.  Non-finite activations give NaN outputs for their token.  ws:
+ * params[1] the K-split rule: 0 by the shape and the row count, 1 by the shape alone, which
+ * the batch-invariant mode takes: output row m is then a function of input row m at every
+ * M).  Non-finite activations give NaN outputs for their token.  ws:
  * the status word, and the codes and scales of the activations. */
 dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw, const float* gx, const float* gw,
                                   void* y, int M, int N, int K, int fmt, void* ws, size_t ws_bytes,
