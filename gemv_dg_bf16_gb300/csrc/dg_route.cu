@@ -1,11 +1,19 @@
 // dg_route.cu -- routing of tokens to experts (dg_moe_route).
 //
-// One warp per token; lane l holds experts j * 32 + l in registers.  The pick compares
-// scores (plus the bias) in binary32, so that it is defined to the last bit: sigmoid as
-// 1 / (1 + expf(-x)), softmax as expf(x - max) / sum with the sum compensated
-// (Knuth's two-sum), which rounds it as the exact sum in all but about 2^-20 of cases
-// whatever the order -- the same pick for any arrangement of lanes.
-// Bound: latency of topk dependent warp reductions; memory (2 or 4 bytes a logit) is small.
+// One warp per token at a time; lane l holds the R consecutive experts l R .. l R + R - 1 in
+// registers, so a lower lane is a lower index and a group of experts is a run of lanes.  The
+// pick compares scores (plus the bias) in binary32, so that it is defined to the last bit:
+// sigmoid as 1 / (1 + expf(-x)), softmax as expf(x - max) / sum with the sum compensated
+// (Knuth's two-sum), which rounds it as the exact sum in all but about 2^-20 of cases whatever
+// the order -- the same pick for any arrangement of lanes.
+//
+// Up to 8 experts a lane, each lane sorts its own (a network, stable), and a pick is one warp
+// maximum over the lanes' heads, a ballot for the lowest lane that holds it, and a shift in
+// that lane.  A group's best one or two are the heads of its lanes, merged by shuffles.  Warps
+// walk over the tokens with the next token's logits already on the way and the bias in
+// registers.  Bound: instructions, about 500 a token of 256 experts (the scores' exponentials
+// and divisions a third of them); memory is 1 KB a token.  32768 x 256, 8 groups, 8 picks:
+// one expert in 32 to a lane, group by group, 74 us.
 #include "dg_common.cuh"
 #include "dg_internal.h"
 
@@ -14,13 +22,19 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// Total order of floats as unsigned (no NaN, no -0 among scores); -inf is kNone.
-__device__ __forceinline__ uint32_t order_key(float f)
-{
-    const uint32_t b = __float_as_uint(f);
-    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-}
-constexpr uint32_t kNone = 0x007fffffu;
+struct RouteArgs {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* w;
+    long long ld;
+    int M, E;
+    int topk, n_group, topk_group, group_top, gsize;
+    int group_lanes;       // lanes of a group where groups are aligned runs of 2^k lanes, else 0
+    int vec;               // rows start on 16-byte boundaries
+    int sigmoid, renorm;
+    float scale;
+};
 
 // s + e += v, exactly up to the rounding of e.
 __device__ __forceinline__ void two_sum(float& s, float& e, float v)
@@ -31,150 +45,260 @@ __device__ __forceinline__ void two_sum(float& s, float& e, float v)
     s = t;
 }
 
-struct RouteArgs {
-    const void* logits;
-    const float* bias;
-    int32_t* ids;
-    float* w;
-    long long ld;
-    int M, E;
-    int topk, n_group, topk_group, group_top, gsize;
-    int sigmoid, renorm;
-    float scale;
-};
+__device__ __forceinline__ float warp_max(float v)
+{
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
 
 template <bool F32>
-__device__ __forceinline__ float load_logit(const RouteArgs& a, long long row, int i)
+__device__ __forceinline__ float logit(const RouteArgs& a, long long row, int i)
 {
     const long long o = row * a.ld + i;
     if constexpr (F32) return static_cast<const float*>(a.logits)[o];
     return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(a.logits)[o]) << 16);
 }
 
+// The lane's R logits; experts past E and NaN as -inf (not available).
+template <int R, bool F32>
+__device__ __forceinline__ void load_row(const RouteArgs& a, long long row, int lane, float (&x)[R])
+{
+    const int i0 = lane * R;
+    constexpr int kVec = F32 ? 4 : 8;
+    if constexpr (R % kVec == 0) {
+        if (a.vec && i0 + R <= a.E) {
+            const uint8_t* p = static_cast<const uint8_t*>(a.logits) + (row * a.ld + i0) * (F32 ? 4 : 2);
+#pragma unroll
+            for (int j = 0; j < R; j += kVec) {
+                const uint4 v = *reinterpret_cast<const uint4*>(p + j * (F32 ? 4 : 2));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    if constexpr (F32) {
+                        x[j + h] = __uint_as_float(w[h]);
+                    } else {
+                        x[j + 2 * h] = bf16_lo(w[h]);
+                        x[j + 2 * h + 1] = bf16_hi(w[h]);
+                    }
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) x[j] = i0 + j < a.E ? logit<F32>(a, row, i0 + j) : -INFINITY;
+}
+
+// Descending, stable: `ord` holds the place that each value came from, four bits a value.
+template <int R>
+__device__ __forceinline__ void sort_keys(float (&k)[R], uint32_t& ord)
+{
+    uint32_t at[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) at[j] = j;
+    // Batcher's odd-even merge sort; equal keys compare by their place.
+#pragma unroll
+    for (int p = 1; p < R; p <<= 1)
+#pragma unroll
+        for (int q = p; q > 0; q >>= 1)
+#pragma unroll
+            for (int j = q % p; j + q < R; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < R && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const int lo = i + j, hi = i + j + q;
+                        const bool swap = k[hi] > k[lo] || (k[hi] == k[lo] && at[hi] < at[lo]);
+                        const float f = swap ? k[hi] : k[lo];
+                        k[hi] = swap ? k[lo] : k[hi];
+                        k[lo] = f;
+                        const uint32_t t = swap ? at[hi] : at[lo];
+                        at[hi] = swap ? at[lo] : at[hi];
+                        at[lo] = t;
+                    }
+    ord = 0;
+#pragma unroll
+    for (int j = 0; j < R; ++j) ord |= at[j] << (4 * j);
+}
+
 template <int R, bool F32>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
 {
+    constexpr bool kSorted = R <= 8;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const long long step = static_cast<long long>(gridDim.x) * kWarps;
+    long long row = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (row >= a.M) return;
-    float x[R];
-    uint32_t key[R];
+    float bias[R];
+    if (a.bias)
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-        const int i = j * 32 + lane;
-        x[j] = i < a.E ? load_logit<F32>(a, row, i) : -INFINITY;
-        if (!(x[j] > -INFINITY)) x[j] = -INFINITY;                 // NaN: not available
-    }
-    float m = 0.0f, sum = 1.0f;
-    if (!a.sigmoid) {
-        float lm = x[0];
+        for (int j = 0; j < R; ++j) bias[j] = lane * R + j < a.E ? a.bias[lane * R + j] : 0.0f;
+    float next[R];
+    load_row<R, F32>(a, row, lane, next);
+    for (; row < a.M; row += step) {
+        float key[R];                                              // logits, then keys
 #pragma unroll
-        for (int j = 1; j < R; ++j) lm = fmaxf(lm, x[j]);
+        for (int j = 0; j < R; ++j) key[j] = next[j] > -INFINITY ? next[j] : -INFINITY;
+        if (row + step < a.M) load_row<R, F32>(a, row + step, lane, next);
+        float m = 0.0f, sum = 1.0f;
+        if (!a.sigmoid) {
+            float lm = key[0];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) lm = fmaxf(lm, __shfl_xor_sync(kFull, lm, o));
-        m = lm;
-        float s = 0.0f, e = 0.0f;
+            for (int j = 1; j < R; ++j) lm = fmaxf(lm, key[j]);
+            m = warp_max(lm);
+            float s = 0.0f, e = 0.0f;
+#pragma unroll
+            for (int j = 0; j < R; ++j)
+                if (key[j] > -INFINITY) {
+                    key[j] = key[j] == m ? 1.0f : expf(key[j] - m);        // (the exponential; a score below)
+                    two_sum(s, e, key[j]);
+                }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                const float s2 = __shfl_xor_sync(kFull, s, o), e2 = __shfl_xor_sync(kFull, e, o);
+                two_sum(s, e, s2);
+                e = __fadd_rn(e, e2);
+            }
+            sum = __fadd_rn(s, e);
+        }
+        auto score = [&](float v) {
+            if (a.sigmoid) return __frcp_rn(__fadd_rn(1.0f, expf(-v)));
+            return __fdiv_rn(v == m ? 1.0f : expf(v - m), sum);
+        };
 #pragma unroll
         for (int j = 0; j < R; ++j)
-            if (x[j] > -INFINITY) two_sum(s, e, x[j] == m ? 1.0f : expf(x[j] - m));
+            if (key[j] > -INFINITY) {
+                float k = a.sigmoid ? __frcp_rn(__fadd_rn(1.0f, expf(-key[j]))) : __fdiv_rn(key[j], sum);
+                if (a.bias) k = __fadd_rn(k, bias[j]);
+                key[j] = k > -INFINITY ? k : -INFINITY;
+            }
+        uint32_t ord = 0;
+        if constexpr (kSorted) sort_keys<R>(key, ord);
+
+        if (a.n_group > 1) {
+            float gs = -INFINITY;
+            if (kSorted && a.group_lanes) {
+                // The best two of the lane are its heads; merged over the group's lanes.
+                float b1 = key[0], b2 = R > 1 ? key[R > 1 ? 1 : 0] : -INFINITY;
+                for (int o = 1; o < a.group_lanes; o <<= 1) {
+                    const float c1 = __shfl_xor_sync(kFull, b1, o), c2 = __shfl_xor_sync(kFull, b2, o);
+                    b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
+                    b1 = fmaxf(b1, c1);
+                }
+                gs = a.group_top == 2 && b2 > -INFINITY ? __fadd_rn(b1, b2) : b1;
+                const int own = lane / a.group_lanes;
+                int rank = 0;
+                for (int g = 0; g < a.n_group; ++g) {
+                    const float o = __shfl_sync(kFull, gs, g * a.group_lanes);
+                    rank += (o > gs || (o == gs && g < own)) ? 1 : 0;
+                }
+                if (rank >= a.topk_group)
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const float s2 = __shfl_xor_sync(kFull, s, o), e2 = __shfl_xor_sync(kFull, e, o);
-            two_sum(s, e, s2);
-            e = __fadd_rn(e, e2);
-        }
-        sum = __fadd_rn(s, e);
-    }
-    auto score = [&](float v) {
-        if (a.sigmoid) return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-v)));
-        return __fdiv_rn(v == m ? 1.0f : expf(v - m), sum);
-    };
+                    for (int j = 0; j < R; ++j) key[j] = -INFINITY;
+            } else {
+                // Groups that cut across lanes: one after the other, lane g keeping the score of g.
+                for (int g = 0; g < a.n_group; ++g) {
+                    float b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-        const int i = j * 32 + lane;
-        key[j] = kNone;
-        if (x[j] > -INFINITY) {
-            float k = score(x[j]);
-            if (a.bias) k = __fadd_rn(k, a.bias[i]);
-            if (k > -INFINITY) key[j] = order_key(k);
-        }
-    }
-    if (a.n_group > 1) {
-        float gs = -INFINITY;                                      // lane g: the score of group g
-        for (int g = 0; g < a.n_group; ++g) {
-            uint32_t a1 = kNone, a2 = kNone;
+                    for (int j = 0; j < R; ++j) {
+                        const int i = lane * R + (kSorted ? static_cast<int>((ord >> (4 * (j & 7))) & 15u) : j);
+                        if (i >= g * a.gsize && i < (g + 1) * a.gsize) {
+                            b2 = fmaxf(b2, fminf(b1, key[j]));
+                            b1 = fmaxf(b1, key[j]);
+                        }
+                    }
+                    const float t1 = warp_max(b1);
+                    const unsigned who = __ballot_sync(kFull, b1 == t1);
+                    const float t2 = warp_max(lane == __ffs(who) - 1 ? b2 : b1);
+                    if (lane == g) gs = a.group_top == 2 && t2 > -INFINITY ? __fadd_rn(t1, t2) : t1;
+                }
+                int rank = 0;
+                for (int g = 0; g < a.n_group; ++g) {
+                    const float o = __shfl_sync(kFull, gs, g);
+                    rank += (o > gs || (o == gs && g < lane)) ? 1 : 0;
+                }
+                const unsigned keep = __ballot_sync(kFull, lane < a.n_group && rank < a.topk_group);
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                const int i = j * 32 + lane;
-                if (i >= g * a.gsize && i < (g + 1) * a.gsize) {
-                    a2 = max(a2, min(a1, key[j]));
-                    a1 = max(a1, key[j]);
+                for (int j = 0; j < R; ++j) {
+                    const int i = lane * R + (kSorted ? static_cast<int>((ord >> (4 * (j & 7))) & 15u) : j);
+                    if (i < a.E && !((keep >> (i / a.gsize)) & 1u)) key[j] = -INFINITY;
+                }
+                // (a lane's heads may be gone: sorted again, places kept)
+                if constexpr (kSorted) {
+                    uint32_t o2;
+                    const uint32_t o1 = ord;
+                    sort_keys<R>(key, o2);
+                    ord = 0;
+#pragma unroll
+                    for (int j = 0; j < R; ++j)
+                        ord |= ((o1 >> (4 * ((o2 >> (4 * j)) & 15u))) & 15u) << (4 * j);
                 }
             }
-            const uint32_t t1 = __reduce_max_sync(kFull, a1);
-            const unsigned own = __ballot_sync(kFull, a1 == t1);
-            const uint32_t t2 = __reduce_max_sync(kFull, lane == __ffs(own) - 1 ? a2 : a1);
-            const float f1 = __uint_as_float((t1 & 0x80000000u) ? t1 ^ 0x80000000u : ~t1);
-            const float f2 = __uint_as_float((t2 & 0x80000000u) ? t2 ^ 0x80000000u : ~t2);
-            const float v = t1 == kNone ? -INFINITY : (a.group_top == 2 && t2 != kNone ? __fadd_rn(f1, f2) : f1);
-            if (lane == g) gs = v;
         }
-        int rank = 0;
-        for (int g = 0; g < a.n_group; ++g) {
-            const float o = __shfl_sync(kFull, gs, g);
-            rank += (o > gs || (o == gs && g < lane)) ? 1 : 0;
-        }
-        const unsigned keep = __ballot_sync(kFull, lane < a.n_group && rank < a.topk_group);
+
+        int id = -1;                                               // lane k: slot k
+        float wv = 0.0f;
+        for (int k = 0; k < a.topk; ++k) {
+            float best = key[0];
+            int at = 0;
+            if constexpr (kSorted) {
+                at = static_cast<int>(ord & 15u);
+            } else {
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const int i = j * 32 + lane;
-            if (i < a.E && !((keep >> (i / a.gsize)) & 1u)) key[j] = kNone;
-        }
-    }
-    int id = -1;                                                   // lane k: slot k
-    for (int k = 0; k < a.topk; ++k) {
-        uint32_t best = kNone;
-        int at = 0x7fffffff;
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-            if (key[j] > best) {
-                best = key[j];
-                at = j * 32 + lane;
+                for (int j = 1; j < R; ++j)
+                    if (key[j] > best) {
+                        best = key[j];
+                        at = j;
+                    }
             }
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        if (top == kNone) break;
-        const int win = static_cast<int>(__reduce_min_sync(kFull, best == top ? static_cast<unsigned>(at) : 0x7fffffffu));
-        if (lane == k) id = win;
+            const float top = warp_max(best);
+            if (!(top > -INFINITY)) break;
+            const int src = __ffs(__ballot_sync(kFull, best == top)) - 1;
+            const int win = __shfl_sync(kFull, lane * R + at, src);
+            if (lane == k) {
+                id = win;
+                wv = top;
+            }
+            if (lane == src) {
+                if constexpr (kSorted) {
 #pragma unroll
-        for (int j = 0; j < R; ++j)
-            if (j * 32 + lane == win) key[j] = kNone;
-    }
-    float wv = 0.0f;
-    if (id >= 0) wv = score(load_logit<F32>(a, row, id));
-    if (a.renorm) {
-        float t = wv;
+                    for (int j = 0; j + 1 < R; ++j) key[j] = key[j + 1];
+                    key[R - 1] = -INFINITY;
+                    ord >>= 4;
+                } else {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
-        wv = t > 0.0f ? __fdiv_rn(wv, t) : 0.0f;
-    }
-    if (lane < a.topk) {
-        a.ids[row * a.topk + lane] = id;
-        a.w[row * a.topk + lane] = __fmul_rn(wv, a.scale);
+                    for (int j = 0; j < R; ++j)
+                        if (j == at) key[j] = -INFINITY;
+                }
+            }
+        }
+        if (a.bias && id >= 0) wv = score(logit<F32>(a, row, id));  // without the bias
+        if (a.renorm) {
+            float t = wv;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
+            wv = t > 0.0f ? __fdiv_rn(wv, t) : 0.0f;
+        }
+        if (lane < a.topk) {
+            a.ids[row * a.topk + lane] = id;
+            a.w[row * a.topk + lane] = __fmul_rn(wv, a.scale);
+        }
     }
 }
 
 template <bool F32>
-const void* route_fn(int E)
+const void* route_fn(int r)
 {
-    const int r = (E + 31) / 32;
-    if (r <= 1) return reinterpret_cast<const void*>(&route_kernel<1, F32>);
-    if (r <= 2) return reinterpret_cast<const void*>(&route_kernel<2, F32>);
-    if (r <= 4) return reinterpret_cast<const void*>(&route_kernel<4, F32>);
-    if (r <= 8) return reinterpret_cast<const void*>(&route_kernel<8, F32>);
-    if (r <= 16) return reinterpret_cast<const void*>(&route_kernel<16, F32>);
-    return reinterpret_cast<const void*>(&route_kernel<32, F32>);
+    switch (r) {
+    case 1: return reinterpret_cast<const void*>(&route_kernel<1, F32>);
+    case 2: return reinterpret_cast<const void*>(&route_kernel<2, F32>);
+    case 4: return reinterpret_cast<const void*>(&route_kernel<4, F32>);
+    case 8: return reinterpret_cast<const void*>(&route_kernel<8, F32>);
+    case 16: return reinterpret_cast<const void*>(&route_kernel<16, F32>);
+    default: return reinterpret_cast<const void*>(&route_kernel<32, F32>);
+    }
 }
 
 }  // namespace
@@ -182,6 +306,9 @@ const void* route_fn(int E)
 dg_status launch_route(const dg_route_params& p, const void* logits, const float* bias, int32_t* ids, float* w,
                        int M, int E, long long ld, bool f32, cudaStream_t stream)
 {
+    dg_status st;
+    const DeviceInfo* dev = current_device(&st);
+    if (!dev) return st;
     RouteArgs a{};
     a.logits = logits;
     a.bias = bias;
@@ -198,10 +325,19 @@ dg_status launch_route(const dg_route_params& p, const void* logits, const float
     a.sigmoid = p.score == DG_SCORE_SIGMOID ? 1 : 0;
     a.renorm = p.renorm;
     a.scale = p.scale;
-    const void* fn = f32 ? route_fn<true>(E) : route_fn<false>(E);
+    const int r = cpow2((E + 31) / 32);
+    const int gl = a.gsize % r == 0 ? a.gsize / r : 0;
+    a.group_lanes = gl > 0 && (gl & (gl - 1)) == 0 ? gl : 0;
+    a.vec = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && (ld * (f32 ? 4 : 2)) % 16 == 0 ? 1 : 0;
+    const void* fn = f32 ? route_fn<true>(r) : route_fn<false>(r);
+    const int occ = occupancy(fn, kWarps * 32, 0);
+    if (occ < 1) return DG_ERR_CUDA;
+    // One token a warp, until every warp slot has some: then they walk.
+    long long grid = (static_cast<long long>(M) + kWarps - 1) / kWarps;
+    const long long most = static_cast<long long>(dev->sm_count) * occ;
+    if (grid > most) grid = most;
     void* args[] = {&a};
-    const unsigned grid = static_cast<unsigned>((static_cast<long long>(M) + kWarps - 1) / kWarps);
-    if (launch_kernel(fn, grid, kWarps * 32, 0, stream, args) != cudaSuccess) {
+    if (launch_kernel(fn, static_cast<unsigned>(grid), kWarps * 32, 0, stream, args) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
     }
