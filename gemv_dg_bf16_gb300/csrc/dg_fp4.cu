@@ -21,13 +21,17 @@ constexpr int kRowCtas = kStep / kWarps;   // CTAs over a scale tile's 128 rows
 static_assert(kRows * kStep == fp4::kTileRows && kStep % kWarps == 0, "a warp's rows are one 16-byte piece");
 
 // The outputs may be weights, which a linear of this library reads before it waits for the
-// launches ahead of it: let the next launch begin only when this thread's stores are
-// visible to the whole device, to plain loads and to bulk copies.
+// launches ahead of it: let the next launch begin only when the CTA's stores are visible to
+// the whole device, to plain loads and to bulk copies (one fence a CTA, behind its barrier:
+// one a thread stalled the warps for a third of their time).
 __device__ __forceinline__ void signal_written()
 {
-    __threadfence();
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-    pdl_launch_dependents();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        pdl_launch_dependents();
+    }
 }
 
 // Where a warp works: its first row, its 16-byte piece in scale tile kt of that tile row.

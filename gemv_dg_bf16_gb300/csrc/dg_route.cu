@@ -7,9 +7,9 @@
 // (Knuth's two-sum), which rounds it as the exact sum in all but about 2^-20 of cases whatever
 // the order -- the same pick for any arrangement of lanes.
 //
-// Up to 8 experts a lane, each lane sorts its own (a network, stable), and a pick is one warp
-// maximum over the lanes' heads, a ballot for the lowest lane that holds it, and a shift in
-// that lane.  A group's best one or two are the heads of its lanes, merged by shuffles.  Warps
+// Up to 8 experts a lane, each lane sorts its keys (a network of maxima and minima), and a pick
+// is one warp maximum over the lanes' heads, a ballot for the lowest lane that holds it, and a
+// shift in that lane; which expert each pick was is looked up at the end for all slots at once.  A group's best one or two are the heads of its lanes, merged by shuffles.  Warps
 // walk over the tokens with the next token's logits already on the way and the bias in
 // registers.  Bound: instructions, about 500 a token of 256 experts (the scores' exponentials
 // and divisions a third of them); memory is 1 KB a token.  32768 x 256, 8 groups, 8 picks:
@@ -30,7 +30,7 @@ struct RouteArgs {
     long long ld;
     int M, E;
     int topk, n_group, topk_group, group_top, gsize;
-    int group_lanes;       // lanes of a group where groups are aligned runs of 2^k lanes, else 0
+    int group_shift;       // k where groups are aligned runs of 2^k lanes, else -1
     int vec;               // rows start on 16-byte boundaries
     int sigmoid, renorm;
     float scale;
@@ -50,6 +50,17 @@ __device__ __forceinline__ float warp_max(float v)
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
+}
+
+// 1 / y, correctly rounded, for 1 <= y < 2^125: one Newton step in fused operations on a
+// reciprocal within an ulp (P. W. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990).  Equal to __frcp_rn(y) for every mantissa, at exponents
+// 0, 1, 3, 23, 73, 113, 124 and 125.
+__device__ __forceinline__ float recip_rn(float y)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+    return __fmaf_rn(r, __fmaf_rn(-y, r, 1.0f), r);
 }
 
 template <bool F32>
@@ -90,14 +101,10 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, long long row, int 
     for (int j = 0; j < R; ++j) x[j] = i0 + j < a.E ? logit<F32>(a, row, i0 + j) : -INFINITY;
 }
 
-// Descending, stable: `ord` holds the place that each value came from, four bits a value.
+// Descending, values alone (Batcher's odd-even merge sort, two instructions a comparison).
 template <int R>
-__device__ __forceinline__ void sort_keys(float (&k)[R], uint32_t& ord)
+__device__ __forceinline__ void sort_keys(float (&k)[R])
 {
-    uint32_t at[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j) at[j] = j;
-    // Batcher's odd-even merge sort; equal keys compare by their place.
 #pragma unroll
     for (int p = 1; p < R; p <<= 1)
 #pragma unroll
@@ -107,18 +114,10 @@ __device__ __forceinline__ void sort_keys(float (&k)[R], uint32_t& ord)
 #pragma unroll
                 for (int i = 0; i < q; ++i)
                     if (i + j + q < R && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-                        const int lo = i + j, hi = i + j + q;
-                        const bool swap = k[hi] > k[lo] || (k[hi] == k[lo] && at[hi] < at[lo]);
-                        const float f = swap ? k[hi] : k[lo];
-                        k[hi] = swap ? k[lo] : k[hi];
-                        k[lo] = f;
-                        const uint32_t t = swap ? at[hi] : at[lo];
-                        at[hi] = swap ? at[lo] : at[hi];
-                        at[lo] = t;
+                        const float hi = fmaxf(k[i + j], k[i + j + q]), lo = fminf(k[i + j], k[i + j + q]);
+                        k[i + j] = hi;
+                        k[i + j + q] = lo;
                     }
-    ord = 0;
-#pragma unroll
-    for (int j = 0; j < R; ++j) ord |= at[j] << (4 * j);
 }
 
 template <int R, bool F32>
@@ -134,13 +133,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
     float bias[R];
     if (a.bias)
 #pragma unroll
-        for (int j = 0; j < R; ++j) bias[j] = lane * R + j < a.E ? a.bias[lane * R + j] : 0.0f;
+        for (int j = 0; j < R; ++j) bias[j] = lane * R + j < a.E ? fminf(fmaxf(a.bias[lane * R + j], -INFINITY), 3.0e38f) : 0.0f;  // NaN: no key
     float next[R];
     load_row<R, F32>(a, row, lane, next);
     for (; row < a.M; row += step) {
         float key[R];                                              // logits, then keys
 #pragma unroll
-        for (int j = 0; j < R; ++j) key[j] = next[j] > -INFINITY ? next[j] : -INFINITY;
+        for (int j = 0; j < R; ++j) key[j] = fmaxf(next[j], -INFINITY);    // (NaN: not available)
         if (row + step < a.M) load_row<R, F32>(a, row + step, lane, next);
         float m = 0.0f, sum = 1.0f;
         if (!a.sigmoid) {
@@ -150,11 +149,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
             m = warp_max(lm);
             float s = 0.0f, e = 0.0f;
 #pragma unroll
-            for (int j = 0; j < R; ++j)
-                if (key[j] > -INFINITY) {
-                    key[j] = key[j] == m ? 1.0f : expf(key[j] - m);        // (the exponential; a score below)
-                    two_sum(s, e, key[j]);
-                }
+            for (int j = 0; j < R; ++j) {
+                const float t = key[j] == m ? 1.0f : expf(key[j] - m);
+                const bool can = key[j] > -INFINITY;
+                two_sum(s, e, can ? t : 0.0f);
+                key[j] = can ? t : -INFINITY;                              // (the exponential; a score below)
+            }
 #pragma unroll
             for (int o = 16; o; o >>= 1) {
                 const float s2 = __shfl_xor_sync(kFull, s, o), e2 = __shfl_xor_sync(kFull, e, o);
@@ -167,43 +167,82 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
             if (a.sigmoid) return __frcp_rn(__fadd_rn(1.0f, expf(-v)));
             return __fdiv_rn(v == m ? 1.0f : expf(v - m), sum);
         };
+        if (a.sigmoid) {
+            float low = 0.0f;
 #pragma unroll
-        for (int j = 0; j < R; ++j)
-            if (key[j] > -INFINITY) {
-                float k = a.sigmoid ? __frcp_rn(__fadd_rn(1.0f, expf(-key[j]))) : __fdiv_rn(key[j], sum);
-                if (a.bias) k = __fadd_rn(k, bias[j]);
-                key[j] = k > -INFINITY ? k : -INFINITY;
+            for (int j = 0; j < R; ++j) {
+                const float x = key[j] > -INFINITY ? key[j] : 0.0f;
+                low = fminf(low, x);
+                const float p = recip_rn(__fadd_rn(1.0f, expf(-x)));
+                key[j] = key[j] > -INFINITY ? p : -INFINITY;
             }
-        uint32_t ord = 0;
-        if constexpr (kSorted) sort_keys<R>(key, ord);
+            if (low < -86.0f) {                                    // 1 + e^-x past recip_rn's range
+                float x[R];
+                load_row<R, F32>(a, row, lane, x);
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    if (x[j] > -INFINITY) key[j] = __frcp_rn(__fadd_rn(1.0f, expf(-x[j])));
+            }
+        } else {
+            // e / sum: the correctly rounded quotient from the correctly rounded reciprocal (the
+            // same method) where no remainder can be subnormal
+            const float r = recip_rn(sum);
+            float low = 1.0f;
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                const float e = key[j] > -INFINITY ? key[j] : 1.0f, q = __fmul_rn(e, r);
+                low = fminf(low, e);
+                const float p = __fmaf_rn(__fmaf_rn(-q, sum, e), r, q);
+                key[j] = key[j] > -INFINITY ? p : -INFINITY;
+            }
+            if (low < 0x1p-90f) {
+                float x[R];
+                load_row<R, F32>(a, row, lane, x);
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    if (x[j] > -INFINITY) key[j] = __fdiv_rn(x[j] == m ? 1.0f : expf(x[j] - m), sum);
+            }
+        }
+        if (a.bias)
+#pragma unroll
+            for (int j = 0; j < R; ++j) key[j] = __fadd_rn(key[j], bias[j]);
+        float head[R];                                             // the keys in descending order
+        if constexpr (kSorted) {
+#pragma unroll
+            for (int j = 0; j < R; ++j) head[j] = key[j];
+            sort_keys<R>(head);
+        }
 
         if (a.n_group > 1) {
             float gs = -INFINITY;
-            if (kSorted && a.group_lanes) {
-                // The best two of the lane are its heads; merged over the group's lanes.
-                float b1 = key[0], b2 = R > 1 ? key[R > 1 ? 1 : 0] : -INFINITY;
-                for (int o = 1; o < a.group_lanes; o <<= 1) {
-                    const float c1 = __shfl_xor_sync(kFull, b1, o), c2 = __shfl_xor_sync(kFull, b2, o);
+            if (kSorted && a.group_shift >= 0) {
+                // The best two of the lane are its heads; merged over the group's lanes.  Then the
+                // best groups one by one, like the picks below.
+                float b1 = head[0], b2 = R > 1 ? head[R > 1 ? 1 : 0] : -INFINITY;
+                for (int o = 0; o < a.group_shift; ++o) {
+                    const float c1 = __shfl_xor_sync(kFull, b1, 1 << o), c2 = __shfl_xor_sync(kFull, b2, 1 << o);
                     b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
                     b1 = fmaxf(b1, c1);
                 }
                 gs = a.group_top == 2 && b2 > -INFINITY ? __fadd_rn(b1, b2) : b1;
-                const int own = lane / a.group_lanes;
-                int rank = 0;
-                for (int g = 0; g < a.n_group; ++g) {
-                    const float o = __shfl_sync(kFull, gs, g * a.group_lanes);
-                    rank += (o > gs || (o == gs && g < own)) ? 1 : 0;
+                const int own = lane >> a.group_shift;
+                bool keep = false;
+                for (int g = 0; g < a.topk_group; ++g) {
+                    const float top = warp_max(gs);
+                    const int src = __ffs(__ballot_sync(kFull, gs == top)) - 1;
+                    const bool mine = own == src >> a.group_shift;
+                    keep = keep || mine;
+                    gs = mine ? -INFINITY : gs;
                 }
-                if (rank >= a.topk_group)
 #pragma unroll
-                    for (int j = 0; j < R; ++j) key[j] = -INFINITY;
+                for (int j = 0; j < R; ++j) head[j] = keep ? head[j] : -INFINITY;
             } else {
                 // Groups that cut across lanes: one after the other, lane g keeping the score of g.
                 for (int g = 0; g < a.n_group; ++g) {
                     float b1 = -INFINITY, b2 = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < R; ++j) {
-                        const int i = lane * R + (kSorted ? static_cast<int>((ord >> (4 * (j & 7))) & 15u) : j);
+                        const int i = lane * R + j;
                         if (i >= g * a.gsize && i < (g + 1) * a.gsize) {
                             b2 = fmaxf(b2, fminf(b1, key[j]));
                             b1 = fmaxf(b1, key[j]);
@@ -222,56 +261,72 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
                 const unsigned keep = __ballot_sync(kFull, lane < a.n_group && rank < a.topk_group);
 #pragma unroll
                 for (int j = 0; j < R; ++j) {
-                    const int i = lane * R + (kSorted ? static_cast<int>((ord >> (4 * (j & 7))) & 15u) : j);
+                    const int i = lane * R + j;
                     if (i < a.E && !((keep >> (i / a.gsize)) & 1u)) key[j] = -INFINITY;
                 }
-                // (a lane's heads may be gone: sorted again, places kept)
                 if constexpr (kSorted) {
-                    uint32_t o2;
-                    const uint32_t o1 = ord;
-                    sort_keys<R>(key, o2);
-                    ord = 0;
 #pragma unroll
-                    for (int j = 0; j < R; ++j)
-                        ord |= ((o1 >> (4 * ((o2 >> (4 * j)) & 15u))) & 15u) << (4 * j);
+                    for (int j = 0; j < R; ++j) head[j] = key[j];
+                    sort_keys<R>(head);
                 }
             }
         }
 
         int id = -1;                                               // lane k: slot k
         float wv = 0.0f;
-        for (int k = 0; k < a.topk; ++k) {
-            float best = key[0];
+        if constexpr (kSorted) {
+            // Each pick: the warp's largest head, the lowest lane that has it.  Which of that
+            // lane's experts it was is found afterwards, for all slots at once: equal keys of a
+            // lane are picked one after the other, so the slot is the `nth` of them.
+            float took = -INFINITY;
+            int from = 0;
+            for (int k = 0; k < a.topk; ++k) {
+                const float top = warp_max(head[0]);
+                if (!(top > -INFINITY)) break;
+                const int src = __ffs(__ballot_sync(kFull, head[0] == top)) - 1;
+                took = lane == k ? top : took;
+                from = lane == k ? src : from;
+                const bool mine = lane == src;
+#pragma unroll
+                for (int j = 0; j + 1 < R; ++j) head[j] = mine ? head[j + 1] : head[j];
+                head[R - 1] = mine ? -INFINITY : head[R - 1];
+            }
+            // nth: how many slots right before this one took the same key from the same lane
+            const float took_before = __shfl_up_sync(kFull, took, 1);
+            const int from_before = __shfl_up_sync(kFull, from, 1);
+            const unsigned same = __ballot_sync(kFull, lane > 0 && took == took_before && from == from_before);
+            int nth = __clz(~(same << (31 - lane)));
             int at = 0;
-            if constexpr (kSorted) {
-                at = static_cast<int>(ord & 15u);
-            } else {
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                const float v = __shfl_sync(kFull, key[j], from);
+                if (v == took && nth-- == 0) at = j;
+            }
+            if (took > -INFINITY) {
+                id = from * R + at;
+                wv = took;
+            }
+        } else {
+            for (int k = 0; k < a.topk; ++k) {
+                float best = key[0];
+                int at = 0;
 #pragma unroll
                 for (int j = 1; j < R; ++j)
                     if (key[j] > best) {
                         best = key[j];
                         at = j;
                     }
-            }
-            const float top = warp_max(best);
-            if (!(top > -INFINITY)) break;
-            const int src = __ffs(__ballot_sync(kFull, best == top)) - 1;
-            const int win = __shfl_sync(kFull, lane * R + at, src);
-            if (lane == k) {
-                id = win;
-                wv = top;
-            }
-            if (lane == src) {
-                if constexpr (kSorted) {
-#pragma unroll
-                    for (int j = 0; j + 1 < R; ++j) key[j] = key[j + 1];
-                    key[R - 1] = -INFINITY;
-                    ord >>= 4;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < R; ++j)
-                        if (j == at) key[j] = -INFINITY;
+                const float top = warp_max(best);
+                if (!(top > -INFINITY)) break;
+                const int src = __ffs(__ballot_sync(kFull, best == top)) - 1;
+                const int win = __shfl_sync(kFull, lane * R + at, src);
+                if (lane == k) {
+                    id = win;
+                    wv = top;
                 }
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    if (lane == src && j == at) key[j] = -INFINITY;
             }
         }
         if (a.bias && id >= 0) wv = score(logit<F32>(a, row, id));  // without the bias
@@ -279,7 +334,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
             float t = wv;
 #pragma unroll
             for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
-            wv = t > 0.0f ? __fdiv_rn(wv, t) : 0.0f;
+            // (a reciprocal within an ulp where neither it nor the sum is subnormal)
+            wv = t > 0x1p-100f ? __fdividef(wv, t) : t > 0.0f ? __fdiv_rn(wv, t) : 0.0f;
         }
         if (lane < a.topk) {
             a.ids[row * a.topk + lane] = id;
@@ -327,7 +383,7 @@ dg_status launch_route(const dg_route_params& p, const void* logits, const float
     a.scale = p.scale;
     const int r = cpow2((E + 31) / 32);
     const int gl = a.gsize % r == 0 ? a.gsize / r : 0;
-    a.group_lanes = gl > 0 && (gl & (gl - 1)) == 0 ? gl : 0;
+    a.group_shift = gl > 0 && (gl & (gl - 1)) == 0 ? clog2(gl) : -1;
     a.vec = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && (ld * (f32 ? 4 : 2)) % 16 == 0 ? 1 : 0;
     const void* fn = f32 ? route_fn<true>(r) : route_fn<false>(r);
     const int occ = occupancy(fn, kWarps * 32, 0);
