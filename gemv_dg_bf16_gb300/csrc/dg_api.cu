@@ -787,7 +787,7 @@ dg_status dg_logprobs(const void* logits, int logits_type, int64_t ld, const int
     if (!(scale >= 1e-6f && scale <= 1e6f) || n_top < 0 || (n_top > 0) != (top_ids != nullptr) ||
         (n_top > 0) != (top_logprobs != nullptr) || (!tokens && (logprob || rank)))
         return DG_ERR_INVALID_ARG;
-    if (n_top > 32 || M > (1 << 28)) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (n_top > 32 || M > (1 << 28) || V > (1 << 24)) return DG_ERR_UNSUPPORTED_SHAPE;
     if (misaligned(tokens, 8) || misaligned(logprob, 4) || misaligned(rank, 4) || misaligned(entropy, 4) ||
         misaligned(top_ids, 4) || misaligned(top_logprobs, 4))
         return DG_ERR_ALIGNMENT;

@@ -5,14 +5,18 @@
 // (the largest logit seen so far times c): y = z c - r, s = sum 2^y, t = sum 2^y y; when
 // the reference moves by d = r_old - r_new, s <- s 2^d and t <- 2^d (t + s d).  Then
 //   logprob = ln 2 (y_token - log2 s),   entropy = ln 2 (log2 s - t / s).
-// Every thread keeps its own reference, and its largest logit for the alternatives: the
-// n-th largest of the threads' largest is a bound that at least n logits reach, so only
-// the threads that reach it are looked at again, with all threads of the CTA.
-// A row belongs to one CTA, or to a cluster of up to 8 when there are few rows; the CTAs'
-// sums and lists meet in shared memory of the first.  The largest, the count and the
+// Every thread keeps its own reference; two terms at a time go through packed binary32
+// operations, and bf16 pairs are compared and clamped as they come.  For the alternatives:
+// the n-th largest of the 32 half-warps' largest logits is a bound that at least n logits
+// reach, so only the threads whose own largest reaches it are looked at again, with all
+// threads of the CTA.
+// A row belongs to one CTA, or to a cluster of up to 16 when there are few rows; the others
+// write their sums and lists into the first one's shared memory.  The largest, the count and the
 // lists do not depend on the split.
 // Bound: memory, 2 or 4 bytes a logit, with many rows; with few, the latency of one
 // CTA's slice and the joins.
+#include <mutex>
+
 #include "dg_common.cuh"
 #include "dg_internal.h"
 
@@ -21,9 +25,12 @@ namespace {
 
 constexpr int kT = 512;                    // threads per CTA
 constexpr int kW = kT / 32;
+constexpr int kU = 8;                      // 16-byte loads in flight a thread (two CTAs an SM: 4: 184 us, 8: 173)
+constexpr int kMaxCs = 16;                 // CTAs of a row (more than 8: the non-portable size)
 constexpr int kMaxTop = 32;
+static_assert(kW == 16, "the first warp joins the warps' sums");
 constexpr int kCand = 1024;                // candidates held at once
-constexpr float kFar = -1.0e30f;           // reference before any logit; far below it counts as none
+constexpr float kFar = -1.0e30f;           // logits are clamped here (masked ones: 0 * y stays 0)
 constexpr float kNear = 1048576.0f;        // |r| up to which z c - r may be off by its rounding (2^-4 at most)
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.442695040888963407f;
@@ -55,6 +62,60 @@ __device__ __forceinline__ float max_nan(float a, float b)
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
+}
+
+// Two binary32 values in one register pair (packed fused multiply-add, add, multiply).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack(float lo, float hi)
+{
+    f32x2 v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Pairs of bf16: the larger (a number where one is NaN; NaN where one is), and -1 in the
+// halves where a > b.
+constexpr uint32_t kFarBf2 = 0xf14af14au;          // about -1e30 twice
+__device__ __forceinline__ uint32_t bf2_max(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf2_max_nan(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t bf2_gt(uint32_t a, uint32_t b)
+{
+    __nv_bfloat162 x, y;
+    memcpy(&x, &a, sizeof x);
+    memcpy(&y, &b, sizeof y);
+    return __hgt2_mask(x, y);
 }
 
 // Order of logits as unsigned: larger is larger, -0 equals +0; 0 for what is never an
@@ -117,14 +178,20 @@ struct Shared {
     Sums sums[kW];
     int count[kW];
     float big[kW];
+    alignas(16) uint32_t half[2 * kW];     // largest keys of the half-warps
     Sums total;
     int total_count;
     float total_big;
-    int n_list, n_cand, n_more;
-    int list[kT];
-    unsigned long long cand[kCand];
+    int n_list, n_cand;
+    uint32_t floor;
     unsigned long long top[kMaxTop];
-    unsigned long long all[8 * kMaxTop];
+    // the first CTA of a cluster: what every CTA found
+    Sums part[kMaxCs];
+    int part_count[kMaxCs];
+    float part_big[kMaxCs];
+    unsigned long long all[kMaxCs * kMaxTop];
+    unsigned long long cand[kCand];
+    int list[kT];
 };
 
 // The row's slice of one CTA: `head` single elements up to a 16-byte boundary (first CTA),
@@ -215,24 +282,56 @@ __device__ void place(const unsigned long long* c, int count, unsigned long long
     for (int i = threadIdx.x; i < count; i += kT) {
         const unsigned long long p = c[i];
         int ahead = 0;
+#pragma unroll 8
         for (int j = 0; j < count; ++j) ahead += c[j] > p ? 1 : 0;
         if (p && ahead < n) out[ahead] = p;
     }
 }
 
-// The slice's n_top largest pairs, in order, in sh.top (0 past the last).
+// The n largest pairs of `lists` lists of n (lists a power of two; each in descending order, 0
+// past its end), in sh.top.  The n-th largest of the lists' first ceil(n / lists) pairs is a
+// bound that the n largest reach; few others do, and those place themselves.
+__device__ void merge(Shared& sh, const unsigned long long* c, int lists, int n)
+{
+    const int lane = threadIdx.x & 31, lg = 31 - __clz(lists), k = (n + lists - 1) >> lg;  // lists * k <= 32
+    const int at = lane >> lg < k ? (lane & (lists - 1)) * n + (lane >> lg) : -1;
+    const unsigned long long v = at >= 0 ? c[at] : 0ull;
+    int above = 0;
+#pragma unroll 8
+    for (int j = 0; j < lists * k; ++j) above += c[(j & (lists - 1)) * n + (j >> lg)] > v ? 1 : 0;
+    const bool in = at >= 0 && above < n;
+    const uint32_t hi = __reduce_min_sync(kFull, in ? static_cast<uint32_t>(v >> 32) : 0xffffffffu);
+    const uint32_t lo = __reduce_min_sync(kFull, in && static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v)
+                                                                                            : 0xffffffffu);
+    const unsigned long long floor = (static_cast<unsigned long long>(hi) << 32) | lo;
+    for (int i = threadIdx.x; i < lists * n; i += kT)
+        if (c[i] && c[i] >= floor) sh.cand[atomicAdd(&sh.n_cand, 1)] = c[i];
+    __syncthreads();
+    place(sh.cand, sh.n_cand, sh.top, n);
+}
+static_assert(kMaxCs * kMaxTop <= kCand, "every pair of the lists fits");
+
+// The slice's n_top largest pairs, in order, in sh.top (0 past the last).  Called with
+// sh.half and cleared counters visible to all threads.
 template <bool F32>
 __device__ void slice_top(Shared& sh, const Slice<F32>& sl, uint32_t mine, int n)
 {
-    if (threadIdx.x < kMaxTop) sh.top[threadIdx.x] = 0;
-    if (threadIdx.x == 0) sh.n_list = sh.n_cand = 0;
-    // The largest bound that n threads reach (1: every key that counts).
-    uint32_t floor = 0;
-    for (int bit = 31; bit >= (F32 ? 0 : 16); --bit) {
-        const uint32_t f = floor | (1u << bit);
-        if (__syncthreads_count(mine >= f) >= n) floor = f;
+    static_assert(2 * kW == 32 && kMaxTop <= 32, "one half-warp a lane, one alternative a half-warp at least");
+    // The n-th largest of the half-warps' largest, the smallest with fewer than n above it
+    // (1: every key that counts); one warp's work, beside the first's sums.
+    if (threadIdx.x >> 5 == 1) {
+        const uint32_t v = sh.half[threadIdx.x & 31];
+        int above = 0;
+#pragma unroll
+        for (int j = 0; j < 2 * kW; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(sh.half + j);
+            above += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
+        }
+        const uint32_t f = __reduce_min_sync(kFull, above < n ? v : 0xffffffffu);
+        if ((threadIdx.x & 31) == 0) sh.floor = f ? f : 1u;
     }
-    if (floor == 0) floor = 1;
+    __syncthreads();
+    const uint32_t floor = sh.floor;
     if (mine >= floor) sh.list[atomicAdd(&sh.n_list, 1)] = threadIdx.x;
     __syncthreads();
     gather<F32>(sh, sl, floor);
@@ -251,34 +350,26 @@ __device__ void slice_top(Shared& sh, const Slice<F32>& sl, uint32_t mine, int n
     }
 }
 
-__device__ __forceinline__ uint32_t peer(const void* p, int rank)
+// Stores into the shared memory of the cluster's first CTA.
+__device__ __forceinline__ uint32_t first_cta(const void* p)
 {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))));
     return r;
 }
 
-__device__ __forceinline__ float peer_f32(const void* p, int rank)
+__device__ __forceinline__ void put_f32(float* p, float v)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer(p, rank)));
-    return v;
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(first_cta(p)), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ unsigned long long peer_u64(const void* p, int rank)
+__device__ __forceinline__ void put_u64(unsigned long long* p, unsigned long long v)
 {
-    unsigned long long v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(peer(p, rank)));
-    return v;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(first_cta(p)), "l"(v) : "memory");
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kT) logprobs_kernel(LpArgs a)
+__global__ void __launch_bounds__(kT, 2) logprobs_kernel(LpArgs a)
 {
     constexpr int VE = Vec<F32>::n;
     __shared__ Shared sh;
@@ -287,6 +378,8 @@ __global__ void __launch_bounds__(kT) logprobs_kernel(LpArgs a)
     const int cs = a.cs, rank_in = static_cast<int>(blockIdx.x) % cs;
     const long long m = blockIdx.x / cs;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (the first CTA runs before others write into it: waited for below)
+    if (cs > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
     Slice<F32> sl;
     sl.row = static_cast<const uint8_t*>(a.logits) + m * a.ld * (F32 ? 4 : 2);
@@ -307,96 +400,166 @@ __global__ void __launch_bounds__(kT) logprobs_kernel(LpArgs a)
     const float zt = has_tok ? Vec<F32>::at(sl.row, static_cast<int>(tok)) : INFINITY;
     const float c = a.scale * kLog2e;
 
-    Sums u{kFar, 0.0f, 0.0f};
-    float big = -INFINITY;                 // largest logit (NaN aside)
+    // The reference before any logit: far below every one that counts, and yet so far above the
+    // clamp below that 2^y of a clamped logit is 0.
+    float r = 0.5f * kFar * c, big = -INFINITY;        // (big: largest logit, NaN aside)
+    f32x2 s2 = pack(0.0f, 0.0f), t2 = s2, nr = pack(-r, -r);
+    const f32x2 c2 = pack(c, c);
     int count = 0;
+    uint32_t masks = 0;                    // sum of comparison masks, see below
     auto refer = [&](float z) {            // moves the reference up to z
-        const float r = z * c;
-        if (r > u.r) {
-            const float d = u.r - r, f = ex2(d);
-            u.t = f * (u.t + u.s * d);
-            u.s *= f;
-            u.r = r;
+        const float to = z * c;
+        if (to > r) {
+            const float d = r - to, f = ex2(d);
+            const f32x2 f2 = pack(f, f), d2 = pack(d, d);
+            t2 = mul2(f2, fma2(s2, d2, t2));
+            s2 = mul2(s2, f2);
+            r = to;
+            nr = pack(-to, -to);
         }
     };
-    auto add = [&](float z) {
-        const float y = max_nan(fmaf(z, c, -u.r), kFar);
-        const float e = ex2(y);
-        u.s += e;
-        u.t = fmaf(e, y, u.t);
-        count += z > zt ? 1 : 0;
+    auto add = [&](float z0, float z1) {
+        const f32x2 y = fma2(pack(z0, z1), c2, nr);
+        float y0, y1;
+        unpack2(y, y0, y1);
+        const f32x2 e = pack(ex2(y0), ex2(y1));
+        s2 = add2(s2, e);
+        t2 = fma2(e, y, t2);
     };
     if (tid < sl.n_single) {
         const float z = Vec<F32>::at(sl.row, sl.single(tid));
         big = fmaxf(big, z);
         refer(big);
-        add(z);
+        add(max_nan(z, kFar), kFar);
+        count += z > zt ? 1 : 0;
     }
-#pragma unroll 4
-    for (int v = sl.v0 + tid; v < sl.v1; v += kT) {
-        float z[VE];
-        Vec<F32>::unpack(ld_stream_after(sl.vec + v), z);
-        float vm = z[0];
+    const uint32_t zt2 = F32 ? 0u : (__float_as_uint(zt) >> 16) * 0x10001u;
+    // Two vectors at a time: one test for a new largest, one for logits above the token's.
+    auto take = [&](const uint4& p, const uint4& q) {
+        const uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+        float vm;
+        if constexpr (F32) {
+            vm = __uint_as_float(w[0]);
 #pragma unroll
-        for (int j = 1; j < VE; ++j) vm = fmaxf(vm, z[j]);
+            for (int j = 1; j < 8; ++j) vm = fmaxf(vm, __uint_as_float(w[j]));
+        } else {
+            const uint32_t m2 = bf2_max(bf2_max(bf2_max(w[0], w[1]), bf2_max(w[2], w[3])),
+                                        bf2_max(bf2_max(w[4], w[5]), bf2_max(w[6], w[7])));
+            vm = fmaxf(bf16_lo(m2), bf16_hi(m2));
+        }
         if (vm > big) {
             big = vm;
             refer(vm);
         }
+        if (vm > zt) {
 #pragma unroll
-        for (int j = 0; j < VE; ++j) add(z[j]);
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (F32)
+                    count += __uint_as_float(w[j]) > zt ? 1 : 0;
+                else               // each mask is -1 in the halves that hold a larger logit: their sum
+                    masks += bf2_gt(w[j], zt2);        // mod 2^32 is 2^16 (n_lo - n_hi) - n_lo
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (F32) {
+                if (j & 1) add(max_nan(__uint_as_float(w[j - 1]), kFar), max_nan(__uint_as_float(w[j]), kFar));
+            } else {
+                const uint32_t z = bf2_max_nan(w[j], kFarBf2);
+                add(bf16_lo(z), bf16_hi(z));
+            }
+        }
+    };
+    // kU loads in flight a thread; past the last vector, masked ones.
+    constexpr uint32_t kMasked = F32 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll 1
+    for (int v = sl.v0 + tid; v < sl.v1; v += kU * kT) {
+        uint4 q[kU];
+#pragma unroll
+        for (int i = 0; i < kU; ++i)
+            q[i] = v + i * kT < sl.v1 ? ld_stream_after(sl.vec + v + i * kT)
+                                      : make_uint4(kMasked, kMasked, kMasked, kMasked);
+#pragma unroll
+        for (int i = 0; i < kU; i += 2) take(q[i], q[i + 1]);
+    }
+    if constexpr (!F32) {
+        const int lo = static_cast<int>((0u - masks) & 0xffffu);
+        count += 2 * lo - (static_cast<int>(masks + static_cast<uint32_t>(lo)) >> 16);
+    }
+    Sums u;
+    {
+        float s0, s1, t0, t1;
+        unpack2(s2, s0, s1);
+        unpack2(t2, t0, t1);
+        u = Sums{r, s0 + s1, t0 + t1};
     }
     const uint32_t mine = order_key(big);
 
-    // CTA totals
+    // CTA totals: warps, then the warps' in the first warp, beside the search for alternatives.
+    auto join_lanes = [&](int from) {
+        for (int o = from; o; o >>= 1) {
+            const Sums v{__shfl_xor_sync(kFull, u.r, o), __shfl_xor_sync(kFull, u.s, o), __shfl_xor_sync(kFull, u.t, o)};
+            u = join(u, v);
+            count += __shfl_xor_sync(kFull, count, o);
+            big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
+        }
+    };
+    uint32_t half = mine;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const Sums v{__shfl_xor_sync(kFull, u.r, o), __shfl_xor_sync(kFull, u.s, o), __shfl_xor_sync(kFull, u.t, o)};
-        u = join(u, v);
-        count += __shfl_xor_sync(kFull, count, o);
-        big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
-    }
+    for (int o = 8; o; o >>= 1) half = max(half, __shfl_xor_sync(kFull, half, o));
+    join_lanes(16);
+    if ((lane & 15) == 0) sh.half[2 * warp + (lane >> 4)] = half;
     if (lane == 0) {
         sh.sums[warp] = u;
         sh.count[warp] = count;
         sh.big[warp] = big;
     }
+    if (tid < kMaxTop) sh.top[tid] = 0;
+    if (tid == 0) sh.n_list = sh.n_cand = 0;
     __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < kW; ++w) {
-            u = join(u, sh.sums[w]);
-            count += sh.count[w];
-            big = fmaxf(big, sh.big[w]);
+    if (warp == 0) {
+        const bool on = lane < kW;
+        u = on ? sh.sums[lane] : Sums{kFar, 0.0f, 0.0f};
+        count = on ? sh.count[lane] : 0;
+        big = on ? sh.big[lane] : -INFINITY;
+        join_lanes(kW / 2);
+        if (lane == 0) {
+            sh.total = u;
+            sh.total_count = count;
+            sh.total_big = big;
         }
-        sh.total = u;
-        sh.total_count = count;
-        sh.total_big = big;
     }
     if (a.n_top > 0) slice_top<F32>(sh, sl, mine, a.n_top);
     __syncthreads();
     if (cs > 1) {
-        cluster_sync();
-        if (rank_in == 0) {
-            if (tid == 0) {
-                for (int r = 1; r < cs; ++r) {
-                    u = join(u, Sums{peer_f32(&sh.total.r, r), peer_f32(&sh.total.s, r), peer_f32(&sh.total.t, r)});
-                    count += __float_as_int(peer_f32(&sh.total_count, r));
-                    big = fmaxf(big, peer_f32(&sh.total_big, r));
-                }
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (tid < a.n_top) put_u64(&sh.all[rank_in * a.n_top + tid], sh.top[tid]);
+        if (tid == 0) {
+            put_f32(&sh.part[rank_in].r, sh.total.r);
+            put_f32(&sh.part[rank_in].s, sh.total.s);
+            put_f32(&sh.part[rank_in].t, sh.total.t);
+            put_f32(reinterpret_cast<float*>(&sh.part_count[rank_in]), __int_as_float(sh.total_count));
+            put_f32(&sh.part_big[rank_in], sh.total_big);
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (rank_in != 0) return;
+        if (tid < kMaxTop) sh.top[tid] = 0;
+        if (tid == 0) sh.n_cand = 0;
+        if (warp == 0) {
+            const bool on = lane < cs;
+            u = on ? sh.part[lane] : Sums{kFar, 0.0f, 0.0f};
+            count = on ? sh.part_count[lane] : 0;
+            big = on ? sh.part_big[lane] : -INFINITY;
+            join_lanes(kMaxCs / 2);
+            if (lane == 0) {
                 sh.total = u;
                 sh.total_count = count;
                 sh.total_big = big;
             }
-            const int n = cs * a.n_top;
-            for (int i = tid; i < n; i += kT) sh.all[i] = peer_u64(&sh.top[i % a.n_top], i / a.n_top);
-            __syncthreads();
-            if (tid < kMaxTop) sh.top[tid] = 0;
-            __syncthreads();
-            place(sh.all, n, sh.top, a.n_top);
-            __syncthreads();
         }
-        cluster_sync();                    // no CTA leaves while the first reads it
-        if (rank_in != 0) return;
+        __syncthreads();
+        if (a.n_top > 0) merge(sh, sh.all, cs, a.n_top);
+        __syncthreads();
     }
     u = sh.total;
     big = sh.total_big;
@@ -448,6 +611,34 @@ __global__ void __launch_bounds__(kT) logprobs_kernel(LpArgs a)
     }
 }
 
+// Whether the device holds a cluster of 16 of these CTAs (asked once per device and type, which
+// also allows the size).
+bool allow_wide_clusters(const DeviceInfo* dev, const void* fn, bool f32)
+{
+    static std::mutex mu;
+    static int known[64][2];
+    std::lock_guard<std::mutex> lk(mu);
+    int& k = known[dev->device][f32 ? 1 : 0];
+    if (k == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kMaxCs);
+        cfg.blockDim = dim3(kT);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kMaxCs;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const bool ok = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0;
+        cudaGetLastError();
+        k = ok ? 1 : -1;
+    }
+    return k > 0;
+}
+
 }  // namespace
 
 dg_status launch_logprobs(const void* logits, bool f32, long long ld, const int64_t* tokens, float scale, int n_top,
@@ -470,12 +661,20 @@ dg_status launch_logprobs(const void* logits, bool f32, long long ld, const int6
     a.top_lp = top_logprobs;
     a.M = M;
     a.V = V;
-    // CTAs per row: as many as fill the SMs, no slice below 4 vectors a thread.
+    // CTAs per row: with few rows as many as two for each SM (one CTA alone is bound by its
+    // instructions: 248320 logits take it 14 us), no slice below two vectors a thread; 16, which
+    // has to lie in one GPC, where the rows are few enough for each to have one.
     int cs = 1;
-    while (cs < 8 && static_cast<long long>(M) * cs * 2 <= dev->sm_count && V / (cs * 2) >= kT * (f32 ? 16 : 32)) cs *= 2;
+    while (cs < kMaxCs && static_cast<long long>(M) * cs * 2 <= 2ll * dev->sm_count &&
+           V / (cs * 2) >= 2 * kT * (f32 ? 4 : 8) && (cs < 8 || M <= 4))
+        cs *= 2;
     a.cs = cs;
     const void* fn = f32 ? reinterpret_cast<const void*>(&logprobs_kernel<true>)
                          : reinterpret_cast<const void*>(&logprobs_kernel<false>);
+    if (cs > 8 && !allow_wide_clusters(dev, fn, f32)) {
+        cs = 8;
+        a.cs = cs;
+    }
     void* args[] = {&a};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(M) * cs));
