@@ -329,51 +329,27 @@ def dg_quant_a8_blockscale(x, q=None, sx=None, stream=None):
     return q, sx
 
 
-# The calls below are small enough that marshalling them shows in a decode step: pointers go
-# to ctypes as plain integers, and the stream is read without making a Stream object.
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
-_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The calls below are small enough that marshalling them shows in a decode step: their checks
+# and the C call run in _marshal.so, which takes the arguments by position.
+_marshal = None
 
 
-def _raw_stream(stream):
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream_of is None:
-        return torch.cuda.current_stream().cuda_stream
-    return _raw_stream_of(_current_device())
-
-
-def _tensor(t, name, dtype, shape):
-    """Address of a dense CUDA tensor of this dtype and shape, or ValueError."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError(f"{name}: tensors must be contiguous CUDA tensors")
-    return t.data_ptr()
-
-
-def _scalar(t, name):
-    """Address of one fp32 on the device (None: none)."""
-    if t is None:
-        return None
-    if t.dtype is not torch.float32 or t.numel() != 1:
-        raise ValueError(f"{name}: expected one torch.float32 value")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: tensors must be contiguous CUDA tensors")
-    return t.data_ptr()
+def _load_marshal():
+    global _marshal
+    lib()
+    try:
+        from . import _marshal as m
+    except ImportError as e:
+        raise ImportError(f"_marshal.so is not built beside {_LIBPATH}; run __graft_entry__.build()") from e
+    m.bind(_LIBPATH)
+    _marshal = m
+    return m
 
 
 def fp4_scale_shape(rows: int, K: int, fmt: int):
     """Shape of the tiled block scales: [ceil(rows / 128), ceil(blocks / 4), 512] bytes."""
     block = 16 if fmt == DG_FP4_NV else 32
     return (rows + 127) // 128, (K // block + 3) // 4, 512
-
-
-def _fp4_fmt(fmt):
-    if fmt not in (DG_FP4_MX, DG_FP4_NV):
-        raise ValueError(f"fmt: {fmt}, expected DG_FP4_MX or DG_FP4_NV")
 
 
 def dg_fp4_scale_bytes(rows: int, K: int, fmt: int) -> int:
@@ -383,91 +359,68 @@ def dg_fp4_scale_bytes(rows: int, K: int, fmt: int) -> int:
 def dg_quant_fp4_blockscale(x, fmt, g=None, q=None, s=None, stream=None):
     """(q [M, K/2] uint8 code pairs, s uint8 tiled block scales) of x [M, K] bf16 in the MX or
     NV 4-bit format; g: the NV tensor scale (one fp32 on the device), None for 1."""
-    M, K = x.shape
-    _fp4_fmt(fmt)
+    m = _marshal or _load_marshal()
     if q is None:
-        q = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
+        q = torch.empty((x.shape[0], x.shape[1] // 2), dtype=torch.uint8, device=x.device)
     if s is None:
-        s = torch.empty(fp4_scale_shape(M, K, fmt), dtype=torch.uint8, device=x.device)
-    _ok(lib().dg_quant_fp4_blockscale(_tensor(x, "x", torch.bfloat16, (M, K)), _tensor(q, "q", torch.uint8, (M, K // 2)),
-                                      _tensor(s, "s", torch.uint8, fp4_scale_shape(M, K, fmt)), _scalar(g, "g"), M, K,
-                                      fmt, _raw_stream(stream)), "dg_quant_fp4_blockscale")
+        s = torch.empty(fp4_scale_shape(x.shape[0], x.shape[1], fmt), dtype=torch.uint8, device=x.device)
+    st = m.quant(x, fmt, g, q, s, None if stream is None else stream.cuda_stream)
+    if st:
+        raise DGError(st, "dg_quant_fp4_blockscale")
     return q, s
 
 
 def dg_dequant_fp4_blockscale(q, s, fmt, g=None, y=None, stream=None):
     """y [M, K] bf16: the values that the codes and scales of dg_quant_fp4_blockscale stand for."""
-    M, K = q.shape[0], 2 * q.shape[1]
-    _fp4_fmt(fmt)
+    m = _marshal or _load_marshal()
     if y is None:
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=q.device)
-    _ok(lib().dg_dequant_fp4_blockscale(_tensor(q, "q", torch.uint8, (M, K // 2)),
-                                        _tensor(s, "s", torch.uint8, fp4_scale_shape(M, K, fmt)), _scalar(g, "g"),
-                                        _tensor(y, "y", torch.bfloat16, (M, K)), M, K, fmt, _raw_stream(stream)),
-        "dg_dequant_fp4_blockscale")
+        y = torch.empty((q.shape[0], 2 * q.shape[1]), dtype=torch.bfloat16, device=q.device)
+    st = m.dequant(q, s, fmt, g, y, None if stream is None else stream.cuda_stream)
+    if st:
+        raise DGError(st, "dg_dequant_fp4_blockscale")
     return y
 
 
 def dg_gemv_a4w4_blockscale(x, Wq, sw, fmt, gx=None, gw=None, y=None, ws=None, choice=None, stream=None):
     """y [M, N] bf16 = microscaled 4-bit product of x [M, K] (bf16, quantised inside the call with
     tensor scale gx) and the weights Wq [N, K/2], sw, gw as dg_quant_fp4_blockscale makes them."""
-    M, K = x.shape
-    N = Wq.shape[0]
-    _fp4_fmt(fmt)
+    m = _marshal or _load_marshal()
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty((x.shape[0], Wq.shape[0]), dtype=torch.bfloat16, device=x.device)
     if ws is None:
-        ws = workspace(DG_OP_GEMV_A4W4, M, N, K, device=x.device)
-    _ok(lib().dg_gemv_a4w4_blockscale(_tensor(x, "x", torch.bfloat16, (M, K)),
-                                      _tensor(Wq, "Wq", torch.uint8, (N, K // 2)),
-                                      _tensor(sw, "sw", torch.uint8, fp4_scale_shape(N, K, fmt)), _scalar(gx, "gx"),
-                                      _scalar(gw, "gw"), _tensor(y, "y", torch.bfloat16, (M, N)), M, N, K, fmt,
-                                      _tensor(ws, "ws", torch.uint8, ws.shape), ws.numel(), _raw_stream(stream),
-                                      _choice(choice)), "dg_gemv_a4w4_blockscale")
+        ws = workspace(DG_OP_GEMV_A4W4, x.shape[0], Wq.shape[0], x.shape[1], device=x.device)
+    if choice is not None and not isinstance(choice, Choice):
+        choice = Choice.make(*choice)
+    st = m.a4w4(x, Wq, sw, fmt, gx, gw, y, ws, None if choice is None else ctypes.addressof(choice),
+                None if stream is None else stream.cuda_stream)
+    if st:
+        raise DGError(st, "dg_gemv_a4w4_blockscale")
     return y
-
-
-def _logits(t):
-    """(address, element type, row stride) of [M, n] logits: bf16 or fp32, rows dense, any row stride."""
-    if t.dtype is torch.bfloat16:
-        kind = DG_LOGITS_BF16
-    elif t.dtype is torch.float32:
-        kind = DG_LOGITS_F32
-    else:
-        raise ValueError(f"logits: dtype {t.dtype}, expected torch.bfloat16 or torch.float32")
-    if t.dim() != 2:
-        raise ValueError(f"logits: shape {tuple(t.shape)}, expected two dimensions")
-    M, n = t.shape
-    ld, one = t.stride()
-    if not t.is_cuda or (one != 1 and n > 1) or (ld < n and M > 1):
-        raise ValueError("logits: rows must be dense and apart, on a CUDA device")
-    return t.data_ptr(), kind, max(ld, n)
 
 
 def dg_moe_route(logits, topk, score=DG_SCORE_SOFTMAX, bias=None, n_group=1, topk_group=1, group_top=1, renorm=True,
                  scale=1.0, ids=None, w=None, stream=None):
     """(ids [M, topk] int32, w [M, topk] fp32): the experts and gate weights of each token, as
-    dg_moe_w1_silu and dg_moe_w2 take them, from router logits [M, E]."""
-    p, kind, ld = _logits(logits)
-    M, E = logits.shape
+    dg_moe_w1_silu and dg_moe_w2 take them, from router logits [M, E] (bf16 or fp32, any row stride)."""
+    m = _marshal or _load_marshal()
     if ids is None:
-        ids = torch.empty((M, topk), dtype=torch.int32, device=logits.device)
+        ids = torch.empty((logits.shape[0], max(topk, 0)), dtype=torch.int32, device=logits.device)
     if w is None:
-        w = torch.empty((M, topk), dtype=torch.float32, device=logits.device)
-    prm = RouteParams(topk, n_group, topk_group, group_top, score, 1 if renorm else 0, scale)
-    _ok(lib().dg_moe_route(p, kind, ld, None if bias is None else _tensor(bias, "bias", torch.float32, (E,)), prm,
-                           _tensor(ids, "ids", torch.int32, (M, topk)), _tensor(w, "w", torch.float32, (M, topk)), M, E,
-                           _raw_stream(stream)), "dg_moe_route")
+        w = torch.empty((logits.shape[0], max(topk, 0)), dtype=torch.float32, device=logits.device)
+    st = m.route(logits, topk, score, bias, n_group, topk_group, group_top, renorm, scale, ids, w,
+                 None if stream is None else stream.cuda_stream)
+    if st:
+        raise DGError(st, "dg_moe_route")
     return ids, w
 
 
 def dg_logprobs(logits, tokens=None, n_top=0, scale=1.0, logprob=None, rank=None, entropy=None, top_ids=None,
                 top_logprobs=None, stream=None):
-    """Log-probabilities over logits [M, V]: a dict of logprob [M], rank [M] (of tokens [M] int64;
-    None without them), entropy [M], top_ids and top_logprobs [M, n_top] (None at 0)."""
-    p, kind, ld = _logits(logits)
-    M, V = logits.shape
-    dev = logits.device
+    """Log-probabilities over logits [M, V] (bf16 or fp32, any row stride): a dict of logprob [M],
+    rank [M] (of tokens [M] int64; None without them), entropy [M], top_ids and top_logprobs
+    [M, n_top] (None at 0)."""
+    m = _marshal or _load_marshal()
+    M, dev = logits.shape[0], logits.device
     if tokens is not None:
         if logprob is None:
             logprob = torch.empty((M,), dtype=torch.float32, device=dev)
@@ -484,13 +437,10 @@ def dg_logprobs(logits, tokens=None, n_top=0, scale=1.0, logprob=None, rank=None
             top_logprobs = torch.empty((M, n_top), dtype=torch.float32, device=dev)
     elif top_ids is not None or top_logprobs is not None:
         raise ValueError("n_top: top_ids and top_logprobs need it")
-    _ok(lib().dg_logprobs(p, kind, ld, None if tokens is None else _tensor(tokens, "tokens", torch.int64, (M,)), scale,
-                          n_top, None if logprob is None else _tensor(logprob, "logprob", torch.float32, (M,)),
-                          None if rank is None else _tensor(rank, "rank", torch.int32, (M,)),
-                          _tensor(entropy, "entropy", torch.float32, (M,)),
-                          None if n_top <= 0 else _tensor(top_ids, "top_ids", torch.int32, (M, n_top)),
-                          None if n_top <= 0 else _tensor(top_logprobs, "top_logprobs", torch.float32, (M, n_top)),
-                          M, V, _raw_stream(stream)), "dg_logprobs")
+    st = m.logprobs(logits, tokens, scale, n_top, logprob, rank, entropy, top_ids, top_logprobs,
+                    None if stream is None else stream.cuda_stream)
+    if st:
+        raise DGError(st, "dg_logprobs")
     return {"logprob": logprob, "rank": rank, "entropy": entropy, "top_ids": top_ids, "top_logprobs": top_logprobs}
 
 

@@ -7,7 +7,7 @@
 //   logprob = ln 2 (y_token - log2 s),   entropy = ln 2 (log2 s - t / s).
 // Every thread keeps its own reference; two terms at a time go through packed binary32
 // operations, and bf16 pairs are compared and clamped as they come.  For the alternatives:
-// the n-th largest of the 32 half-warps' largest logits is a bound that at least n logits
+// the n-th largest of the 32 parts' largest logits is a bound that at least n logits
 // reach, so only the threads whose own largest reaches it are looked at again, with all
 // threads of the CTA.
 // A row belongs to one CTA, or to a cluster of up to 16 when there are few rows; the others
@@ -23,12 +23,13 @@
 namespace dg {
 namespace {
 
-constexpr int kT = 512;                    // threads per CTA
-constexpr int kW = kT / 32;
-constexpr int kU = 8;                      // 16-byte loads in flight a thread (two CTAs an SM: 4: 184 us, 8: 173)
+// Threads per CTA (template parameter T).  A row costs a CTA a few us beside its bytes, so many
+// short rows take small CTAs, eight or more of them on an SM.
+constexpr int kWide = 512, kNarrow = 128;
+constexpr int kU = 8;                      // 16-byte loads in flight a thread (two wide CTAs an SM: 4: 184 us, 8: 173)
 constexpr int kMaxCs = 16;                 // CTAs of a row (more than 8: the non-portable size)
 constexpr int kMaxTop = 32;
-static_assert(kW == 16, "the first warp joins the warps' sums");
+
 constexpr int kCand = 1024;                // candidates held at once
 constexpr float kFar = -1.0e30f;           // logits are clamped here (masked ones: 0 * y stays 0)
 constexpr float kNear = 1048576.0f;        // |r| up to which z c - r may be off by its rounding (2^-4 at most)
@@ -174,11 +175,14 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b)
     return {r, a.s * fa + b.s * fb, fa * (a.t + a.s * da) + fb * (b.t + b.s * db)};
 }
 
+template <int T>
 struct Shared {
+    static constexpr int kW = T / 32;
+    static_assert(kW >= 2 && kW <= 32, "the first warp joins the warps' sums, the second finds the bound");
     Sums sums[kW];
     int count[kW];
     float big[kW];
-    alignas(16) uint32_t half[2 * kW];     // largest keys of the half-warps
+    alignas(16) uint32_t part_key[32];     // largest keys of T / 32 threads each
     Sums total;
     int total_count;
     float total_big;
@@ -191,12 +195,12 @@ struct Shared {
     float part_big[kMaxCs];
     unsigned long long all[kMaxCs * kMaxTop];
     unsigned long long cand[kCand];
-    int list[kT];
+    int list[T];
 };
 
 // The row's slice of one CTA: `head` single elements up to a 16-byte boundary (first CTA),
 // vectors [v0, v1), `tail` single elements (last CTA).  Single elements belong to the
-// threads 0.. in order, vectors to thread (v - v0) % kT.
+// threads 0.. in order, vectors to thread (v - v0) % T.
 template <bool F32>
 struct Slice {
     const void* row;
@@ -210,12 +214,12 @@ struct Slice {
 };
 
 // Every (key, index) of this thread's share of `list` that reaches `floor`, to the candidates.
-template <bool F32>
-__device__ void gather(Shared& sh, const Slice<F32>& sl, uint32_t floor)
+template <bool F32, int T>
+__device__ void gather(Shared<T>& sh, const Slice<F32>& sl, uint32_t floor)
 {
-    const int per = (sl.v1 - sl.v0 + kT - 1) / kT;
+    const int per = (sl.v1 - sl.v0 + T - 1) / T;
     const int n = sh.n_list * (per + 1);
-    for (int q = threadIdx.x; q < n; q += kT) {
+    for (int q = threadIdx.x; q < n; q += T) {
         const int e = q / (per + 1), k = q - e * (per + 1), t = sh.list[e];
         if (k == per) {
             if (t < sl.n_single) {
@@ -228,7 +232,7 @@ __device__ void gather(Shared& sh, const Slice<F32>& sl, uint32_t floor)
             }
             continue;
         }
-        const int v = sl.v0 + k * kT + t;
+        const int v = sl.v0 + k * T + t;
         if (v >= sl.v1) continue;
         float z[Vec<F32>::n];
         Vec<F32>::unpack(sl.vec[v], z);
@@ -244,8 +248,8 @@ __device__ void gather(Shared& sh, const Slice<F32>& sl, uint32_t floor)
 }
 
 // The largest pair of the slice below `below`, for every thread.
-template <bool F32>
-__device__ unsigned long long next_pair(Shared& sh, const Slice<F32>& sl, unsigned long long below)
+template <bool F32, int T>
+__device__ unsigned long long next_pair(Shared<T>& sh, const Slice<F32>& sl, unsigned long long below)
 {
     unsigned long long best = 0;
     auto see = [&](float z, int i) {
@@ -257,7 +261,7 @@ __device__ unsigned long long next_pair(Shared& sh, const Slice<F32>& sl, unsign
         const int i = sl.single(threadIdx.x);
         see(Vec<F32>::at(sl.row, i), i);
     }
-    for (int v = sl.v0 + threadIdx.x; v < sl.v1; v += kT) {
+    for (int v = sl.v0 + threadIdx.x; v < sl.v1; v += T) {
         float z[Vec<F32>::n];
         Vec<F32>::unpack(sl.vec[v], z);
 #pragma unroll
@@ -266,7 +270,7 @@ __device__ unsigned long long next_pair(Shared& sh, const Slice<F32>& sl, unsign
     __syncthreads();
     sh.cand[threadIdx.x] = best;
     __syncthreads();
-    for (int o = kT / 2; o; o >>= 1) {
+    for (int o = T / 2; o; o >>= 1) {
         if (static_cast<int>(threadIdx.x) < o)
             sh.cand[threadIdx.x] = max(sh.cand[threadIdx.x], sh.cand[threadIdx.x + o]);
         __syncthreads();
@@ -277,9 +281,10 @@ __device__ unsigned long long next_pair(Shared& sh, const Slice<F32>& sl, unsign
 }
 
 // The n largest pairs among c, each thread placing its own by counting those ahead.
+template <int T>
 __device__ void place(const unsigned long long* c, int count, unsigned long long* out, int n)
 {
-    for (int i = threadIdx.x; i < count; i += kT) {
+    for (int i = threadIdx.x; i < count; i += T) {
         const unsigned long long p = c[i];
         int ahead = 0;
 #pragma unroll 8
@@ -291,7 +296,8 @@ __device__ void place(const unsigned long long* c, int count, unsigned long long
 // The n largest pairs of `lists` lists of n (lists a power of two; each in descending order, 0
 // past its end), in sh.top.  The n-th largest of the lists' first ceil(n / lists) pairs is a
 // bound that the n largest reach; few others do, and those place themselves.
-__device__ void merge(Shared& sh, const unsigned long long* c, int lists, int n)
+template <int T>
+__device__ void merge(Shared<T>& sh, const unsigned long long* c, int lists, int n)
 {
     const int lane = threadIdx.x & 31, lg = 31 - __clz(lists), k = (n + lists - 1) >> lg;  // lists * k <= 32
     const int at = lane >> lg < k ? (lane & (lists - 1)) * n + (lane >> lg) : -1;
@@ -304,27 +310,27 @@ __device__ void merge(Shared& sh, const unsigned long long* c, int lists, int n)
     const uint32_t lo = __reduce_min_sync(kFull, in && static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v)
                                                                                             : 0xffffffffu);
     const unsigned long long floor = (static_cast<unsigned long long>(hi) << 32) | lo;
-    for (int i = threadIdx.x; i < lists * n; i += kT)
+    for (int i = threadIdx.x; i < lists * n; i += T)
         if (c[i] && c[i] >= floor) sh.cand[atomicAdd(&sh.n_cand, 1)] = c[i];
     __syncthreads();
-    place(sh.cand, sh.n_cand, sh.top, n);
+    place<T>(sh.cand, sh.n_cand, sh.top, n);
 }
 static_assert(kMaxCs * kMaxTop <= kCand, "every pair of the lists fits");
 
 // The slice's n_top largest pairs, in order, in sh.top (0 past the last).  Called with
-// sh.half and cleared counters visible to all threads.
-template <bool F32>
-__device__ void slice_top(Shared& sh, const Slice<F32>& sl, uint32_t mine, int n)
+// sh.part_key and cleared counters visible to all threads.
+template <bool F32, int T>
+__device__ void slice_top(Shared<T>& sh, const Slice<F32>& sl, uint32_t mine, int n)
 {
-    static_assert(2 * kW == 32 && kMaxTop <= 32, "one half-warp a lane, one alternative a half-warp at least");
-    // The n-th largest of the half-warps' largest, the smallest with fewer than n above it
+    static_assert(kMaxTop <= 32, "one alternative a part at least");
+    // The n-th largest of the parts' largest, the smallest with fewer than n above it
     // (1: every key that counts); one warp's work, beside the first's sums.
     if (threadIdx.x >> 5 == 1) {
-        const uint32_t v = sh.half[threadIdx.x & 31];
+        const uint32_t v = sh.part_key[threadIdx.x & 31];
         int above = 0;
 #pragma unroll
-        for (int j = 0; j < 2 * kW; j += 4) {
-            const uint4 o = *reinterpret_cast<const uint4*>(sh.half + j);
+        for (int j = 0; j < 32; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(sh.part_key + j);
             above += (o.x > v ? 1 : 0) + (o.y > v ? 1 : 0) + (o.z > v ? 1 : 0) + (o.w > v ? 1 : 0);
         }
         const uint32_t f = __reduce_min_sync(kFull, above < n ? v : 0xffffffffu);
@@ -334,17 +340,17 @@ __device__ void slice_top(Shared& sh, const Slice<F32>& sl, uint32_t mine, int n
     const uint32_t floor = sh.floor;
     if (mine >= floor) sh.list[atomicAdd(&sh.n_list, 1)] = threadIdx.x;
     __syncthreads();
-    gather<F32>(sh, sl, floor);
+    gather<F32, T>(sh, sl, floor);
     __syncthreads();
     const int c = sh.n_cand;
     if (c <= kCand) {
-        place(sh.cand, c, sh.top, n);
+        place<T>(sh.cand, c, sh.top, n);
         return;
     }
     // More logits at the bound than are held (rows of equal values): one at a time.
     unsigned long long p = ~0ull;
     for (int k = 0; k < n; ++k) {
-        p = next_pair<F32>(sh, sl, p);
+        p = next_pair<F32, T>(sh, sl, p);
         if (!p) break;
         if (threadIdx.x == 0) sh.top[k] = p;
     }
@@ -368,11 +374,11 @@ __device__ __forceinline__ void put_u64(unsigned long long* p, unsigned long lon
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(first_cta(p)), "l"(v) : "memory");
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(kT, 2) logprobs_kernel(LpArgs a)
+template <bool F32, int T>
+__global__ void __launch_bounds__(T, 1024 / T) logprobs_kernel(LpArgs a)
 {
-    constexpr int VE = Vec<F32>::n;
-    __shared__ Shared sh;
+    constexpr int VE = Vec<F32>::n, kW = T / 32;
+    __shared__ Shared<T> sh;
     pdl_launch_dependents();
     pdl_wait();
     const int cs = a.cs, rank_in = static_cast<int>(blockIdx.x) % cs;
@@ -473,11 +479,11 @@ __global__ void __launch_bounds__(kT, 2) logprobs_kernel(LpArgs a)
     // kU loads in flight a thread; past the last vector, masked ones.
     constexpr uint32_t kMasked = F32 ? 0xff800000u : 0xff80ff80u;
 #pragma unroll 1
-    for (int v = sl.v0 + tid; v < sl.v1; v += kU * kT) {
+    for (int v = sl.v0 + tid; v < sl.v1; v += kU * T) {
         uint4 q[kU];
 #pragma unroll
         for (int i = 0; i < kU; ++i)
-            q[i] = v + i * kT < sl.v1 ? ld_stream_after(sl.vec + v + i * kT)
+            q[i] = v + i * T < sl.v1 ? ld_stream_after(sl.vec + v + i * T)
                                       : make_uint4(kMasked, kMasked, kMasked, kMasked);
 #pragma unroll
         for (int i = 0; i < kU; i += 2) take(q[i], q[i + 1]);
@@ -504,11 +510,11 @@ __global__ void __launch_bounds__(kT, 2) logprobs_kernel(LpArgs a)
             big = fmaxf(big, __shfl_xor_sync(kFull, big, o));
         }
     };
-    uint32_t half = mine;
+    uint32_t part = mine;
 #pragma unroll
-    for (int o = 8; o; o >>= 1) half = max(half, __shfl_xor_sync(kFull, half, o));
+    for (int o = T / 64; o; o >>= 1) part = max(part, __shfl_xor_sync(kFull, part, o));
     join_lanes(16);
-    if ((lane & 15) == 0) sh.half[2 * warp + (lane >> 4)] = half;
+    if (tid % (T / 32) == 0) sh.part_key[tid / (T / 32)] = part;
     if (lane == 0) {
         sh.sums[warp] = u;
         sh.count[warp] = count;
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(kT, 2) logprobs_kernel(LpArgs a)
             sh.total_big = big;
         }
     }
-    if (a.n_top > 0) slice_top<F32>(sh, sl, mine, a.n_top);
+    if (a.n_top > 0) slice_top<F32, T>(sh, sl, mine, a.n_top);
     __syncthreads();
     if (cs > 1) {
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -568,7 +574,7 @@ __global__ void __launch_bounds__(kT, 2) logprobs_kernel(LpArgs a)
         // A reference so large that the rounding of z c is no small shift of y any more, or no
         // logit above -1e30 / c: sums against the largest logit itself.
         float s = 0.0f, t = 0.0f;
-        for (int i = tid; i < a.V; i += kT) {
+        for (int i = tid; i < a.V; i += T) {
             const float z = Vec<F32>::at(sl.row, i);
             if (z == -INFINITY) continue;
             const float y = max_nan((z - big) * c, kFar), e = ex2(y);
@@ -622,7 +628,7 @@ bool allow_wide_clusters(const DeviceInfo* dev, const void* fn, bool f32)
     if (k == 0) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(kMaxCs);
-        cfg.blockDim = dim3(kT);
+        cfg.blockDim = dim3(kWide);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = kMaxCs;
@@ -664,13 +670,19 @@ dg_status launch_logprobs(const void* logits, bool f32, long long ld, const int6
     // CTAs per row: with few rows as many as two for each SM (one CTA alone is bound by its
     // instructions: 248320 logits take it 14 us), no slice below two vectors a thread; 16, which
     // has to lie in one GPC, where the rows are few enough for each to have one.
+    // Many short rows: at most 16 vectors a thread of a wide CTA with four rows for every SM, or 4
+    // with two (4096 x 8000: 85 us wide, 24 narrow; 304 x 65536: 11.0 and 15.8).
+    const int ve = f32 ? 4 : 8;
+    const bool narrow = V <= 16 * kWide * ve && M >= (V <= 4 * kWide * ve ? 2 : 4) * dev->sm_count;
     int cs = 1;
-    while (cs < kMaxCs && static_cast<long long>(M) * cs * 2 <= 2ll * dev->sm_count &&
-           V / (cs * 2) >= 2 * kT * (f32 ? 4 : 8) && (cs < 8 || M <= 4))
+    while (!narrow && cs < kMaxCs && static_cast<long long>(M) * cs * 2 <= 2ll * dev->sm_count &&
+           V / (cs * 2) >= 2 * kWide * ve && (cs < 8 || M <= 4))
         cs *= 2;
     a.cs = cs;
-    const void* fn = f32 ? reinterpret_cast<const void*>(&logprobs_kernel<true>)
-                         : reinterpret_cast<const void*>(&logprobs_kernel<false>);
+    const void* fn = narrow ? (f32 ? reinterpret_cast<const void*>(&logprobs_kernel<true, kNarrow>)
+                                   : reinterpret_cast<const void*>(&logprobs_kernel<false, kNarrow>))
+                            : (f32 ? reinterpret_cast<const void*>(&logprobs_kernel<true, kWide>)
+                                   : reinterpret_cast<const void*>(&logprobs_kernel<false, kWide>));
     if (cs > 8 && !allow_wide_clusters(dev, fn, f32)) {
         cs = 8;
         a.cs = cs;
@@ -678,7 +690,7 @@ dg_status launch_logprobs(const void* logits, bool f32, long long ld, const int6
     void* args[] = {&a};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(M) * cs));
-    cfg.blockDim = dim3(kT);
+    cfg.blockDim = dim3(narrow ? kNarrow : kWide);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

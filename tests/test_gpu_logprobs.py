@@ -75,6 +75,23 @@ def test_logprobs_many_rows_and_the_same_bits_again(cuda_device):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [5, 130, 4099, 30011])
+def test_logprobs_many_short_rows(cuda_device, dtype, V):
+    """Rows that take small thread blocks, equal values and masked rows among them."""
+    M = 310
+    x = _logits(M, V, V, dtype)
+    x[3] = 1.5
+    x[4, ::2] = -INF
+    x[5] = -INF
+    x[6] = torch.finfo(dtype).min
+    x[7, V // 2] = float("nan")
+    _check(x, _tokens(M, V, 3), n_top=min(V, 12))
+    one = dg.dg_logprobs(x[:9].contiguous(), n_top=min(V, 12))     # (a few rows take large ones)
+    many = dg.dg_logprobs(x, n_top=min(V, 12))
+    assert torch.equal(one["top_ids"], many["top_ids"][:9])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_logprobs_ties_and_orders(cuda_device, dtype):
     """Equal logits, sorted rows, the largest ones all in one thread's share, signed zeros."""
     V = 70000
