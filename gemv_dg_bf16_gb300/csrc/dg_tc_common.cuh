@@ -177,12 +177,16 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
             : "memory");
 }
 
-// One 512-byte scale tile (32 rows of 16 bytes, 8-row groups 128 bytes apart, no swizzle)
-// from shared memory to four tensor-memory columns, the same in every lane quarter.
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t smem)
+// Descriptor of a 512-byte scale tile (32 rows of 16 bytes, 8-row groups 128 bytes apart, no
+// swizzle), and its copy to four tensor-memory columns, the same in every lane quarter.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem)
 {
-    const uint64_t desc = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
-                          (static_cast<uint64_t>(1) << 46);
+    return static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) |
+           (static_cast<uint64_t>(1) << 46);
+}
+
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc)
+{
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 

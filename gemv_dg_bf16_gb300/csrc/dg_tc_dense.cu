@@ -480,6 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         pdl_wait();
         if (tc::elect_one()) {
+            const uint32_t ring = tc::su32(smem), xring = (A4 && !a.preq) ? tc::su32(xq) : ring + kXOff;
+            const uint64_t dw0 = tc::sw128_desc(ring), dx0 = tc::sw128_desc(xring);              // (A4)
+            const uint64_t dsw0 = tc::scale_desc(ring + kWBox), dsx0 = tc::scale_desc(xring + kXBox);
             int s = -1;
             uint32_t round = 0;
             for (int i = 0; i < nkb; ++i) {
@@ -508,29 +511,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if constexpr (A4) {
                     if (!a.preq && i == 0 && !tc::bar_wait(accf0, 0, abort_flag)) break;     // activations quantised
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t sw = wa + kWBox;
-                    const uint32_t xa = a.preq ? wa + kXOff : tc::su32(xq + static_cast<size_t>(i) * kXBlock);
-                    const uint32_t sx = xa + kXBox;
+                    // Descriptors count 16-byte units: a stage, a K-block or 64 elements further on
+                    // is an addition.
+                    const uint32_t ws = static_cast<uint32_t>(s * (kStage / 16));
+                    const uint32_t xs = a.preq ? ws : static_cast<uint32_t>(i * (kXBlock / 16));
+                    const uint64_t dw = dw0 + ws, dx = dx0 + xs, dsw = dsw0 + ws, dsx = dsx0 + xs;
                     const uint32_t cw = tmem + kSfw + (i & 1) * kSfCols;
                     const uint32_t cx = tmem + kSfx + (i & 1) * kSfCols;
                     const int kleft = a.K - (kb0 + i) * kA4Block;
-                    const int steps = kleft >= kA4Block ? kA4Block / 64 : (kleft + 63) / 64;      // 64 elements an MMA
                     constexpr int kPer = fp4::tile_k(NV) / 64;                                    // MMAs per scale tile
                     // tcgen05.cp and tcgen05.mma of one thread run in order
-#pragma unroll
-                    for (int j = 0; j < kSfTiles; ++j) {
-                        if (j * kPer >= steps) break;
-                        tc::copy_scales(cw + 4 * j, sw + j * fp4::kTileBytes);
-                        tc::copy_scales(cx + 4 * j, sx + j * fp4::kTileBytes);
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < kA4Block / 64; ++kk) {
-                        if (kk >= steps) break;
+                    auto scales = [&](int j) {
+                        tc::copy_scales(cw + 4 * j, dsw + j * (fp4::kTileBytes / 16));
+                        tc::copy_scales(cx + 4 * j, dsx + j * (fp4::kTileBytes / 16));
+                    };
+                    auto mma = [&](int kk) {
                         const int j = kk / kPer;
                         const uint32_t id = static_cast<uint32_t>(kk % kPer) * 2;                 // MX: byte pair 0 or 2
-                        tc::mma_fp4<NV>(tmem, tc::sw128_desc(wa + kk * 32), tc::sw128_desc(xa + kk * 32),
-                                        kIdesc | (id << 4) | (id << 29), cw + 4 * j, cx + 4 * j,
-                                        (i > 0 || kk > 0) ? 1u : 0u);
+                        tc::mma_fp4<NV>(tmem, dw + kk * 2, dx + kk * 2, kIdesc | (id << 4) | (id << 29), cw + 4 * j,
+                                        cx + 4 * j, (i > 0 || kk > 0) ? 1u : 0u);
+                    };
+                    if (kleft >= kA4Block) {           // straight: a test in front of each cost 0.1 us a block
+#pragma unroll
+                        for (int j = 0; j < kSfTiles; ++j) scales(j);
+#pragma unroll
+                        for (int kk = 0; kk < kA4Block / 64; ++kk) mma(kk);
+                    } else {
+                        const int steps = (kleft + 63) / 64;
+#pragma unroll 1
+                        for (int j = 0; j * kPer < steps; ++j) scales(j);
+#pragma unroll 1
+                        for (int kk = 0; kk < steps; ++kk) mma(kk);
                     }
                     tc::commit(empty0 + 8 * s);
                 } else {
