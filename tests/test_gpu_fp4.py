@@ -248,6 +248,24 @@ def test_linear_after_quantising_its_weights_and_in_a_graph(cuda_device):
         assert torch.equal(y.view(torch.int16), want[i].view(torch.int16))
 
 
+def test_linear_in_the_sweep_and_the_table(cuda_device, tmp_path):
+    """The sweep measures pipeline depths for either format, the table it writes drives the call, same bits."""
+    M, N, K = 16, 512, 1024
+    path = str(tmp_path / "t.json")
+    dg.dg_sweep([(dg.DG_OP_GEMV_A4W4, M, N, K, dg.DG_FP4_NV), (dg.DG_OP_GEMV_A4W4, 2, N, K, dg.DG_FP4_MX)], path, reps=3)
+    x = _x(M, K, 1)
+    Wq, sw, _, _ = _weights(N, K, dg.DG_FP4_NV, None, 2)
+    ref = dg.dg_gemv_a4w4_blockscale(x, Wq, sw, dg.DG_FP4_NV)
+    dg.dg_table_load(path)
+    try:
+        assert dg.dg_table_entries() == 2
+        assert dg.dg_select(dg.DG_OP_GEMV_A4W4, M, N, K).from_table == 1
+        y = dg.dg_gemv_a4w4_blockscale(x, Wq, sw, dg.DG_FP4_NV)
+    finally:
+        dg.dg_table_clear()
+    assert torch.equal(y.view(torch.int16), ref.view(torch.int16))
+
+
 def test_linear_refusals(cuda_device):
     Wq, sw, _, _ = _weights(64, 256, 1, None, 1)
     x = _x(2, 256, 1)
