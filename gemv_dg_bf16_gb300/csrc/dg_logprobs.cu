@@ -10,13 +10,11 @@
 // the n-th largest of the 32 parts' largest logits is a bound that at least n logits
 // reach, so only the threads whose own largest reaches it are looked at again, with all
 // threads of the CTA.
-// A row belongs to one CTA, or to a cluster of up to 16 when there are few rows; the others
+// A row belongs to one CTA, or to a cluster of up to 8 when there are few rows; the others
 // write their sums and lists into the first one's shared memory.  The largest, the count and the
 // lists do not depend on the split.
 // Bound: memory, 2 or 4 bytes a logit, with many rows; with few, the latency of one
 // CTA's slice and the joins.
-#include <mutex>
-
 #include "dg_common.cuh"
 #include "dg_internal.h"
 
@@ -27,7 +25,7 @@ namespace {
 // short rows take small CTAs, eight or more of them on an SM.
 constexpr int kWide = 512, kNarrow = 128;
 constexpr int kU = 8;                      // 16-byte loads in flight a thread (two wide CTAs an SM: 4: 184 us, 8: 173)
-constexpr int kMaxCs = 16;                 // CTAs of a row (more than 8: the non-portable size)
+constexpr int kMaxCs = 8;                  // CTAs of a row
 constexpr int kMaxTop = 32;
 
 constexpr int kCand = 1024;                // candidates held at once
@@ -401,6 +399,19 @@ __global__ void __launch_bounds__(T, 1024 / T) logprobs_kernel(LpArgs a)
     sl.tail = rank_in == cs - 1 ? a.V - sl.tail0 : 0;
     sl.n_single = sl.head + sl.tail;
 
+    // kU loads in flight a thread (past the last vector, masked ones), the first of them before
+    // the token's logit is looked up: that is two round trips.
+    constexpr uint32_t kMasked = F32 ? 0xff800000u : 0xff80ff80u;
+    uint4 q[kU];
+    auto load = [&](int v) {
+#pragma unroll
+        for (int i = 0; i < kU; ++i)
+            q[i] = v + i * T < sl.v1 ? ld_stream_after(sl.vec + v + i * T)
+                                     : make_uint4(kMasked, kMasked, kMasked, kMasked);
+    };
+    int at = sl.v0 + tid;
+    load(at);
+
     const long long tok = a.tokens ? a.tokens[m] : -1;
     const bool has_tok = tok >= 0 && tok < a.V;
     const float zt = has_tok ? Vec<F32>::at(sl.row, static_cast<int>(tok)) : INFINITY;
@@ -476,17 +487,12 @@ __global__ void __launch_bounds__(T, 1024 / T) logprobs_kernel(LpArgs a)
             }
         }
     };
-    // kU loads in flight a thread; past the last vector, masked ones.
-    constexpr uint32_t kMasked = F32 ? 0xff800000u : 0xff80ff80u;
-#pragma unroll 1
-    for (int v = sl.v0 + tid; v < sl.v1; v += kU * T) {
-        uint4 q[kU];
-#pragma unroll
-        for (int i = 0; i < kU; ++i)
-            q[i] = v + i * T < sl.v1 ? ld_stream_after(sl.vec + v + i * T)
-                                      : make_uint4(kMasked, kMasked, kMasked, kMasked);
+    for (;;) {
 #pragma unroll
         for (int i = 0; i < kU; i += 2) take(q[i], q[i + 1]);
+        at += kU * T;
+        if (at >= sl.v1) break;
+        load(at);
     }
     if constexpr (!F32) {
         const int lo = static_cast<int>((0u - masks) & 0xffffu);
@@ -617,34 +623,6 @@ __global__ void __launch_bounds__(T, 1024 / T) logprobs_kernel(LpArgs a)
     }
 }
 
-// Whether the device holds a cluster of 16 of these CTAs (asked once per device and type, which
-// also allows the size).
-bool allow_wide_clusters(const DeviceInfo* dev, const void* fn, bool f32)
-{
-    static std::mutex mu;
-    static int known[64][2];
-    std::lock_guard<std::mutex> lk(mu);
-    int& k = known[dev->device][f32 ? 1 : 0];
-    if (k == 0) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(kMaxCs);
-        cfg.blockDim = dim3(kWide);
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = kMaxCs;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        const bool ok = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0;
-        cudaGetLastError();
-        k = ok ? 1 : -1;
-    }
-    return k > 0;
-}
-
 }  // namespace
 
 dg_status launch_logprobs(const void* logits, bool f32, long long ld, const int64_t* tokens, float scale, int n_top,
@@ -668,25 +646,21 @@ dg_status launch_logprobs(const void* logits, bool f32, long long ld, const int6
     a.M = M;
     a.V = V;
     // CTAs per row: with few rows as many as two for each SM (one CTA alone is bound by its
-    // instructions: 248320 logits take it 14 us), no slice below two vectors a thread; 16, which
-    // has to lie in one GPC, where the rows are few enough for each to have one.
+    // instructions: 248320 logits take it 11 us), but no slice below six vectors a thread, which
+    // one round of loads brings (a cluster's join costs about 1.5 us).
     // Many short rows: at most 16 vectors a thread of a wide CTA with four rows for every SM, or 4
     // with two (4096 x 8000: 85 us wide, 24 narrow; 304 x 65536: 11.0 and 15.8).
     const int ve = f32 ? 4 : 8;
     const bool narrow = V <= 16 * kWide * ve && M >= (V <= 4 * kWide * ve ? 2 : 4) * dev->sm_count;
     int cs = 1;
     while (!narrow && cs < kMaxCs && static_cast<long long>(M) * cs * 2 <= 2ll * dev->sm_count &&
-           V / (cs * 2) >= 2 * kWide * ve && (cs < 8 || M <= 4))
+           V / (cs * 2) >= 6 * kWide * ve)
         cs *= 2;
     a.cs = cs;
     const void* fn = narrow ? (f32 ? reinterpret_cast<const void*>(&logprobs_kernel<true, kNarrow>)
                                    : reinterpret_cast<const void*>(&logprobs_kernel<false, kNarrow>))
                             : (f32 ? reinterpret_cast<const void*>(&logprobs_kernel<true, kWide>)
                                    : reinterpret_cast<const void*>(&logprobs_kernel<false, kWide>));
-    if (cs > 8 && !allow_wide_clusters(dev, fn, f32)) {
-        cs = 8;
-        a.cs = cs;
-    }
     void* args[] = {&a};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(M) * cs));
