@@ -777,10 +777,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else
                         tc::tmem_ld32(at, v);
                     const int left = n < a.N ? rows_here - c : 0;
+                    if (left >= kC) {
 #pragma unroll
-                    for (int j = 0; j < kC; ++j) {
-                        if (j < left) *dst = f32_to_bf16_bits(__uint_as_float(v[j]) * alpha);
-                        dst += a.ld_out;
+                        for (int j = 0; j < kC; ++j)
+                            dst[static_cast<size_t>(c + j) * a.ld_out] = f32_to_bf16_bits(__uint_as_float(v[j]) * alpha);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kC; ++j)
+                            if (j < left)
+                                dst[static_cast<size_t>(c + j) * a.ld_out] =
+                                    f32_to_bf16_bits(__uint_as_float(v[j]) * alpha);
                     }
                 }
             }
