@@ -137,12 +137,13 @@ __global__ void __launch_bounds__(kWarps * 32) fp4_dequant_kernel(const uint8_t*
             else
                 f = sb == 0xffu ? __uint_as_float(0x7fffffffu) : fp4::pow2(static_cast<int>(sb) - 127);
             f = __fmul_rn(f, g);
+            float v[8];
+            fp4::from_e2m1x8(codes[i], v);
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 v = fp4::from_e2m1x2(codes[i], j);
-                w[j] = f32_to_bf16_bits(__fmul_rn(v.x, f)) |
-                       (static_cast<uint32_t>(f32_to_bf16_bits(__fmul_rn(v.y, f))) << 16);
+                const __nv_bfloat162 p = __floats2bfloat162_rn(__fmul_rn(v[2 * j], f), __fmul_rn(v[2 * j + 1], f));
+                memcpy(&w[j], &p, sizeof w[j]);
             }
             *reinterpret_cast<uint4*>(y + static_cast<size_t>(row) * K + k) = make_uint4(w[0], w[1], w[2], w[3]);
         }

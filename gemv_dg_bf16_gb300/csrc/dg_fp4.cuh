@@ -125,18 +125,26 @@ __device__ __forceinline__ uint32_t encode8(float (&v)[8], const Scale& s)
     return s.live ? c : 0u;
 }
 
-// Two codes of byte j of `codes` -> fp32 (exact).
-__device__ __forceinline__ float2 from_e2m1x2(uint32_t codes, int j)
+// Eight codes -> fp32 (exact).
+__device__ __forceinline__ void from_e2m1x8(uint32_t codes, float (&v)[8])
 {
-    uint32_t h2;
-    asm("{\n\t.reg .b8 b;\n\t"
-        "cvt.u8.u32 b, %1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
-        : "=r"(h2)
-        : "r"((codes >> (8 * j)) & 0xffu));
-    __half2 h;
-    memcpy(&h, &h2, sizeof h);
-    return __half22float2(h);
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        __half2 p;
+        memcpy(&p, &h[j], sizeof p);
+        const float2 f = __half22float2(p);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+    }
 }
 
 // Eight bf16 values of one 16-byte load as fp32.
