@@ -1,7 +1,7 @@
 // dg_tc_dense.cu -- tcgen05 tensor-core family (DG_VAR_TC) for the bf16 linear and
 // the fused gate/up + SiLU.mul (the default from 13 token rows up for the linear and
-// from 9 for gate/up, where the tile is a real dense contraction), and the A8W8
-// block-scaled linear.
+// from 9 for gate/up, where the tile is a real dense contraction), the A8W8
+// block-scaled linear and the A4W4 linear on microscaled 4-bit operands.
 //
 // Swap-AB: a CTA owns a tile of 128 weight rows (the MMA's M) and one fixed K
 // range; the tokens are the MMA's N (M padded to MP in {16, 32, 64, 128, 256};
@@ -9,7 +9,7 @@
 // D[128, MP] = W_tile[128, Kr] . x[MP, Kr]^T accumulates in TMEM (fp32).
 //   warp 0      TMA producer: 128x64 weight box + MPx64 activation box per stage
 //               (128-byte swizzle), into a ring of `stages` shared-memory slots
-//   warp 1      allocates TMEM; lane 0 issues tcgen05.mma (4 x K=16 per stage),
+//   warp 1      allocates TMEM; one elected lane issues tcgen05.mma (4 x K=16 per stage),
 //               commits each stage back to its "empty" barrier and the last one
 //               to the accumulator barrier
 //   warps 2..5  epilogue: tcgen05.ld the accumulator (warp w reads TMEM lanes
@@ -25,6 +25,15 @@
 // parks its partial tile in its own shared memory and, after a cluster barrier,
 // the folding ranks read them through distributed shared memory.  Pipeline depth
 // and the fold's transport change no bits.
+// A4W4 (EPI 3, 4) differs in three places.  A stage holds 256 K elements as e2m1 codes and
+// their block scales, which tcgen05.cp takes to TMEM for the block-scaled MMA
+// (kind::mxf4 / kind::mxf4nvf4, 64 elements each): y = sum (qx sx)(qw sw) needs no scaling
+// of ours but the tensor scales' product.  Tokens are cut into groups of up to 128, a CTA
+// (or cluster) each, by a model (a4_plan).  Outputs leave TMEM straight to memory, and a
+// K-split's ranks fold tokens, not rows.  Bound: up to some 32 rows the fixed chain (launch,
+// first load, fold: 4.9 us for 1 x 4096 x 4096, of whose 9.4 MB the bytes need 1.4); with
+// many rows the bytes that an SM takes in, 36 KB a K-block and 128 x 128 outputs (512 x
+// 24576 x 4096: 36 us, 96 GB/s an SM on average).
 // Every mbarrier wait is bounded: on timeout the kernel flags
 // DG_DEVERR_WAIT_TIMEOUT in the workspace status word and winds down.
 #include <cuda.h>
@@ -1407,16 +1416,17 @@ struct A4Plan {
     int tg, ns;
 };
 
-// The cheapest cut by a model of what a CTA does, in units of 10 ns, measured on GB300 (graphs of
-// calls, 1 to 512 rows over 14 weight shapes; the cut it takes is within 0.4 % of the best one on
-// average, 4 % at worst): 33 a K-block of 256 elements, whatever the token group (issue and
-// scale copies, not bytes, set the pace); kEnd the epilogue of a group; with a K-split the
-// fold, kFold + kFoldRank per rank (partials through distributed shared memory at about 25
-// GB/s a CTA).  One wave: at most 264 of the 304 CTA slots -- fuller grids leave no room for
-// the next launch's CTAs to start under this one's tail (12288 x 4096 at 16 rows: 192 CTAs
-// 7.6 us, 288 9.8).  Few rows take few, small groups and a K-split; many rows split tokens
-// instead, and the tile's weights come from L2 to each group (128 x 4096 x 4096: one group of
-// 128 and 4 ranks 12.1 us, 4 groups of 32 and 2 ranks 9.6).
+// The cheapest cut by a model of what a CTA does, in units of about 10 ns, fitted on GB300 to
+// graphs of calls of 1 to 512 rows over 20 weight shapes and every cut (the one it takes is
+// within 0.3 % of the best on average, 5 % at worst; any K-block cost from 25 to 33 picks the
+// same): 33 a K-block of 256 elements, whatever the token group (issue and scale copies, not
+// bytes, set a CTA's pace); kEnd the epilogue of a group; with a K-split the fold, kFold +
+// kFoldRank per rank (partials through distributed shared memory at about 25 GB/s a CTA).
+// One wave: at most 263 of the 304 CTA slots -- fuller grids leave no room for the next
+// launch's CTAs to start under this one's tail (12288 x 4096 at 16 rows: 192 CTAs 7.3 us, 288
+// 8.6).  Few rows take few, small groups and a K-split; many rows split tokens instead, and
+// the tile's weights come from L2 to each group (128 x 4096 x 4096: one group of 128 and 4
+// ranks 11.9 us, 4 groups of 32 and 2 ranks 9.0).
 static A4Plan a4_plan(const DeviceInfo* dev, int N, int K, int M, bool fixed)
 {
     constexpr int kTg[4] = {16, 32, 64, 128};
@@ -1475,9 +1485,9 @@ size_t smem_bytes_a4(int mp, bool nv, int stages, size_t recv, int xq_blocks)
 }
 
 // The linear's own CTAs quantise the activations where a rank has at most this many
-// (row, K-block) pieces: every row tile repeats the work, about 0.14 us a piece and warp, against
-// a launch of its own (4096 x 4096, us fused / apart: 1 row 5.1 / 6.1, 4 rows 6.2 / 6.2, 8 rows
-// 8.1 / 6.6; 12288 x 4096, twice the K-blocks a rank: 4 rows 9.7 / 8.1).
+// (row, K-block) pieces: every row tile repeats the work, against a launch of its own (4096 x
+// 4096, us fused / apart: 1 row 4.9 / 5.8, 4 rows 5.8 / 5.8, 8 rows 7.5 / 6.3; 12288 x 4096,
+// twice the K-blocks a rank: 4 rows 9.1 / 7.8).
 constexpr int kA4FusePieces = 16;
 
 }  // namespace
