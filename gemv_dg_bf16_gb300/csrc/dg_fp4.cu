@@ -8,7 +8,7 @@
 // No shared memory and no barrier: every row's loads are in flight before the first is used.
 // Bound: memory, 2 + 1/2 + 1/16 (or 1/32) bytes an element and direction.  24576 x 4096 in MX:
 // there 50 us and back 39, of 37.5 for the bytes each; 105 and 71 instructions for 8 elements,
-// the former's conversions keeping the ALU two thirds busy.  16 x 4096 there and back: 3.2 us.
+// the former's conversions keeping the ALU two thirds busy.  16 x 4096 there and back: 3.4 us.
 #include "dg_fp4.cuh"
 #include "dg_internal.h"
 

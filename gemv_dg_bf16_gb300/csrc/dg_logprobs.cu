@@ -13,10 +13,10 @@
 // A row belongs to one CTA, or to a cluster of up to 8 when there are few rows; the others
 // write their sums and lists into the first one's shared memory.  The largest, the count and the
 // lists do not depend on the split.
-// Bound: with many rows memory, 2 or 4 bytes a logit (2048 x 248320 bf16: 175 us, 5.8 TB/s, 86 %
-// of the copy rate; 66 % of the issue slots, 8.7 instructions a logit); with few, a chain of
-// latencies: launch, two round trips of loads, four block barriers, the cluster's join (one
-// row of 248320: 7.5 us).
+// Bound: with many rows memory, 2 or 4 bytes a logit (2048 x 248320 bf16: 176 us, 5.8 TB/s, 85 %
+// of the copy rate; 66 % of the issue slots, 8.7 instructions a logit); with few, latencies
+// one after the other -- loads, the bound, the gathering, the cluster's join (one row of
+// 248320: 7.5 us).
 #include "dg_common.cuh"
 #include "dg_internal.h"
 

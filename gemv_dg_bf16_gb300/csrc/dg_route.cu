@@ -9,13 +9,12 @@
 //
 // Up to 8 experts a lane, each lane sorts its keys (a network of maxima and minima), and a pick
 // is one warp maximum over the lanes' heads, a ballot for the lowest lane that holds it, and a
-// shift in that lane; which expert each pick was is looked up at the end for all slots at once.  A group's best one or two are the heads of its lanes, merged by shuffles.  Warps
-// walk over the tokens with the next token's logits already on the way and the bias in
-// registers.  Bound: instructions, 733 a token of 256 experts with 8 groups and 8 picks (some
-// 180 for the scores, 28 a pick) where memory would be 1 KB a token: 32768 tokens take 30 us
-// at 67 % of the issue slots, 5 us of bytes.  With one expert in 32 to a lane and the groups
-// one after the other it was 1119 instructions and 74 us; a token alone takes 2.8 us, of which
-// the launch is about 2.
+// shift in that lane; which expert each pick was is looked up at the end for all slots at
+// once.  A group's best one or two are the heads of its lanes, merged by shuffles.  Warps walk
+// over the tokens with the next token's logits already on the way and the bias in registers.  Bound: instructions, 733 a token of 256 experts with 8 groups and 8 picks (28
+// of them a pick) where memory would be 1 KB a token: 32768 tokens take 30 us at 67 % of the
+// issue slots, 5 us of bytes.  With one expert in 32 to a lane and the groups one after the
+// other it took 74 us.  A token alone takes 2.8 us.
 #include "dg_common.cuh"
 #include "dg_internal.h"
 

@@ -32,8 +32,9 @@
 // (or cluster) each, by a model (a4_plan).  Outputs leave TMEM straight to memory, and a
 // K-split's ranks fold tokens, not rows.  Bound: up to some 32 rows the fixed chain (launch,
 // first load, fold: 4.9 us for 1 x 4096 x 4096, of whose 9.4 MB the bytes need 1.4); with
-// many rows the bytes that an SM takes in, 36 KB a K-block and 128 x 128 outputs (512 x
-// 24576 x 4096: 36 us, 96 GB/s an SM on average).
+// many rows neither memory nor the MMAs (512 x 24576 x 4096: 36 us, DRAM 20 %, tensor pipe
+// 38 %) but, as far as the counters tell, the 36 KB that a K-block of 128 x 128 outputs brings
+// into an SM (82 GB/s an SM on average).
 // Every mbarrier wait is bounded: on timeout the kernel flags
 // DG_DEVERR_WAIT_TIMEOUT in the workspace status word and winds down.
 #include <cuda.h>
@@ -1417,10 +1418,9 @@ struct A4Plan {
 };
 
 // The cheapest cut by a model of what a CTA does, in units of about 10 ns, fitted on GB300 to
-// graphs of calls of 1 to 512 rows over 20 weight shapes and every cut (the one it takes is
-// within 0.3 % of the best on average, 5 % at worst; any K-block cost from 25 to 33 picks the
-// same): 33 a K-block of 256 elements, whatever the token group (issue and scale copies, not
-// bytes, set a CTA's pace); kEnd the epilogue of a group; with a K-split the fold, kFold +
+// graphs of calls of 1 to 512 rows over 16 weight shapes (44 cases: the one it takes is within
+// 0.4 % of the best on average, 8 % at worst): 33 a K-block of 256 elements, whatever the token
+// group (issue and scale copies, not bytes, set a CTA's pace); kEnd the epilogue of a group; with a K-split the fold, kFold +
 // kFoldRank per rank (partials through distributed shared memory at about 25 GB/s a CTA).
 // One wave: at most 263 of the 304 CTA slots -- fuller grids leave no room for the next
 // launch's CTAs to start under this one's tail (12288 x 4096 at 16 rows: 192 CTAs 7.3 us, 288
@@ -1486,8 +1486,8 @@ size_t smem_bytes_a4(int mp, bool nv, int stages, size_t recv, int xq_blocks)
 
 // The linear's own CTAs quantise the activations where a rank has at most this many
 // (row, K-block) pieces: every row tile repeats the work, against a launch of its own (4096 x
-// 4096, us fused / apart: 1 row 4.9 / 5.8, 4 rows 5.8 / 5.8, 8 rows 7.5 / 6.3; 12288 x 4096,
-// twice the K-blocks a rank: 4 rows 9.1 / 7.8).
+// 4096, us fused / apart: 1 row 4.7 / 5.8, 4 rows 5.7 / 5.7, 8 rows 7.6 / 6.3, 16 rows 10.3 /
+// 6.1; 12288 x 4096, twice the K-blocks a rank: 1 row 6.9 / 7.7, 4 rows 9.2 / 7.8).
 constexpr int kA4FusePieces = 16;
 
 }  // namespace
