@@ -15,6 +15,8 @@
 // of them a pick) where memory would be 1 KB a token: 32768 tokens take 30 us at 67 % of the
 // issue slots, 5 us of bytes.  With one expert in 32 to a lane and the groups one after the
 // other it took 74 us.  A token alone takes 2.8 us.
+#include <cfloat>
+
 #include "dg_common.cuh"
 #include "dg_internal.h"
 
@@ -62,6 +64,13 @@ __device__ __forceinline__ float recip_rn(float y)
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
     return __fmaf_rn(r, __fmaf_rn(-y, r, 1.0f), r);
+}
+
+// Score of a group of experts from its best two keys (-inf: no such key).  A sum below the type's
+// range stays above -inf, which marks groups that hold no key and groups already taken.
+__device__ __forceinline__ float group_score(float b1, float b2, int group_top)
+{
+    return group_top == 2 && b2 > -INFINITY ? fmaxf(__fadd_rn(b1, b2), -FLT_MAX) : b1;
 }
 
 template <bool F32>
@@ -225,7 +234,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
                     b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
                     b1 = fmaxf(b1, c1);
                 }
-                gs = a.group_top == 2 && b2 > -INFINITY ? __fadd_rn(b1, b2) : b1;
+                gs = group_score(b1, b2, a.group_top);
                 const int own = lane >> a.group_shift;
                 bool keep = false;
                 for (int g = 0; g < a.topk_group; ++g) {
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
                     const float t1 = warp_max(b1);
                     const unsigned who = __ballot_sync(kFull, b1 == t1);
                     const float t2 = warp_max(lane == __ffs(who) - 1 ? b2 : b1);
-                    if (lane == g) gs = a.group_top == 2 && t2 > -INFINITY ? __fadd_rn(t1, t2) : t1;
+                    if (lane == g) gs = group_score(t1, t2, a.group_top);
                 }
                 int rank = 0;
                 for (int g = 0; g < a.n_group; ++g) {
