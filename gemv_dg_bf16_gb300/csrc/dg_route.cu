@@ -140,10 +140,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
     const long long step = static_cast<long long>(gridDim.x) * kWarps;
     long long row = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     if (row >= a.M) return;
-    float bias[R];
+    float bias[R];                         // NaN: no key; at most FLT_MAX, as -inf and +inf would make a NaN key
     if (a.bias)
 #pragma unroll
-        for (int j = 0; j < R; ++j) bias[j] = lane * R + j < a.E ? fminf(fmaxf(a.bias[lane * R + j], -INFINITY), 3.0e38f) : 0.0f;  // NaN: no key
+        for (int j = 0; j < R; ++j)
+            bias[j] = lane * R + j < a.E ? fminf(fmaxf(a.bias[lane * R + j], -INFINITY), FLT_MAX) : 0.0f;
     float next[R];
     load_row<R, F32>(a, row, lane, next);
     for (; row < a.M; row += step) {

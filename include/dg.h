@@ -404,7 +404,9 @@ dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw,
  *   p[e]   = 1 / (1 + exp(-x[e]))                                DG_SCORE_SIGMOID
  *          = exp(x[e] - max x) / sum exp(x - max x)              DG_SCORE_SOFTMAX
  *   key[e] = p[e] + bias[e]       (bias NULL: p[e]); experts whose logit is -inf or NaN have
- *            no key: they are never picked and add nothing to the sum
+ *            no key: they are never picked and add nothing to the sum; neither have those
+ *            whose bias is -inf or NaN, which do add to the sum (+inf counts as the type's
+ *            largest value)
  *   with n_group > 1 the experts are n_group equal runs; a run's score is its largest key
  *            (group_top 1) or the sum of its two largest (group_top 2; of one if it has one; a
  *            sum below the type's range is the type's lowest value), and only the topk_group
