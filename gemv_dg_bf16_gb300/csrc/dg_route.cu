@@ -55,7 +55,7 @@ __device__ __forceinline__ float warp_max(float v)
     return r;
 }
 
-// 1 / y, correctly rounded, for 1 <= y < 2^125: one Newton step in fused operations on a
+// 1 / y, correctly rounded, for 2^-60 <= y < 2^125: one Newton step in fused operations on a
 // reciprocal within an ulp (P. W. Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000 processor", 1990).  Equal to __frcp_rn(y) for every mantissa, at exponents
 // 0, 1, 3, 23, 73, 113, 124 and 125.
@@ -64,6 +64,14 @@ __device__ __forceinline__ float recip_rn(float y)
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
     return __fmaf_rn(r, __fmaf_rn(-y, r, 1.0f), r);
+}
+
+// e / y, correctly rounded, from r = recip_rn(y) (the same method), for e = 0 or e >= 2^-90 (no
+// remainder is subnormal) with a quotient of at most 2^60.
+__device__ __forceinline__ float quotient_rn(float e, float y, float r)
+{
+    const float q = __fmul_rn(e, r);
+    return __fmaf_rn(__fmaf_rn(-q, y, e), r, q);
 }
 
 // Score of a group of experts from its best two keys (-inf: no such key).  A sum below the type's
@@ -195,15 +203,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
                     if (x[j] > -INFINITY) key[j] = __frcp_rn(__fadd_rn(1.0f, expf(-x[j])));
             }
         } else {
-            // e / sum: the correctly rounded quotient from the correctly rounded reciprocal (the
-            // same method) where no remainder can be subnormal
             const float r = recip_rn(sum);
             float low = 1.0f;
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                const float e = key[j] > -INFINITY ? key[j] : 1.0f, q = __fmul_rn(e, r);
+                const float e = key[j] > -INFINITY ? key[j] : 1.0f;
                 low = fminf(low, e);
-                const float p = __fmaf_rn(__fmaf_rn(-q, sum, e), r, q);
+                const float p = quotient_rn(e, sum, r);
                 key[j] = key[j] > -INFINITY ? p : -INFINITY;
             }
             if (low < 0x1p-90f) {
@@ -345,8 +351,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
             float t = wv;
 #pragma unroll
             for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
-            // (a reciprocal within an ulp where neither it nor the sum is subnormal)
-            wv = t > 0x1p-100f ? __fdividef(wv, t) : t > 0.0f ? __fdiv_rn(wv, t) : 0.0f;
+            if (t < 0x1p-60f || (wv > 0.0f && wv < 0x1p-90f)) {    // where quotient_rn is not exact
+                wv = t > 0.0f ? __fdiv_rn(wv, t) : 0.0f;
+            } else {
+                wv = quotient_rn(wv, t, recip_rn(t));
+            }
         }
         if (lane < a.topk) {
             a.ids[row * a.topk + lane] = id;

@@ -413,7 +413,9 @@ dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw,
  *            best runs that hold a key keep their keys
  *   ids    = the topk largest keys in descending order; equal keys (and equal runs) go to the
  *            lower index; a slot that finds none holds -1 with weight 0
- *   w      = p[ids], divided by their sum if renorm (0 where the sum is 0), times scale
+ *   w      = p[ids], divided by their sum if renorm (0 where the sum is 0), times scale; the
+ *            sum in binary32 over 32 slots (p = 0 past topk): slot s takes slot s ^ 16's value
+ *            to its own, then s ^ 8's, 4, 2, 1
  * logits [M, E] (ld), bias [E] fp32 or NULL, ids [M, topk] int32, w [M, topk] fp32.
  * M >= 1, 1 <= E <= 1024, 1 <= topk <= 32 and topk <= topk_group * E / n_group,
  * 1 <= n_group <= 32 dividing E, 1 <= topk_group <= n_group. */
