@@ -18,7 +18,7 @@ from ._binding import (  # noqa: F401
     dg_head_fp8_argmax_noalloc, dg_head_fp8_argmax_noalloc_status, dg_head_fp8_argmax_noalloc_scratch,
     dg_init, dg_launch_flags, dg_moe_w1_silu, dg_set_launch_flags, DG_LAUNCH_PDL,
     dg_set_numerics, dg_numerics, DG_NUMERICS_FASTEST, DG_NUMERICS_BATCH_INVARIANT, dg_moe_w2, dg_select,
-    dg_selection_space, dg_selftest_wait_timeout, dg_moe_route_debug, DG_ROUTE_DEBUG_INTS, dg_status_str,
+    dg_selection_space, dg_selftest_wait_timeout, dg_selftest_route_division, dg_moe_route_debug, DG_ROUTE_DEBUG_INTS, dg_status_str,
     dg_sweep,
     dg_table_check, dg_table_clear, dg_table_entries, dg_table_load, dg_workspace_bytes, lib,
     library_path, workspace,

@@ -98,6 +98,8 @@ def lib():
     L.dg_device_status_clear.argtypes = [P, P]
     L.dg_selftest_wait_timeout.argtypes = [P, I, P]
     L.dg_selftest_wait_timeout.restype = S
+    L.dg_selftest_route_division.argtypes = [P, P, P, P, I, P]
+    L.dg_selftest_route_division.restype = S
     L.dg_moe_route_debug.argtypes = [P, I, I, I, P, P, P]
     L.dg_moe_route_debug.restype = S
     L.dg_set_launch_flags.argtypes = [ctypes.c_uint]
@@ -233,6 +235,19 @@ def dg_selftest_wait_timeout(ws, timeout_us: int = 20000, stream=None):
 
 
 DG_ROUTE_DEBUG_INTS = 2 + 128 + 16 + 128 + 129 + 128 + 128
+
+
+def dg_selftest_route_division(e, y, stream=None):
+    """(1 / y, e / y) as dg_moe_route divides, of two fp32 device tensors of one shape."""
+    for t, name in ((e, "e"), (y, "y")):
+        _expect(t, name, torch.float32)
+    _check_dev(e, y)
+    if e.shape != y.shape:
+        raise ValueError(f"e: shape {tuple(e.shape)}, y: {tuple(y.shape)}")
+    recip, quot = torch.empty_like(y), torch.empty_like(y)
+    _ok(lib().dg_selftest_route_division(_ptr(e), _ptr(y), _ptr(recip), _ptr(quot), y.numel(), _stream(stream)),
+        "dg_selftest_route_division")
+    return recip, quot
 
 
 def dg_moe_route_debug(topk_ids, E: int, ws=None, stream=None) -> dict:

@@ -19,9 +19,13 @@
 
 #include "dg_common.cuh"
 #include "dg_internal.h"
+#include "dg_route.cuh"
 
 namespace dg {
 namespace {
+
+using route::quotient_rn;
+using route::recip_rn;
 
 constexpr int kWarps = 4;
 
@@ -53,25 +57,6 @@ __device__ __forceinline__ float warp_max(float v)
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
-}
-
-// 1 / y, correctly rounded, for 2^-60 <= y < 2^125: one Newton step in fused operations on a
-// reciprocal within an ulp (P. W. Markstein, "Computation of elementary functions on the IBM
-// RISC System/6000 processor", 1990).  Equal to __frcp_rn(y) for every mantissa, at exponents
-// 0, 1, 3, 23, 73, 113, 124 and 125.
-__device__ __forceinline__ float recip_rn(float y)
-{
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
-    return __fmaf_rn(r, __fmaf_rn(-y, r, 1.0f), r);
-}
-
-// e / y, correctly rounded, from r = recip_rn(y) (the same method), for e = 0 or e >= 2^-90 (no
-// remainder is subnormal) with a quotient of at most 2^60.
-__device__ __forceinline__ float quotient_rn(float e, float y, float r)
-{
-    const float q = __fmul_rn(e, r);
-    return __fmaf_rn(__fmaf_rn(-q, y, e), r, q);
 }
 
 // Score of a group of experts from its best two keys (-inf: no such key).  A sum below the type's
@@ -212,7 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
                 const float p = quotient_rn(e, sum, r);
                 key[j] = key[j] > -INFINITY ? p : -INFINITY;
             }
-            if (low < 0x1p-90f) {
+            if (low < route::kLeastE) {
                 float x[R];
                 load_row<R, F32>(a, row, lane, x);
 #pragma unroll
@@ -351,7 +336,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
             float t = wv;
 #pragma unroll
             for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
-            if (t < 0x1p-60f || (wv > 0.0f && wv < 0x1p-90f)) {    // where quotient_rn is not exact
+            if (t < route::kLeastY || (wv > 0.0f && wv < route::kLeastE)) {    // where quotient_rn is not exact
                 wv = t > 0.0f ? __fdiv_rn(wv, t) : 0.0f;
             } else {
                 wv = quotient_rn(wv, t, recip_rn(t));

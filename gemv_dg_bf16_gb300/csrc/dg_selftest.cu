@@ -4,9 +4,11 @@
 //    `timeout_us`, and reports DG_DEVERR_WAIT_TIMEOUT through the workspace status
 //    word, leaving the context usable;
 //  * an export of the MoE routing tables, computed by the same routing scan the
-//    MoE kernels run, so that they can be compared bit for bit with the oracle.
+//    MoE kernels run, so that they can be compared bit for bit with the oracle;
+//  * the division of dg_moe_route on its own, to be compared with correct rounding.
 #include "dg_internal.h"
 #include "dg_moe.cuh"
+#include "dg_route.cuh"
 #include "dg_tc_common.cuh"
 
 namespace dg {
@@ -87,6 +89,40 @@ extern "C" dg_status dg_moe_route_debug(const int32_t* topk_ids, int M, int topk
     if (!dg::current_device(&s)) return s;
     dg::route_debug_kernel<<<1, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(topk_ids, M, topk, E, out,
                                                                                   static_cast<uint8_t*>(ws));
+    if (cudaGetLastError() != cudaSuccess) return DG_ERR_CUDA;
+    return DG_OK;
+}
+
+// ------------------------------------------------------------------ routing division
+
+namespace dg {
+namespace {
+
+__global__ void route_division_kernel(const float* e, const float* y, float* recip, float* quot, int n)
+{
+    for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < n;
+         i += static_cast<long long>(gridDim.x) * blockDim.x) {
+        const float r = route::recip_rn(y[i]);
+        recip[i] = r;
+        quot[i] = route::quotient_rn(e[i], y[i], r);
+    }
+}
+
+}  // namespace
+}  // namespace dg
+
+extern "C" dg_status dg_selftest_route_division(const float* e, const float* y, float* recip, float* quot, int n,
+                                                dg_stream_t stream)
+{
+    if (!e || !y || !recip || !quot || n < 1) return DG_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(e) | reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(recip) |
+         reinterpret_cast<uintptr_t>(quot)) & 3u)
+        return DG_ERR_ALIGNMENT;
+    dg_status s;
+    if (!dg::current_device(&s)) return s;
+    const int blocks = n / 256 + 1;
+    dg::route_division_kernel<<<blocks < 1024 ? blocks : 1024, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        e, y, recip, quot, n);
     if (cudaGetLastError() != cudaSuccess) return DG_ERR_CUDA;
     return DG_OK;
 }

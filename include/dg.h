@@ -229,6 +229,13 @@ dg_status dg_selftest_wait_timeout(void* ws, int timeout_us, dg_stream_t stream)
 dg_status dg_moe_route_debug(const int32_t* topk_ids, int M, int topk, int E, int32_t* out, void* ws,
                              dg_stream_t stream);
 
+/* Test hook: the division that dg_moe_route uses (no counterpart on the pages), on its own.
+ * recip[i] = 1 / y[i] and quot[i] = e[i] / y[i], both correctly rounded for
+ * 2^-60 <= y < 2^125, e = 0 or e >= 2^-90, and a quotient of at most 2^60.  n values each,
+ * device fp32; asynchronous on `stream`. */
+dg_status dg_selftest_route_division(const float* e, const float* y, float* recip, float* quot, int n,
+                                     dg_stream_t stream);
+
 /* ---------------------------------------------------------------- compute */
 
 /* Decode linear, mstar PR #1104 (decode GEMM table), "Why" / "What changed":
