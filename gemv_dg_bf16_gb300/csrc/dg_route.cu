@@ -4,8 +4,8 @@
 // registers, so a lower lane is a lower index and a group of experts is a run of lanes.  The
 // pick compares scores (plus the bias) in binary32, so that it is defined to the last bit:
 // sigmoid as 1 / (1 + expf(-x)), softmax as expf(x - max) / sum with the sum compensated
-// (Knuth's two-sum), which rounds it as the exact sum in all but about 2^-20 of cases whatever
-// the order -- the same pick for any arrangement of lanes.
+// (Knuth's two-sum), which rounds it as the exact sum whatever the order, the exact sum's own
+// ties included; only a sum within about 2^-43 of a tie from below may go up instead.
 //
 // Up to 8 experts a lane, each lane sorts its keys (a network of maxima and minima), and a pick
 // is one warp maximum over the lanes' heads, a ballot for the lowest lane that holds it, and a
@@ -43,12 +43,13 @@ struct RouteArgs {
     float scale;
 };
 
-// s + e += v, exactly up to the rounding of e.
+// s + e += v, exactly but for the rounding of e, upwards: of a sum next to a tie between two floats
+// a trace of further terms (all are positive) stays on the right side, however small.
 __device__ __forceinline__ void two_sum(float& s, float& e, float v)
 {
     const float t = __fadd_rn(s, v);
     const float z = __fsub_rn(t, s);
-    e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(v, z)));
+    e = __fadd_ru(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(v, z)));
     s = t;
 }
 
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
             for (int o = 16; o; o >>= 1) {
                 const float s2 = __shfl_xor_sync(kFull, s, o), e2 = __shfl_xor_sync(kFull, e, o);
                 two_sum(s, e, s2);
-                e = __fadd_rn(e, e2);
+                e = __fadd_ru(e, e2);
             }
             sum = __fadd_rn(s, e);
         }

@@ -410,6 +410,7 @@ dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw,
  * from router logits.  Per token, in binary32 (expf, divisions correctly rounded):
  *   p[e]   = 1 / (1 + exp(-x[e]))                                DG_SCORE_SIGMOID
  *          = exp(x[e] - max x) / sum exp(x - max x)              DG_SCORE_SOFTMAX
+ *            (the exact sum rounded once, up to 2^-43 of it)
  *   key[e] = p[e] + bias[e]       (bias NULL: p[e]); experts whose logit is -inf or NaN have
  *            no key: they are never picked and add nothing to the sum; neither have those
  *            whose bias is -inf or NaN, which do add to the sum (+inf counts as the type's
