@@ -97,9 +97,10 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float (&v)[8])
 }
 
 // Codes of eight elements of a block.  NV divides by s g: with r the correctly rounded
-// reciprocal and q within an ulp of x / f, q + r (x - q f) in fused steps is the correctly
+// reciprocal and q within an ulp of x / f, q - r (q f - x) in fused steps is the correctly
 // rounded quotient (P. W. Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990) -- three instructions an element for a division's dozen.
+// (With x - q f the quotient of -0 would come out as +0.)
 // Where the remainder or the quotient could leave the normal range (divisors outside
 // 2^-100 .. 2^100, a scale that saturated far below its block): plain division.
 template <bool NV>
@@ -111,7 +112,7 @@ __device__ __forceinline__ uint32_t encode8(float (&v)[8], const Scale& s)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float q = __fmul_rn(v[i], r);
-                v[i] = __fmaf_rn(__fmaf_rn(-q, s.f, v[i]), r, q);
+                v[i] = __fmaf_rn(-__fmaf_rn(q, s.f, -v[i]), r, q);
             }
         } else {
 #pragma unroll
