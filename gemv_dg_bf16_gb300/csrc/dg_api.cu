@@ -702,7 +702,7 @@ static dg_status check_fp4(const void* const* ptrs, int n, const float* g, const
         if (!ptrs[i]) return DG_ERR_INVALID_ARG;
     if (M < 1 || K < 1 || (fmt != DG_FP4_MX && fmt != DG_FP4_NV)) return DG_ERR_INVALID_ARG;
     if (fmt == DG_FP4_MX && (g || g2)) return DG_ERR_INVALID_ARG;
-    if (K % 32 != 0 || M > 0x7fffff00) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (K % 32 != 0 || M > fp4::kMaxLen || K > fp4::kMaxLen) return DG_ERR_UNSUPPORTED_SHAPE;
     for (int i = 0; i < n; ++i)
         if (!aligned16(ptrs[i])) return DG_ERR_ALIGNMENT;
     if ((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(g2)) & 3u) return DG_ERR_ALIGNMENT;
@@ -737,6 +737,7 @@ dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw,
     const void* ptrs[] = {x, Wq, sw, y};
     dg_status s = check_fp4(ptrs, 4, gx, gw, M, K, fmt);
     if (s != DG_OK) return s;
+    if (N > fp4::kMaxLen) return DG_ERR_UNSUPPORTED_SHAPE;
     s = check_common(ptrs, 4, ws, ws_bytes, dg_workspace_bytes(DG_OP_GEMV_A4W4, M, N, K, 0));
     if (s != DG_OK) return s;
     const DeviceInfo* dev = current_device(&s);

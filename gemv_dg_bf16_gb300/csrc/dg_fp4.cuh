@@ -25,13 +25,17 @@ namespace fp4 {
 
 constexpr int kTileRows = 128;             // rows of a scale tile
 constexpr int kTileBytes = 512;
+constexpr int kMaxLen = 0x7fffff00;        // rows, and elements of a row: indices past the end stay in 32 bits
 
 __host__ __device__ constexpr int block_len(bool nv) { return nv ? 16 : 32; }
 __host__ __device__ constexpr int tile_k(bool nv) { return 4 * block_len(nv); }     // K elements of a scale tile
-__host__ __device__ constexpr int scale_tiles(int K, bool nv) { return (K + tile_k(nv) - 1) / tile_k(nv); }
+__host__ __device__ constexpr int scale_tiles(int K, bool nv)
+{
+    return K / tile_k(nv) + (K % tile_k(nv) != 0);
+}
 __host__ __device__ constexpr size_t scale_bytes(int rows, int K, bool nv)
 {
-    return static_cast<size_t>((rows + kTileRows - 1) / kTileRows) * scale_tiles(K, nv) * kTileBytes;
+    return static_cast<size_t>(rows / kTileRows + (rows % kTileRows != 0)) * scale_tiles(K, nv) * kTileBytes;
 }
 // Byte of row r (0..127), block b (0..3) inside a tile.
 __host__ __device__ constexpr int tile_offset(int r, int b) { return (r % 32) * 16 + (r / 32) * 4 + b; }

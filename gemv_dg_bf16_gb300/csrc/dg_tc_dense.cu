@@ -1461,7 +1461,7 @@ size_t a4_workspace_bytes(int M, int K)
     const size_t q = (static_cast<size_t>(M) * K / 2 + 255) / 256 * 256;
     // the wider of the two formats' scales, a tile row for each 32 tokens (the smallest group)
     return kWsData + q +
-           static_cast<size_t>((M + 31) / 32) * fp4::scale_tiles(K, true) * fp4::kTileBytes;
+           static_cast<size_t>(M / 32 + (M % 32 != 0)) * fp4::scale_tiles(K, true) * fp4::kTileBytes;
 }
 
 namespace {

@@ -375,8 +375,8 @@ dg_status dg_quant_a8_blockscale(const void* x, void* q, float* sx, int M, int K
 size_t dg_fp4_scale_bytes(int rows, int K, int fmt);   /* 0 for a bad argument */
 
 /* q, s = the codes and tiled scales of x [M, K] bf16 (activations, or weights with M = N).
- * M >= 1, K % 32 == 0; g NULL with DG_FP4_MX.  Asynchronous on `stream`; a linear launched
- * after it may read q and s as its weights. */
+ * M and K from 1 to 2^31 - 256, K % 32 == 0; g NULL with DG_FP4_MX.  Asynchronous on
+ * `stream`; a linear launched after it may read q and s as its weights. */
 dg_status dg_quant_fp4_blockscale(const void* x, void* q, void* s, const float* g, int M, int K, int fmt,
                                   dg_stream_t stream);
 
@@ -391,8 +391,8 @@ dg_status dg_dequant_fp4_blockscale(const void* q, const void* s, const float* g
  * x [M, K] bf16, Wq [N, K / 2] codes and sw tiled scales of the weights in the same format,
  * gx, gw: device pointers to the tensor scales of the activations (calibrated ahead) and of
  * the weights (NULL: 1; both NULL with DG_FP4_MX), y [M, N] bf16.
- * 1 <= M <= 512, K % 32 == 0.  Tensor cores only (DG_VAR_TC; params[0] pipeline stages,
- * params[1] the K-split rule: 0 by the shape and the row count, 1 by the shape alone, which
+ * 1 <= M <= 512, K % 32 == 0, N and K up to 2^31 - 256.  Tensor cores only (DG_VAR_TC;
+ * params[0] pipeline stages, params[1] the K-split rule: 0 by the shape and the row count, 1 by the shape alone, which
  * the batch-invariant mode takes: output row m is then a function of input row m at every
  * M).  Non-finite activations give NaN outputs for their token.  ws:
  * the status word, and the codes and scales of the activations. */
