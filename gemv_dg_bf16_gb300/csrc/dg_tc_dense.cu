@@ -1514,6 +1514,10 @@ dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const
     if (stages == 0) {
         stages = 5;
         while (stages > 2 && smem_bytes_a4(mp, nv, stages, recv, xq) > kCoResidentSmem) --stages;
+    } else if (c.from_table) {
+        // A pick holds for both formats, every row count of its bucket and both K-split rules, whose
+        // stages differ in size: as deep as this call's fit (depth changes no bits).
+        while (stages > 2 && smem_bytes_a4(mp, nv, stages, recv, xq) > kMaxDynSmem) --stages;
     }
     if (stages < 2 || stages > 8) return DG_ERR_BAD_VARIANT;
     // A K-split parks its partial tile in the ring.

@@ -392,9 +392,9 @@ dg_status dg_dequant_fp4_blockscale(const void* q, const void* s, const float* g
  * gx, gw: device pointers to the tensor scales of the activations (calibrated ahead) and of
  * the weights (NULL: 1; both NULL with DG_FP4_MX), y [M, N] bf16.
  * 1 <= M <= 512, K % 32 == 0, N and K up to 2^31 - 256.  Tensor cores only (DG_VAR_TC;
- * params[0] pipeline stages, params[1] the K-split rule: 0 by the shape and the row count, 1 by the shape alone, which
- * the batch-invariant mode takes: output row m is then a function of input row m at every
- * M).  Non-finite activations give NaN outputs for their token.  ws:
+ * params[0] pipeline stages, params[1] the K-split rule: 0 by the shape and the row count, 1
+ * by the shape alone, which the batch-invariant mode takes: output row m is then a function of
+ * input row m at every M).  Non-finite activations give NaN outputs for their token.  ws:
  * the status word, and the codes and scales of the activations. */
 dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw, const float* gx, const float* gw,
                                   void* y, int M, int N, int K, int fmt, void* ws, size_t ws_bytes,
@@ -505,7 +505,7 @@ dg_status dg_table_check(const char* path, const char* arch, int driver_version,
  * Each record names the op and its sizes as dg_workspace_bytes does (N = N_half
  * for gate/up, N = I and K = hidden for MoE W1, N = Nout and K = I for MoE W2);
  * E is the expert count (0 = 128); for A4W4 topk names the format (DG_FP4_*) that is
- * measured, and the pick serves both.  The table is written to out_path as JSON with
+ * measured; the pick serves both, with fewer stages where a call has room for fewer.  The table is written to out_path as JSON with
  * this build's identity.  The sweep allocates and frees its own device buffers
  * (it is an offline tool, not a decode-loop call) and synchronises the device.
  * Returns the first error met; shapes after it are not measured. */
