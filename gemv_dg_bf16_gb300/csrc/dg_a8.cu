@@ -37,7 +37,8 @@ dg_status launch_a8_quant(const void* x, void* q, float* sx, int M, int K, cudaS
     const uint16_t* xa = static_cast<const uint16_t*>(x);
     uint8_t* qa = static_cast<uint8_t*>(q);
     void* args[] = {&xa, &qa, &sx, &M, &K};
-    if (launch_kernel(reinterpret_cast<const void*>(&a8_quant_kernel), grid, 256, 0, stream, args) != cudaSuccess) {
+    if (launch_kernel(reinterpret_cast<const void*>(&a8_quant_kernel), grid, 256, 0, stream, args,
+                      Early::kNothing) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
     }

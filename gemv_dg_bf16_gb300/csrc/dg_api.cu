@@ -8,6 +8,8 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <set>
+#include <thread>
 #include <tuple>
 #include <utility>
 
@@ -57,17 +59,63 @@ namespace {
 std::atomic<int> g_launch_flags{DG_LAUNCH_PDL};
 }
 
-bool pdl_enabled() { return (g_launch_flags.load(std::memory_order_relaxed) & DG_LAUNCH_PDL) != 0; }
-
 namespace {
+
 thread_local int t_check_only = 0;
+
+// Streams on which weights were written and no kernel that reads weights early has been
+// launched since.  (The default streams go by device, the per-thread one by thread too.)
+using StreamKey = std::tuple<int, uintptr_t, std::thread::id>;
+std::mutex g_written_mu;
+std::set<StreamKey> g_written;
+std::atomic<int> g_written_n{0};
+
+StreamKey stream_key(cudaStream_t s)
+{
+    if (s == nullptr) s = cudaStreamLegacy;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();
+    return StreamKey(dev, reinterpret_cast<uintptr_t>(s),
+                     s == cudaStreamPerThread ? std::this_thread::get_id() : std::thread::id());
+}
+
+}  // namespace
+
+void weights_written(cudaStream_t stream)
+{
+    std::lock_guard<std::mutex> lk(g_written_mu);
+    g_written.insert(stream_key(stream));
+    g_written_n = static_cast<int>(g_written.size());
+}
+
+cudaError_t launch_ordered(cudaLaunchConfig_t cfg, cudaLaunchAttribute* attr, unsigned n, const void* fn, void** args,
+                           Early early)
+{
+    bool pdl = (g_launch_flags.load(std::memory_order_relaxed) & DG_LAUNCH_PDL) != 0;
+    bool written = false;
+    if (early == Early::kWeights && g_written_n.load() != 0) {
+        std::lock_guard<std::mutex> lk(g_written_mu);
+        written = g_written.count(stream_key(cfg.stream)) != 0;
+    }
+    pdl = pdl && !written;
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = n + 1;
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (written && e == cudaSuccess) {
+        std::lock_guard<std::mutex> lk(g_written_mu);
+        g_written.erase(stream_key(cfg.stream));
+        g_written_n = static_cast<int>(g_written.size());
+    }
+    return e;
 }
 
 CheckOnly::CheckOnly() { ++t_check_only; }
 CheckOnly::~CheckOnly() { --t_check_only; }
 
 cudaError_t launch_kernel(const void* fn, unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
-                          void** args)
+                          void** args, Early early)
 {
     if (t_check_only) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
@@ -76,11 +124,7 @@ cudaError_t launch_kernel(const void* fn, unsigned grid, unsigned block, size_t 
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelExC(&cfg, fn, args);
+    return launch_ordered(cfg, attr, 0, fn, args, early);
 }
 
 cudaError_t launch_kernel_cooperative(const void* fn, unsigned grid, unsigned block, size_t smem,
@@ -95,11 +139,7 @@ cudaError_t launch_kernel_cooperative(const void* fn, unsigned grid, unsigned bl
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelExC(&cfg, fn, args);
+    return launch_ordered(cfg, attr, 1, fn, args, Early::kWeights);
 }
 
 int occupancy(const void* fn, int threads, size_t smem)
@@ -716,7 +756,10 @@ dg_status dg_quant_fp4_blockscale(const void* x, void* q, void* s, const float* 
     dg_status st = check_fp4(ptrs, 3, g, nullptr, M, K, fmt);
     if (st != DG_OK) return st;
     if (!current_device(&st)) return st;
-    return launch_fp4_quant(fmt == DG_FP4_NV, x, q, s, g, M, K, fp4::kTileRows, false, reinterpret_cast<cudaStream_t>(stream));
+    st = launch_fp4_quant(fmt == DG_FP4_NV, x, q, s, g, M, K, fp4::kTileRows, false,
+                          reinterpret_cast<cudaStream_t>(stream));
+    if (st == DG_OK) weights_written(reinterpret_cast<cudaStream_t>(stream));
+    return st;
 }
 
 dg_status dg_dequant_fp4_blockscale(const void* q, const void* s, const float* g, void* y, int M, int K, int fmt,
@@ -726,7 +769,9 @@ dg_status dg_dequant_fp4_blockscale(const void* q, const void* s, const float* g
     dg_status st = check_fp4(ptrs, 3, g, nullptr, M, K, fmt);
     if (st != DG_OK) return st;
     if (!current_device(&st)) return st;
-    return launch_fp4_dequant(fmt == DG_FP4_NV, q, s, g, y, M, K, reinterpret_cast<cudaStream_t>(stream));
+    st = launch_fp4_dequant(fmt == DG_FP4_NV, q, s, g, y, M, K, reinterpret_cast<cudaStream_t>(stream));
+    if (st == DG_OK) weights_written(reinterpret_cast<cudaStream_t>(stream));
+    return st;
 }
 
 dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw, const float* gx, const float* gw,

@@ -155,8 +155,10 @@ __device__ __forceinline__ void reduce_scatter(float (&v)[Q], int lane)
     Butterfly<16, Q>::run(v, lane);
 }
 
-// Programmatic dependent launch.  A kernel may read weights (never written by this
-// library's kernels) before pdl_wait(); everything a preceding kernel may have
+// Programmatic dependent launch.  A kernel may read weights before pdl_wait(): the
+// kernels of this library that write any (the 4-bit quantisation and its inverse) never signal
+// early and are noted on the stream, and the next launch that reads weights early is then made
+// without the programmatic dependency (launch_ordered); everything else a preceding kernel may have
 // produced or may still read (activations, routing, scales, outputs, workspace) is
 // touched only after it.  pdl_wait() returns at once when the launch had no
 // programmatic dependency.

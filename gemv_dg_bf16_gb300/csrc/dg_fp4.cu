@@ -6,6 +6,12 @@
 // by shuffles, and 8 or 16 lanes put together the 16 scale bytes that those rows have side
 // by side in a scale tile (4-byte stores of them, one row at a time, cost 4 us on 16 rows).
 // No shared memory and no barrier: every row's loads are in flight before the first is used.
+// The outputs may be weights, which a linear reads before it waits for what is ahead of it: the
+// entry points' kernels let no launch begin before they have completed, and note on the stream
+// that weights were written (weights_written).  Inside the linear, which waits for the codes,
+// the quantisation lets it begin at once (`early`).
+// The inputs are not __restrict__: loads of what the launch ahead may have written must stay
+// behind pdl_wait() and off the non-coherent path.
 // Bound: memory, 2 + 1/2 + 1/16 (or 1/32) bytes an element and direction.  24576 x 4096 in MX:
 // there 50 us and back 39, of 37.5 for the bytes each; 105 and 71 instructions for 8 elements,
 // the former's conversions keeping the ALU two thirds busy.  16 x 4096 there and back: 3.4 us.
@@ -21,20 +27,6 @@ constexpr int kRows = 4;                   // rows per warp, 32 apart, all in fl
 constexpr int kStep = 32;                  // rows r, r + 32, r + 64, r + 96 of a scale tile share 16 bytes
 constexpr int kRowCtas = kStep / kWarps;   // CTAs over a scale tile's 128 rows
 static_assert(kRows * kStep == fp4::kTileRows && kStep % kWarps == 0, "a warp's rows are one 16-byte piece");
-
-// The outputs may be weights, which a linear of this library reads before it waits for the
-// launches ahead of it: let the next launch begin only when the CTA's stores are visible to
-// the whole device, to plain loads and to bulk copies (one fence a CTA, behind its barrier:
-// one a thread stalled the warps for a third of their time).
-__device__ __forceinline__ void signal_written()
-{
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-        pdl_launch_dependents();
-    }
-}
 
 // Where a warp works: its first row, its 16-byte piece in scale tile kt of that tile row.
 struct Place {
@@ -56,9 +48,8 @@ struct Place {
 };
 
 template <bool NV>
-__global__ void __launch_bounds__(kWarps * 32) fp4_quant_kernel(const uint16_t* __restrict__ x,
-                                                                uint8_t* __restrict__ q, uint8_t* __restrict__ s,
-                                                                const float* __restrict__ gp, int M, int K,
+__global__ void __launch_bounds__(kWarps * 32) fp4_quant_kernel(const uint16_t* x, uint8_t* __restrict__ q,
+                                                                uint8_t* __restrict__ s, const float* gp, int M, int K,
                                                                 int col_tiles, int tile_rows, int early)
 {
     constexpr int kShare = fp4::block_len(NV) / 8;             // lanes per block
@@ -99,16 +90,12 @@ __global__ void __launch_bounds__(kWarps * 32) fp4_quant_kernel(const uint16_t* 
     }
     if (lane % kWord == 0 && at.col_tile * kTiles + lane / kWord < nkt)
         *reinterpret_cast<uint4*>(s + at.scales) = make_uint4(words[0], words[1], words[2], words[3]);
-    if (!early) signal_written();
 }
 
 // y = bf16(code * (scale * g)), each step rounded to binary32 (MX: exact).
 template <bool NV>
-__global__ void __launch_bounds__(kWarps * 32) fp4_dequant_kernel(const uint8_t* __restrict__ q,
-                                                                  const uint8_t* __restrict__ s,
-                                                                  const float* __restrict__ gp,
-                                                                  uint16_t* __restrict__ y, int M, int K,
-                                                                  int col_tiles)
+__global__ void __launch_bounds__(kWarps * 32) fp4_dequant_kernel(const uint8_t* q, const uint8_t* s, const float* gp,
+                                                                  uint16_t* y, int M, int K, int col_tiles)
 {
     constexpr int kShare = fp4::block_len(NV) / 8;
     constexpr int kWord = 4 * kShare;
@@ -150,7 +137,6 @@ __global__ void __launch_bounds__(kWarps * 32) fp4_dequant_kernel(const uint8_t*
             *reinterpret_cast<uint4*>(y + static_cast<size_t>(row) * K + k) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    signal_written();
 }
 
 }  // namespace
@@ -164,7 +150,7 @@ dg_status launch_fp4_quant(bool nv, const void* x, void* q, void* s, const float
     const void* fn = nv ? reinterpret_cast<const void*>(&fp4_quant_kernel<true>)
                         : reinterpret_cast<const void*>(&fp4_quant_kernel<false>);
     void* args[] = {&x, &q, &s, &g, &M, &K, &col_tiles, &tile_rows, &now};
-    if (launch_kernel(fn, static_cast<unsigned>(grid), kWarps * 32, 0, stream, args) != cudaSuccess) {
+    if (launch_kernel(fn, static_cast<unsigned>(grid), kWarps * 32, 0, stream, args, Early::kNothing) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
     }
@@ -180,7 +166,7 @@ dg_status launch_fp4_dequant(bool nv, const void* q, const void* s, const float*
     const void* fn = nv ? reinterpret_cast<const void*>(&fp4_dequant_kernel<true>)
                         : reinterpret_cast<const void*>(&fp4_dequant_kernel<false>);
     void* args[] = {&q, &s, &g, &y, &M, &K, &col_tiles};
-    if (launch_kernel(fn, static_cast<unsigned>(grid), kWarps * 32, 0, stream, args) != cudaSuccess) {
+    if (launch_kernel(fn, static_cast<unsigned>(grid), kWarps * 32, 0, stream, args, Early::kNothing) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
     }

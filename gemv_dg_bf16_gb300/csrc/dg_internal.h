@@ -119,10 +119,20 @@ const DeviceInfo* current_device(dg_status* err);
 // (cached); also raises the kernel's dynamic shared memory limit once.
 int occupancy(const void* fn, int threads, size_t smem);
 
-// Launch with this library's attributes (programmatic dependent launch when enabled).
-bool pdl_enabled();
+// What a kernel touches before its pdl_wait(): weights, or nothing.
+enum class Early { kWeights, kNothing };
+
+// Launch with this library's attributes: programmatic dependent launch when enabled -- but for a
+// kernel that reads weights early behind weights_written() on its stream, which waits for what is
+// ahead of it in full.  (A captured graph's edges from other streams may be programmatic all the
+// same: writers of weights never signal early, so those wait for their completion too.)  attr has
+// room for one attribute past the n given.
+cudaError_t launch_ordered(cudaLaunchConfig_t cfg, cudaLaunchAttribute* attr, unsigned n, const void* fn, void** args,
+                           Early early);
 cudaError_t launch_kernel(const void* fn, unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
-                          void** args);
+                          void** args, Early early = Early::kWeights);
+// The launch just made on `stream` writes what a kernel of this library may read as weights.
+void weights_written(cudaStream_t stream);
 // The same as a cooperative launch: the runtime starts it only with every CTA resident
 // at once, whatever else the GPU runs -- for kernels with a grid-wide barrier.
 cudaError_t launch_kernel_cooperative(const void* fn, unsigned grid, unsigned block, size_t smem,

@@ -673,11 +673,7 @@ dg_status launch_logprobs(const void* logits, bool f32, long long ld, const int6
     attr[0].val.clusterDim.x = static_cast<unsigned>(cs);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+    if (launch_ordered(cfg, attr, 1, fn, args, Early::kNothing) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
     }

@@ -399,7 +399,7 @@ dg_status launch_route(const dg_route_params& p, const void* logits, const float
     const long long most = static_cast<long long>(dev->sm_count) * occ;
     if (grid > most) grid = most;
     void* args[] = {&a};
-    if (launch_kernel(fn, static_cast<unsigned>(grid), kWarps * 32, 0, stream, args) != cudaSuccess) {
+    if (launch_kernel(fn, static_cast<unsigned>(grid), kWarps * 32, 0, stream, args, Early::kNothing) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
     }

@@ -1259,11 +1259,7 @@ dg_status launch_tc(bool gate_up, const DeviceInfo* dev, const dg_choice& c, con
     attr[0].val.clusterDim.x = static_cast<unsigned>(a.nsplit);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+    if (launch_ordered(cfg, attr, 1, fn, args, Early::kWeights) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
     }
@@ -1399,11 +1395,7 @@ dg_status launch_tc_a8(const DeviceInfo* dev, const dg_choice& c, const void* x,
     attr[0].val.clusterDim.x = static_cast<unsigned>(a.nsplit);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+    if (launch_ordered(cfg, attr, 1, fn, args, Early::kWeights) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
     }
@@ -1564,7 +1556,7 @@ dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const
     else if (!encode_2d(&tmX, qws, kb, static_cast<uint64_t>(M), 128, static_cast<uint32_t>(mp), true))
         return DG_ERR_CUDA;
     if (!fuse) {
-        const dg_status st = launch_fp4_quant(nv, x, qws, sws, gx, M, K, mp < fp4::kTileRows ? mp : fp4::kTileRows, true, stream);
+        const dg_status st = launch_fp4_quant(nv, x, qws, sws, gx, M, K, mp, true, stream);
         if (st != DG_OK) return st;
     }
     void* args[] = {&tmW, &tmX, &a};
@@ -1578,11 +1570,7 @@ dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const
     attr[0].val.clusterDim.x = static_cast<unsigned>(ns);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (cudaLaunchKernelExC(&cfg, fn, args) != cudaSuccess) {
+    if (launch_ordered(cfg, attr, 1, fn, args, Early::kWeights) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
     }

@@ -169,8 +169,11 @@ dg_status dg_device_status(const void* ws, int32_t* host_out, dg_stream_t stream
 /* Launch flags (process-wide).  DG_LAUNCH_PDL (on by default): every kernel is
  * launched with programmatic dependent launch, so it can be scheduled while the
  * preceding kernel on the stream finishes; before waiting for that kernel it
- * touches nothing but weights (streams them into L2 or shared memory), which this
- * library never writes.  A preceding kernel that does not signal early (any
+ * touches nothing but weights (streams them into L2 or shared memory).  Of this
+ * library dg_quant_fp4_blockscale and dg_dequant_fp4_blockscale write what may be
+ * weights: no kernel begins before they have completed, and the next one on their
+ * stream that reads weights early is launched without the overlap.  Other outputs of this library are no weights of a call on
+ * the same stream while the flag is on.  A preceding kernel that does not signal early (any
  * kernel not from this library) still completes before this one starts its
  * dependent work.  Turn it off when a kernel of this library must wait for a
  * preceding launch that writes the weights it reads.
