@@ -345,7 +345,8 @@ def dg_quant_a8_blockscale(x, q=None, sx=None, stream=None):
 
 
 # The calls below are small enough that marshalling them shows in a decode step: their checks
-# and the C call run in _marshal.so, which takes the arguments by position.
+# and the C call run in _marshal.so, which takes the arguments by position.  Given a stream, they
+# run with it as the current one, so that the buffers they make are made, and reused, in its order.
 _marshal = None
 
 
@@ -374,12 +375,15 @@ def dg_fp4_scale_bytes(rows: int, K: int, fmt: int) -> int:
 def dg_quant_fp4_blockscale(x, fmt, g=None, q=None, s=None, stream=None):
     """(q [M, K/2] uint8 code pairs, s uint8 tiled block scales) of x [M, K] bf16 in the MX or
     NV 4-bit format; g: the NV tensor scale (one fp32 on the device), None for 1."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_quant_fp4_blockscale(x, fmt, g, q, s)
     m = _marshal or _load_marshal()
     if q is None:
         q = torch.empty((x.shape[0], x.shape[1] // 2), dtype=torch.uint8, device=x.device)
     if s is None:
         s = torch.empty(fp4_scale_shape(x.shape[0], x.shape[1], fmt), dtype=torch.uint8, device=x.device)
-    st = m.quant(x, fmt, g, q, s, None if stream is None else stream.cuda_stream)
+    st = m.quant(x, fmt, g, q, s)
     if st:
         raise DGError(st, "dg_quant_fp4_blockscale")
     return q, s
@@ -387,10 +391,13 @@ def dg_quant_fp4_blockscale(x, fmt, g=None, q=None, s=None, stream=None):
 
 def dg_dequant_fp4_blockscale(q, s, fmt, g=None, y=None, stream=None):
     """y [M, K] bf16: the values that the codes and scales of dg_quant_fp4_blockscale stand for."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_dequant_fp4_blockscale(q, s, fmt, g, y)
     m = _marshal or _load_marshal()
     if y is None:
         y = torch.empty((q.shape[0], 2 * q.shape[1]), dtype=torch.bfloat16, device=q.device)
-    st = m.dequant(q, s, fmt, g, y, None if stream is None else stream.cuda_stream)
+    st = m.dequant(q, s, fmt, g, y)
     if st:
         raise DGError(st, "dg_dequant_fp4_blockscale")
     return y
@@ -399,6 +406,9 @@ def dg_dequant_fp4_blockscale(q, s, fmt, g=None, y=None, stream=None):
 def dg_gemv_a4w4_blockscale(x, Wq, sw, fmt, gx=None, gw=None, y=None, ws=None, choice=None, stream=None):
     """y [M, N] bf16 = microscaled 4-bit product of x [M, K] (bf16, quantised inside the call with
     tensor scale gx) and the weights Wq [N, K/2], sw, gw as dg_quant_fp4_blockscale makes them."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_gemv_a4w4_blockscale(x, Wq, sw, fmt, gx, gw, y, ws, choice)
     m = _marshal or _load_marshal()
     if y is None:
         y = torch.empty((x.shape[0], Wq.shape[0]), dtype=torch.bfloat16, device=x.device)
@@ -406,8 +416,7 @@ def dg_gemv_a4w4_blockscale(x, Wq, sw, fmt, gx=None, gw=None, y=None, ws=None, c
         ws = workspace(DG_OP_GEMV_A4W4, x.shape[0], Wq.shape[0], x.shape[1], device=x.device)
     if choice is not None and not isinstance(choice, Choice):
         choice = Choice.make(*choice)
-    st = m.a4w4(x, Wq, sw, fmt, gx, gw, y, ws, None if choice is None else ctypes.addressof(choice),
-                None if stream is None else stream.cuda_stream)
+    st = m.a4w4(x, Wq, sw, fmt, gx, gw, y, ws, None if choice is None else ctypes.addressof(choice))
     if st:
         raise DGError(st, "dg_gemv_a4w4_blockscale")
     return y
@@ -417,13 +426,15 @@ def dg_moe_route(logits, topk, score=DG_SCORE_SOFTMAX, bias=None, n_group=1, top
                  scale=1.0, ids=None, w=None, stream=None):
     """(ids [M, topk] int32, w [M, topk] fp32): the experts and gate weights of each token, as
     dg_moe_w1_silu and dg_moe_w2 take them, from router logits [M, E] (bf16 or fp32, any row stride)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_moe_route(logits, topk, score, bias, n_group, topk_group, group_top, renorm, scale, ids, w)
     m = _marshal or _load_marshal()
     if ids is None:
         ids = torch.empty((logits.shape[0], max(topk, 0)), dtype=torch.int32, device=logits.device)
     if w is None:
         w = torch.empty((logits.shape[0], max(topk, 0)), dtype=torch.float32, device=logits.device)
-    st = m.route(logits, topk, score, bias, n_group, topk_group, group_top, renorm, scale, ids, w,
-                 None if stream is None else stream.cuda_stream)
+    st = m.route(logits, topk, score, bias, n_group, topk_group, group_top, renorm, scale, ids, w)
     if st:
         raise DGError(st, "dg_moe_route")
     return ids, w
@@ -434,6 +445,9 @@ def dg_logprobs(logits, tokens=None, n_top=0, scale=1.0, logprob=None, rank=None
     """Log-probabilities over logits [M, V] (bf16 or fp32, any row stride): a dict of logprob [M],
     rank [M] (of tokens [M] int64; None without them), entropy [M], top_ids and top_logprobs
     [M, n_top] (None at 0)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_logprobs(logits, tokens, n_top, scale, logprob, rank, entropy, top_ids, top_logprobs)
     m = _marshal or _load_marshal()
     M, dev = logits.shape[0], logits.device
     if tokens is not None:
@@ -452,8 +466,7 @@ def dg_logprobs(logits, tokens=None, n_top=0, scale=1.0, logprob=None, rank=None
             top_logprobs = torch.empty((M, n_top), dtype=torch.float32, device=dev)
     elif top_ids is not None or top_logprobs is not None:
         raise ValueError("n_top: top_ids and top_logprobs need it")
-    st = m.logprobs(logits, tokens, scale, n_top, logprob, rank, entropy, top_ids, top_logprobs,
-                    None if stream is None else stream.cuda_stream)
+    st = m.logprobs(logits, tokens, scale, n_top, logprob, rank, entropy, top_ids, top_logprobs)
     if st:
         raise DGError(st, "dg_logprobs")
     return {"logprob": logprob, "rank": rank, "entropy": entropy, "top_ids": top_ids, "top_logprobs": top_logprobs}

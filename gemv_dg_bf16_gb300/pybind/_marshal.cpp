@@ -124,16 +124,8 @@ bool whole(PyObject* o, long long* v)
     return true;
 }
 
-// The caller's stream (its address), or the current one of the current device.
-bool stream_of(PyObject* o, dg_stream_t* s)
-{
-    if (o == Py_None) {
-        *s = reinterpret_cast<dg_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
-        return true;
-    }
-    *s = reinterpret_cast<dg_stream_t>(PyLong_AsVoidPtr(o));
-    return !PyErr_Occurred();
-}
+// The current stream of the current device.
+dg_stream_t current_stream() { return reinterpret_cast<dg_stream_t>(c10::cuda::getCurrentCUDAStream().stream()); }
 
 bool count_args(Py_ssize_t got, Py_ssize_t want)
 {
@@ -164,7 +156,7 @@ PyObject* guarded(F&& f)
     }
 }
 
-// (x, fmt, g, q, s, stream)
+// (x, fmt, g, q, s)
 PyObject* quant(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
@@ -172,17 +164,15 @@ PyObject* quant(PyObject*, PyObject* const* a, Py_ssize_t n)
         long long fmt;
         void *x, *q, *s;
         const float* g;
-        dg_stream_t st;
-        if (!count_args(n, 6) || !format_of(a[1], &fmt) || !two_dims(a[0], "x", &M, &K) ||
+        if (!count_args(n, 5) || !format_of(a[1], &fmt) || !two_dims(a[0], "x", &M, &K) ||
             !dense(a[0], "x", ScalarType::BFloat16, {M, K}, &x) || !dense(a[3], "q", ScalarType::Byte, {M, K / 2}, &q) ||
-            !dense(a[4], "s", ScalarType::Byte, {row_tiles(M), k_tiles(K, fmt), 512}, &s) || !scalar(a[2], "g", &g) ||
-            !stream_of(a[5], &st))
+            !dense(a[4], "s", ScalarType::Byte, {row_tiles(M), k_tiles(K, fmt), 512}, &s) || !scalar(a[2], "g", &g))
             return nullptr;
-        return PyLong_FromLong(g_quant(x, q, s, g, static_cast<int>(M), static_cast<int>(K), static_cast<int>(fmt), st));
+        return PyLong_FromLong(g_quant(x, q, s, g, static_cast<int>(M), static_cast<int>(K), static_cast<int>(fmt), current_stream()));
     });
 }
 
-// (q, s, fmt, g, y, stream)
+// (q, s, fmt, g, y)
 PyObject* dequant(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
@@ -190,8 +180,7 @@ PyObject* dequant(PyObject*, PyObject* const* a, Py_ssize_t n)
         long long fmt;
         void *q, *s, *y;
         const float* g;
-        dg_stream_t st;
-        if (!count_args(n, 6) || !format_of(a[2], &fmt) || !two_dims(a[0], "q", &M, &half)) return nullptr;
+        if (!count_args(n, 5) || !format_of(a[2], &fmt) || !two_dims(a[0], "q", &M, &half)) return nullptr;
         const int64_t K = 2 * half;
         if (K > INT32_MAX) {
             refuse("q", "a dimension past 2^31 - 1");
@@ -199,13 +188,13 @@ PyObject* dequant(PyObject*, PyObject* const* a, Py_ssize_t n)
         }
         if (!dense(a[0], "q", ScalarType::Byte, {M, half}, &q) ||
             !dense(a[1], "s", ScalarType::Byte, {row_tiles(M), k_tiles(K, fmt), 512}, &s) || !scalar(a[3], "g", &g) ||
-            !dense(a[4], "y", ScalarType::BFloat16, {M, K}, &y) || !stream_of(a[5], &st))
+            !dense(a[4], "y", ScalarType::BFloat16, {M, K}, &y))
             return nullptr;
-        return PyLong_FromLong(g_dequant(q, s, g, y, static_cast<int>(M), static_cast<int>(K), static_cast<int>(fmt), st));
+        return PyLong_FromLong(g_dequant(q, s, g, y, static_cast<int>(M), static_cast<int>(K), static_cast<int>(fmt), current_stream()));
     });
 }
 
-// (x, Wq, sw, fmt, gx, gw, y, ws, choice address or None, stream)
+// (x, Wq, sw, fmt, gx, gw, y, ws, choice address or None)
 PyObject* a4w4(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
@@ -213,8 +202,7 @@ PyObject* a4w4(PyObject*, PyObject* const* a, Py_ssize_t n)
         long long fmt;
         void *x, *w, *sw, *y;
         const float *gx, *gw;
-        dg_stream_t st;
-        if (!count_args(n, 10) || !format_of(a[3], &fmt) || !two_dims(a[0], "x", &M, &K) ||
+        if (!count_args(n, 9) || !format_of(a[3], &fmt) || !two_dims(a[0], "x", &M, &K) ||
             !two_dims(a[1], "Wq", &N, &half) || !dense(a[0], "x", ScalarType::BFloat16, {M, K}, &x) ||
             !dense(a[1], "Wq", ScalarType::Byte, {N, K / 2}, &w) ||
             !dense(a[2], "sw", ScalarType::Byte, {row_tiles(N), k_tiles(K, fmt), 512}, &sw) ||
@@ -231,13 +219,12 @@ PyObject* a4w4(PyObject*, PyObject* const* a, Py_ssize_t n)
             choice = static_cast<const dg_choice*>(PyLong_AsVoidPtr(a[8]));
             if (PyErr_Occurred()) return nullptr;
         }
-        if (!stream_of(a[9], &st)) return nullptr;
         return PyLong_FromLong(g_a4w4(x, w, sw, gx, gw, y, static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
-                                      static_cast<int>(fmt), ws->data_ptr(), static_cast<size_t>(ws->numel()), st, choice));
+                                      static_cast<int>(fmt), ws->data_ptr(), static_cast<size_t>(ws->numel()), current_stream(), choice));
     });
 }
 
-// (logits, topk, score, bias, n_group, topk_group, group_top, renorm, scale, ids, w, stream)
+// (logits, topk, score, bias, n_group, topk_group, group_top, renorm, scale, ids, w)
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
@@ -246,26 +233,24 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
         int64_t ld, M, E;
         long long v[6];
         void *bias, *ids, *w;
-        dg_stream_t st;
-        if (!count_args(n, 12) || !logits_of(a[0], &x, &type, &ld, &M, &E) || !whole(a[1], &v[0]) || !whole(a[2], &v[1]) ||
+        if (!count_args(n, 11) || !logits_of(a[0], &x, &type, &ld, &M, &E) || !whole(a[1], &v[0]) || !whole(a[2], &v[1]) ||
             !whole(a[4], &v[2]) || !whole(a[5], &v[3]) || !whole(a[6], &v[4]))
             return nullptr;
         const int renorm = PyObject_IsTrue(a[7]);
         const double scale = PyFloat_AsDouble(a[8]);
         if (renorm < 0 || PyErr_Occurred()) return nullptr;
         if (!dense_or_none(a[3], "bias", ScalarType::Float, {E}, &bias) ||
-            !dense(a[9], "ids", ScalarType::Int, {M, v[0]}, &ids) || !dense(a[10], "w", ScalarType::Float, {M, v[0]}, &w) ||
-            !stream_of(a[11], &st))
+            !dense(a[9], "ids", ScalarType::Int, {M, v[0]}, &ids) || !dense(a[10], "w", ScalarType::Float, {M, v[0]}, &w))
             return nullptr;
         const dg_route_params p = {static_cast<int32_t>(v[0]), static_cast<int32_t>(v[2]), static_cast<int32_t>(v[3]),
                                    static_cast<int32_t>(v[4]), static_cast<int32_t>(v[1]), renorm,
                                    static_cast<float>(scale)};
         return PyLong_FromLong(g_route(x, type, ld, static_cast<const float*>(bias), &p, static_cast<int32_t*>(ids),
-                                       static_cast<float*>(w), static_cast<int>(M), static_cast<int>(E), st));
+                                       static_cast<float*>(w), static_cast<int>(M), static_cast<int>(E), current_stream()));
     });
 }
 
-// (logits, tokens, scale, n_top, logprob, rank, entropy, top_ids, top_logprobs, stream)
+// (logits, tokens, scale, n_top, logprob, rank, entropy, top_ids, top_logprobs)
 PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject* {
@@ -274,8 +259,7 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n)
         int64_t ld, M, V;
         long long top;
         void *tok, *lp, *rank, *ent, *ti, *tl;
-        dg_stream_t st;
-        if (!count_args(n, 10) || !logits_of(a[0], &x, &type, &ld, &M, &V) || !whole(a[3], &top)) return nullptr;
+        if (!count_args(n, 9) || !logits_of(a[0], &x, &type, &ld, &M, &V) || !whole(a[3], &top)) return nullptr;
         const double scale = PyFloat_AsDouble(a[2]);
         if (PyErr_Occurred()) return nullptr;
         if (!dense_or_none(a[1], "tokens", ScalarType::Long, {M}, &tok) ||
@@ -283,12 +267,12 @@ PyObject* logprobs(PyObject*, PyObject* const* a, Py_ssize_t n)
             !dense_or_none(a[5], "rank", ScalarType::Int, {M}, &rank) ||
             !dense_or_none(a[6], "entropy", ScalarType::Float, {M}, &ent) ||
             !dense_or_none(a[7], "top_ids", ScalarType::Int, {M, top}, &ti) ||
-            !dense_or_none(a[8], "top_logprobs", ScalarType::Float, {M, top}, &tl) || !stream_of(a[9], &st))
+            !dense_or_none(a[8], "top_logprobs", ScalarType::Float, {M, top}, &tl))
             return nullptr;
         return PyLong_FromLong(g_logprobs(x, type, ld, static_cast<const int64_t*>(tok), static_cast<float>(scale),
                                           static_cast<int>(top), static_cast<float*>(lp), static_cast<int32_t*>(rank),
                                           static_cast<float*>(ent), static_cast<int32_t*>(ti), static_cast<float*>(tl),
-                                          static_cast<int>(M), static_cast<int>(V), st));
+                                          static_cast<int>(M), static_cast<int>(V), current_stream()));
     });
 }
 
