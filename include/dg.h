@@ -452,9 +452,12 @@ dg_status dg_moe_route(const void* logits, int logits_type, int64_t ld, const fl
  * gives logprob -inf and entropy 0; alternatives that a row lacks are id -1, -inf.  A NaN or
  * +inf in a row makes its logprob, entropy and top_logprobs NaN; NaN is never an alternative.
  * A token outside [0, V) gives logprob NaN and rank -1.
+ * Ranks and alternatives compare the logits as they are.  Sums are held in binary32, of
+ * exponentials within 2 ulp; at every V a log-probability is within 4e-5 and 2^-21 of itself,
+ * the entropy H within 1e-4 (1 + H).
  * logits [M, V] (ld), tokens [M] int64 or NULL (then logprob and rank are NULL too); each of
  * logprob [M] fp32, rank [M] int32, entropy [M] fp32 may be NULL; 0 <= n_top <= 32 (both top
- * pointers NULL at 0).  M >= 1, 1 <= V <= 2^24, 1e-6 <= scale <= 1e6. */
+ * pointers NULL at 0).  1 <= M <= 2^28, 1 <= V <= 2^24, 1e-6 <= scale <= 1e6. */
 dg_status dg_logprobs(const void* logits, int logits_type, int64_t ld, const int64_t* tokens, float scale, int n_top,
                       float* logprob, int32_t* rank, float* entropy, int32_t* top_ids, float* top_logprobs, int M,
                       int V, dg_stream_t stream);
