@@ -356,7 +356,8 @@ def _load_marshal():
     try:
         from . import _marshal as m
     except ImportError as e:
-        raise ImportError(f"_marshal.so is not built beside {_LIBPATH}; run __graft_entry__.build()") from e
+        why = f"cannot be loaded ({e})" if os.path.exists(os.path.join(_HERE, "_marshal.so")) else "is not built"
+        raise ImportError(f"_marshal.so beside {_LIBPATH} {why}; run __graft_entry__.build()") from e
     m.bind(_LIBPATH)
     _marshal = m
     return m

@@ -1,12 +1,15 @@
 """Build libdecodegemm.so in-tree with nvcc for sm_103a (no cmake, parallel TUs), and the Python
-marshalling module _marshal.so with g++ against the installed torch."""
+marshalling module _marshal.so with g++ against the installed torch.  The library does not depend
+on the module: it is linked whether or not that compiles."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import hashlib
 import os
+import platform
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -57,6 +60,23 @@ def _fresh(out: str, inputs) -> bool:
     return os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(f) for f in inputs)
 
 
+def _marshal_host() -> str:
+    """What the Python module's ABI depends on; kept beside the module it was built for."""
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version}, {platform.machine()}\n"
+
+
+def _marshal_stamp() -> str:
+    return os.path.join(OBJ, "_marshal.host")
+
+
+def _marshal_fresh(inputs) -> bool:
+    if not _fresh(PYMOD, inputs) or not os.path.exists(_marshal_stamp()):
+        return False
+    with open(_marshal_stamp()) as f:
+        return f.read() == _marshal_host()
+
+
 def _build_marshal() -> None:
     import torch
     from torch.utils import cpp_extension as ce
@@ -72,31 +92,30 @@ def _build_marshal() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {PYSRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, PYMOD)
+    with open(_marshal_stamp(), "w") as f:
+        f.write(_marshal_host())
 
 
-def build(force: bool = False, jobs: int | None = None) -> str:
+def _build_lib(jobs: int | None) -> None:
     srcs = sources()
-    header = os.path.join(INCLUDE, "dg.h")
-    lib_ok = not force and _fresh(LIB, glob.glob(os.path.join(CSRC, "*")) + [header])
-    py_ok = not force and _fresh(PYMOD, [PYSRC, header])
-    if lib_ok and py_ok:
-        return LIB
-    if lib_ok:
-        _build_marshal()
-        return LIB
-    os.makedirs(OBJ, exist_ok=True)
     bid = build_id()
-    jobs = jobs or min(len(srcs), os.cpu_count() or 4)
-    with cf.ThreadPoolExecutor(jobs + 1) as ex:
-        marshal = None if py_ok else ex.submit(_build_marshal)
+    with cf.ThreadPoolExecutor(jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
         objs = list(ex.map(lambda s: _compile(s, bid), srcs))
-        if marshal:
-            marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([_nvcc(), *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, jobs: int | None = None) -> str:
+    header = os.path.join(INCLUDE, "dg.h")
+    os.makedirs(OBJ, exist_ok=True)
+    with cf.ThreadPoolExecutor(1) as ex:
+        marshal = ex.submit(lambda: None if not force and _marshal_fresh([PYSRC, header]) else _build_marshal())
+        if force or not _fresh(LIB, glob.glob(os.path.join(CSRC, "*")) + [header]):
+            _build_lib(jobs)
+        marshal.result()                   # (after the library is in place)
     return LIB
 
 
