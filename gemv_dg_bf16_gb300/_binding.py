@@ -363,6 +363,13 @@ def _load_marshal():
     return m
 
 
+def _rows(t, name):
+    """(rows, columns) of a tensor from whose shape a buffer is made."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
+    return t.shape
+
+
 def fp4_scale_shape(rows: int, K: int, fmt: int):
     """Shape of the tiled block scales: [ceil(rows / 128), ceil(blocks / 4), 512] bytes."""
     block = 16 if fmt == DG_FP4_NV else 32
@@ -381,9 +388,10 @@ def dg_quant_fp4_blockscale(x, fmt, g=None, q=None, s=None, stream=None):
             return dg_quant_fp4_blockscale(x, fmt, g, q, s)
     m = _marshal or _load_marshal()
     if q is None:
-        q = torch.empty((x.shape[0], x.shape[1] // 2), dtype=torch.uint8, device=x.device)
+        M, K = _rows(x, "x")
+        q = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
     if s is None:
-        s = torch.empty(fp4_scale_shape(x.shape[0], x.shape[1], fmt), dtype=torch.uint8, device=x.device)
+        s = torch.empty(fp4_scale_shape(*_rows(x, "x"), fmt), dtype=torch.uint8, device=x.device)
     st = m.quant(x, fmt, g, q, s)
     if st:
         raise DGError(st, "dg_quant_fp4_blockscale")
@@ -397,7 +405,8 @@ def dg_dequant_fp4_blockscale(q, s, fmt, g=None, y=None, stream=None):
             return dg_dequant_fp4_blockscale(q, s, fmt, g, y)
     m = _marshal or _load_marshal()
     if y is None:
-        y = torch.empty((q.shape[0], 2 * q.shape[1]), dtype=torch.bfloat16, device=q.device)
+        M, half = _rows(q, "q")
+        y = torch.empty((M, 2 * half), dtype=torch.bfloat16, device=q.device)
     st = m.dequant(q, s, fmt, g, y)
     if st:
         raise DGError(st, "dg_dequant_fp4_blockscale")
@@ -412,9 +421,10 @@ def dg_gemv_a4w4_blockscale(x, Wq, sw, fmt, gx=None, gw=None, y=None, ws=None, c
             return dg_gemv_a4w4_blockscale(x, Wq, sw, fmt, gx, gw, y, ws, choice)
     m = _marshal or _load_marshal()
     if y is None:
-        y = torch.empty((x.shape[0], Wq.shape[0]), dtype=torch.bfloat16, device=x.device)
+        y = torch.empty((_rows(x, "x")[0], _rows(Wq, "Wq")[0]), dtype=torch.bfloat16, device=x.device)
     if ws is None:
-        ws = workspace(DG_OP_GEMV_A4W4, x.shape[0], Wq.shape[0], x.shape[1], device=x.device)
+        M, K = _rows(x, "x")
+        ws = workspace(DG_OP_GEMV_A4W4, M, _rows(Wq, "Wq")[0], K, device=x.device)
     if choice is not None and not isinstance(choice, Choice):
         choice = Choice.make(*choice)
     st = m.a4w4(x, Wq, sw, fmt, gx, gw, y, ws, None if choice is None else ctypes.addressof(choice))
@@ -432,9 +442,9 @@ def dg_moe_route(logits, topk, score=DG_SCORE_SOFTMAX, bias=None, n_group=1, top
             return dg_moe_route(logits, topk, score, bias, n_group, topk_group, group_top, renorm, scale, ids, w)
     m = _marshal or _load_marshal()
     if ids is None:
-        ids = torch.empty((logits.shape[0], max(topk, 0)), dtype=torch.int32, device=logits.device)
+        ids = torch.empty((_rows(logits, "logits")[0], max(topk, 0)), dtype=torch.int32, device=logits.device)
     if w is None:
-        w = torch.empty((logits.shape[0], max(topk, 0)), dtype=torch.float32, device=logits.device)
+        w = torch.empty((_rows(logits, "logits")[0], max(topk, 0)), dtype=torch.float32, device=logits.device)
     st = m.route(logits, topk, score, bias, n_group, topk_group, group_top, renorm, scale, ids, w)
     if st:
         raise DGError(st, "dg_moe_route")
@@ -450,7 +460,7 @@ def dg_logprobs(logits, tokens=None, n_top=0, scale=1.0, logprob=None, rank=None
         with torch.cuda.stream(stream):
             return dg_logprobs(logits, tokens, n_top, scale, logprob, rank, entropy, top_ids, top_logprobs)
     m = _marshal or _load_marshal()
-    M, dev = logits.shape[0], logits.device
+    M, dev = _rows(logits, "logits")[0], logits.device
     if tokens is not None:
         if logprob is None:
             logprob = torch.empty((M,), dtype=torch.float32, device=dev)
