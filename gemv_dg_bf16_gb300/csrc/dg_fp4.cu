@@ -13,8 +13,9 @@
 // The inputs are not __restrict__: loads of what the launch ahead may have written must stay
 // behind pdl_wait() and off the non-coherent path.
 // Bound: memory, 2 + 1/2 + 1/16 (or 1/32) bytes an element and direction.  24576 x 4096 in MX:
-// there 50 us and back 39, of 37.5 for the bytes each; 105 and 71 instructions for 8 elements,
-// the former's conversions keeping the ALU two thirds busy.  16 x 4096 there and back: 3.4 us.
+// there 47 us and back 38, of 37.5 for the bytes each; 103 and 71 instructions for 8 elements,
+// the former's conversions keeping the ALU 70 % busy.  In NV: there 63 us (a division a block and
+// lane, two more operations an element) and back 39, of 38.  16 x 4096 there and back: 2.5 us.
 #include "dg_fp4.cuh"
 #include "dg_internal.h"
 

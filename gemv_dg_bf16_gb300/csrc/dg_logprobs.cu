@@ -16,7 +16,10 @@
 // Bound: with many rows memory, 2 or 4 bytes a logit (2048 x 248320 bf16: 176 us, 5.8 TB/s, 85 %
 // of the copy rate; 66 % of the issue slots, 8.7 instructions a logit); with few, latencies
 // one after the other -- loads, the bound, the gathering, the cluster's join (one row of
-// 248320: 7.5 us).
+// 248320: 7.5 us).  Rows where fewer logits than alternatives are above a value that more than
+// kCand share (a mask by the type's lowest value) take a pass for each alternative: 20 of 248320
+// with three logits left 105 us for one row and 9.3 ms for 2048, against 6.7 and 166 us where
+// the mask is -inf.
 #include "dg_common.cuh"
 #include "dg_internal.h"
 

@@ -31,10 +31,11 @@
 // of ours but the tensor scales' product.  Tokens are cut into groups of up to 128, a CTA
 // (or cluster) each, by a model (a4_plan).  Outputs leave TMEM straight to memory, and a
 // K-split's ranks fold tokens, not rows.  Bound: up to some 32 rows the fixed chain (launch,
-// first load, fold: 4.9 us for 1 x 4096 x 4096, of whose 9.4 MB the bytes need 1.4); with
-// many rows neither memory nor the MMAs (512 x 24576 x 4096: 36 us, DRAM 20 %, tensor pipe
-// 38 %) but, as far as the counters tell, the 36 KB that a K-block of 128 x 128 outputs brings
-// into an SM (82 GB/s an SM on average).
+// first load, fold: 4.8 us for 1 x 4096 x 4096, of whose 9.4 MB the bytes need 1.4); with
+// many rows neither memory nor the MMAs (512 x 24576 x 4096: 36 us, DRAM 21 %, tensor pipe
+// 36 %) but a CTA's pace: alone it takes 0.30 us a K-block at 16 or 32 tokens, 0.38 at 64 and
+// 0.51 to 0.56 at 128 (NV; MX 0.25, 0.30, 0.42), 16 of which and an epilogue make each of the three
+// waves that 768 CTAs are.  What sets that pace was not measured.
 // Every mbarrier wait is bounded: on timeout the kernel flags
 // DG_DEVERR_WAIT_TIMEOUT in the workspace status word and winds down.
 #include <cuda.h>
@@ -1411,9 +1412,11 @@ struct A4Plan {
 
 // The cheapest cut by a model of what a CTA does, in units of about 10 ns, fitted on GB300 to
 // graphs of calls of 1 to 512 rows over 16 weight shapes (44 cases: the one it takes is within
-// 0.4 % of the best on average, 8 % at worst): 33 a K-block of 256 elements, whatever the token
-// group (issue and scale copies, not bytes, set a CTA's pace); kEnd the epilogue of a group; with a K-split the fold, kFold +
-// kFoldRank per rank (partials through distributed shared memory at about 25 GB/s a CTA).
+// 0.4 % of the best on average, 8 % at worst): 33 a K-block of 256 elements; kEnd the epilogue
+// of a group; with a K-split the fold, kFold + kFoldRank per rank (partials through distributed
+// shared memory at about 25 GB/s a CTA).  The constants are of calls as a whole and an earlier
+// loop: measured alone, today's K-blocks take 25 to 56 by format and token group (at the top of
+// this file), which the model does not tell apart.
 // One wave: at most 263 of the 304 CTA slots -- fuller grids leave no room for the next
 // launch's CTAs to start under this one's tail (12288 x 4096 at 16 rows: 192 CTAs 7.3 us, 288
 // 8.6).  Few rows take few, small groups and a K-split; many rows split tokens instead, and
