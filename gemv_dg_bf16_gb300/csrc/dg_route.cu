@@ -62,11 +62,14 @@ __device__ __forceinline__ float warp_max(float v)
     return r;
 }
 
-// Score of a group of experts from its best two keys (-inf: no such key).  A sum below the type's
-// range stays above -inf, which marks groups that hold no key and groups already taken.
+// Score of a group of experts from its best two keys (-inf: no such key).  NaN marks groups that
+// hold no key, and groups already taken: -inf is the score of two keys whose sum is below the
+// type's range.
+constexpr uint32_t kNoScore = 0x7fc00000u;
 __device__ __forceinline__ float group_score(float b1, float b2, int group_top)
 {
-    return group_top == 2 && b2 > -INFINITY ? fmaxf(__fadd_rn(b1, b2), -FLT_MAX) : b1;
+    if (!(b1 > -INFINITY)) return __uint_as_float(kNoScore);
+    return group_top == 2 && b2 > -INFINITY ? __fadd_rn(b1, b2) : b1;
 }
 
 template <bool F32>
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
         }
 
         if (a.n_group > 1) {
-            float gs = -INFINITY;
+            float gs = __uint_as_float(kNoScore);
             if (kSorted && a.group_shift >= 0) {
                 // The best two of the lane are its heads; merged over the group's lanes.  Then the
                 // best groups one by one, like the picks below.
@@ -233,11 +236,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
                 const int own = lane >> a.group_shift;
                 bool keep = false;
                 for (int g = 0; g < a.topk_group; ++g) {
-                    const float top = warp_max(gs);
+                    const float top = warp_max(gs);        // (NaN where no group is left: equal to none)
                     const int src = __ffs(__ballot_sync(kFull, gs == top)) - 1;
                     const bool mine = own == src >> a.group_shift;
                     keep = keep || mine;
-                    gs = mine ? -INFINITY : gs;
+                    gs = mine ? __uint_as_float(kNoScore) : gs;
                 }
 #pragma unroll
                 for (int j = 0; j < R; ++j) head[j] = keep ? head[j] : -INFINITY;

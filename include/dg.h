@@ -419,9 +419,9 @@ dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw,
  *            whose bias is -inf or NaN, which do add to the sum (+inf counts as the type's
  *            largest value)
  *   with n_group > 1 the experts are n_group equal runs; a run's score is its largest key
- *            (group_top 1) or the sum of its two largest (group_top 2; of one if it has one; a
- *            sum below the type's range is the type's lowest value), and only the topk_group
- *            best runs that hold a key keep their keys
+ *            (group_top 1) or the sum of its two largest (group_top 2; of one if it has one; -inf
+ *            where that is below the type's range), and only the topk_group best runs of those
+ *            that hold a key keep their keys
  *   ids    = the topk largest keys in descending order; equal keys (and equal runs) go to the
  *            lower index; a slot that finds none holds -1 with weight 0
  *   w      = p[ids], divided by their sum if renorm (0 where the sum is 0), times scale; the

@@ -1,7 +1,7 @@
 """Routing with biases at the type's lowest value over whole runs of experts.
 
-Two such keys sum past binary32's range; the run still holds keys, so it ranks below every run
-with larger ones and above a run without any, equal runs by the index.
+Two such keys sum past binary32's range, to -inf; the run still holds keys, so it ranks below every
+run with a larger sum and above a run without any key, equal runs by the index.
 """
 import numpy as np
 import pytest
@@ -33,4 +33,25 @@ def test_route_lowest_bias_over_whole_runs(cuda_device, E, n_group, sigmoid):
             ri, rw, _ = R.route(x.cpu().numpy(), topk, sigmoid, bias=bias.cpu().numpy(), **kw)
             # which experts, whatever the order of scores that are a rounding apart
             assert np.array_equal(np.sort(ids.cpu().numpy(), -1), np.sort(ri, -1)), (first, last, group_top)
+            assert np.allclose(np.sort(w.cpu().numpy(), -1), np.sort(rw, -1), rtol=1e-5, atol=1e-9)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,n_group", [(32, 8), (256, 8), (24, 8), (384, 8), (1024, 16)])
+def test_route_run_with_one_expert_left_ranks_above_runs_with_none(cuda_device, E, n_group, sigmoid):
+    """Its two best keys sum to the lowest value, those of a run of lowest keys to less; runs without keys come last."""
+    size = E // n_group
+    x = (torch.randint(0, 9, (4, E), generator=torch.Generator().manual_seed(E)).float() / 4).cuda()
+    x[1, :2 * size] = -float("inf")                            # two runs without keys in front
+    bias = torch.full((E,), LOW, device="cuda")
+    for live in ((n_group - 1, n_group - 2), (3, 5)):
+        b = bias.clone()
+        for k in live:
+            b[k * size + size // 2] = 0.0
+        for topk_group in (1, 2, 4, n_group):
+            topk = min(32, topk_group * size)
+            kw = dict(n_group=n_group, topk_group=topk_group, group_top=2)
+            ids, w = dg.dg_moe_route(x, topk, score=dg.DG_SCORE_SIGMOID if sigmoid else dg.DG_SCORE_SOFTMAX, bias=b, **kw)
+            ri, rw, _ = R.route(x.cpu().numpy(), topk, sigmoid, bias=b.cpu().numpy(), **kw)
+            assert np.array_equal(np.sort(ids.cpu().numpy(), -1), np.sort(ri, -1)), (live, topk_group)
             assert np.allclose(np.sort(w.cpu().numpy(), -1), np.sort(rw, -1), rtol=1e-5, atol=1e-9)
