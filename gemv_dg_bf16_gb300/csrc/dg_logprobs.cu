@@ -636,8 +636,8 @@ __global__ void __launch_bounds__(T, 1024 / T) logprobs_kernel(LpArgs a)
     auto logprob = [&](float z) {
         if (none || z == -INFINITY) return u.s != u.s ? u.s : -INFINITY;
         const float y = near ? fmaf(z, c, -u.r) : (z - big) * c;
-        if (y < kFar && l2s == l2s)        // the factor log2(e) may overflow where scale does not
-            return near ? fmaf(z, a.scale, -u.r * kLn2) : (z - big) * a.scale;
+        if (y < kFar && l2s == l2s)        // the factor log2(e) may overflow where scale does not, or z - big
+            return near ? fmaf(z, a.scale, -u.r * kLn2) : (0.5f * z - 0.5f * big) * a.scale * 2.0f;
         return (y - l2s) * kLn2;
     };
     if (tid == 0) {
