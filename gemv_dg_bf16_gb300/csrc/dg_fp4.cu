@@ -15,7 +15,7 @@
 // Bound: memory, 2 + 1/2 + 1/16 (or 1/32) bytes an element and direction.  24576 x 4096 in MX:
 // there 47 us and back 38, of 37.5 for the bytes each; 103 and 71 instructions for 8 elements,
 // the former's conversions keeping the ALU 70 % busy.  In NV: there 63 us (a division a block and
-// lane, two more operations an element) and back 39, of 38.  16 x 4096 there and back: 2.5 us.
+// lane, two more operations an element) and back 39, of 38.  16 x 4096 there and back: 2.6 us.
 #include "dg_fp4.cuh"
 #include "dg_internal.h"
 

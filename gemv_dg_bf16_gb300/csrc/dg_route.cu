@@ -13,7 +13,7 @@
 // once.  A group's best one or two are the heads of its lanes, merged by shuffles.  Warps walk
 // over the tokens with the next token's logits already on the way and the bias in registers.
 // Bound: instructions, 736 a token of 256 experts with 8 groups and 8 picks (28 of them a pick)
-// where memory would be 1 KB a token: 32768 tokens take 30 us at 67 % of the issue slots, 5 us
+// where memory would be 1 KB a token: 32768 tokens take 29 us at 68 % of the issue slots, 5 us
 // of bytes.  With one expert in 32 to a lane and the groups one after the other it took 74 us.  A
 // token alone takes 2.8 us.  Past 256 experts a lane searches its experts for each pick: 16 tokens
 // of 384 experts 3.7 us without groups and 7.0 with 8, 32768 tokens of 384 62 us and of 512 77.
