@@ -7,9 +7,12 @@ missing (there is no CPU fallback).
 """
 from ._binding import (  # noqa: F401
     DG_OP_GATE_UP_SILU, DG_OP_GEMV_BF16, DG_OP_HEAD_FP8_ARGMAX, DG_OP_MOE_W1, DG_OP_MOE_W2, DG_OP_GEMV_A8W8, DG_OP_GEMV_A4W4,
+    DG_OP_GEMV_I8,
     DG_FP4_MX, DG_FP4_NV, DG_LOGITS_BF16, DG_LOGITS_F32, DG_SCORE_SOFTMAX, DG_SCORE_SIGMOID,
     dg_fp4_scale_bytes, fp4_scale_shape, dg_quant_fp4_blockscale, dg_dequant_fp4_blockscale, dg_gemv_a4w4_blockscale,
     dg_moe_route, dg_logprobs,
+    dg_quant_i8_rowscale, dg_gemv_i8_rowscale, dg_moe_sort, dg_moe_gather, dg_moe_combine, dg_moe_combine_grad,
+    dg_logits_adjust,
     dg_gemv_a8w8_blockscale, dg_quant_a8_blockscale,
     DG_VAR_CC_BULK, DG_VAR_CC_WARP, DG_VAR_DEFAULT, DG_VAR_MMA, DG_VAR_TC, DGError,
     DG_OK, DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT, DG_ERR_UNSUPPORTED_SHAPE, DG_ERR_WORKSPACE_TOO_SMALL, DG_ERR_CUDA,

@@ -16,7 +16,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIBPATH = os.path.join(_HERE, "libdecodegemm.so")
 
-DG_OP_GEMV_BF16, DG_OP_GATE_UP_SILU, DG_OP_HEAD_FP8_ARGMAX, DG_OP_MOE_W1, DG_OP_MOE_W2, DG_OP_GEMV_A8W8, DG_OP_GEMV_A4W4 = range(7)
+DG_OP_GEMV_BF16, DG_OP_GATE_UP_SILU, DG_OP_HEAD_FP8_ARGMAX, DG_OP_MOE_W1, DG_OP_MOE_W2, DG_OP_GEMV_A8W8, DG_OP_GEMV_A4W4, DG_OP_GEMV_I8 = range(8)
 DG_VAR_DEFAULT, DG_VAR_CC_WARP, DG_VAR_CC_BULK, DG_VAR_TC, DG_VAR_MMA = range(5)
 (DG_OK, DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT, DG_ERR_UNSUPPORTED_SHAPE, DG_ERR_WORKSPACE_TOO_SMALL, DG_ERR_CUDA,
  DG_ERR_TABLE_REFUSED, DG_ERR_NO_DEVICE, DG_ERR_BAD_VARIANT) = range(9)
@@ -65,6 +65,13 @@ class RouteParams(ctypes.Structure):
     _fields_ = [("topk", ctypes.c_int32), ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32),
                 ("group_top", ctypes.c_int32), ("score", ctypes.c_int32), ("renorm", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class LogitsEdits(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("tokens", "lengths", "prompt_lengths", "repetition", "frequency",
+                                                     "presence", "bias_ids", "bias", "mask")] + \
+               [("ld_tokens", ctypes.c_int64), ("ld_mask", ctypes.c_int64), ("n_tokens", ctypes.c_int32),
+                ("n_bias", ctypes.c_int32)]
 
 
 class DGError(RuntimeError):
@@ -127,6 +134,13 @@ def lib():
     L.dg_gemv_a4w4_blockscale.argtypes = [P, P, P, P, P, P, I, I, I, I, P, Z, P, P]
     L.dg_moe_route.argtypes = [P, I, ctypes.c_int64, P, ctypes.POINTER(RouteParams), P, P, I, I, P]
     L.dg_logprobs.argtypes = [P, I, ctypes.c_int64, P, ctypes.c_float, I, P, P, P, P, P, I, I, P]
+    L.dg_quant_i8_rowscale.argtypes = [P, P, P, I, I, P]
+    L.dg_gemv_i8_rowscale.argtypes = [P, P, P, P, I, I, I, P, Z, P, P]
+    L.dg_moe_sort.argtypes = [P, P, P, P, I, I, I, P]
+    L.dg_moe_gather.argtypes = [P, P, P, I, I, I, ctypes.c_int64, P]
+    L.dg_moe_combine.argtypes = [P, P, P, P, I, I, I, I, P]
+    L.dg_moe_combine_grad.argtypes = [P, P, P, P, P, P, I, I, I, I, P]
+    L.dg_logits_adjust.argtypes = [P, I, ctypes.c_int64, P, ctypes.c_int64, ctypes.POINTER(LogitsEdits), I, I, P]
     L.dg_select.argtypes = [I, I, I, I, ctypes.POINTER(Choice)]
     L.dg_table_load.argtypes = [ctypes.c_char_p]
     L.dg_table_clear.argtypes = []
@@ -144,6 +158,8 @@ def lib():
                  "dg_moe_w2", "dg_select",
                  "dg_gemv_a8w8_blockscale", "dg_quant_a8_blockscale", "dg_quant_fp4_blockscale",
                  "dg_dequant_fp4_blockscale", "dg_gemv_a4w4_blockscale", "dg_moe_route", "dg_logprobs",
+                 "dg_quant_i8_rowscale", "dg_gemv_i8_rowscale", "dg_moe_sort", "dg_moe_gather", "dg_moe_combine",
+                 "dg_moe_combine_grad", "dg_logits_adjust",
                  "dg_table_load", "dg_table_check", "dg_sweep"):
         getattr(L, name).restype = S
     _lib = L
@@ -483,6 +499,128 @@ def dg_logprobs(logits, tokens=None, n_top=0, scale=1.0, logprob=None, rank=None
     return {"logprob": logprob, "rank": rank, "entropy": entropy, "top_ids": top_ids, "top_logprobs": top_logprobs}
 
 
+def dg_quant_i8_rowscale(x, q=None, s=None, stream=None):
+    """(q [M, K] int8 codes, s [M] fp32 scales) of the rows of x [M, K] bf16: q = rint(x 127 / max|x|)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_quant_i8_rowscale(x, q, s)
+    m = _marshal or _load_marshal()
+    if q is None:
+        q = torch.empty(_rows(x, "x"), dtype=torch.int8, device=x.device)
+    if s is None:
+        s = torch.empty((_rows(x, "x")[0],), dtype=torch.float32, device=x.device)
+    st = m.quant_i8(x, q, s)
+    if st:
+        raise DGError(st, "dg_quant_i8_rowscale")
+    return q, s
+
+
+def dg_gemv_i8_rowscale(x, Wq, sw, y=None, ws=None, choice=None, stream=None):
+    """y [M, N] bf16 = 8-bit integer product of x [M, K] (bf16, quantised per token inside the call) and
+    Wq [N, K] int8 with one fp32 scale a row, sw [N]; the sums are exact integers."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_gemv_i8_rowscale(x, Wq, sw, y, ws, choice)
+    m = _marshal or _load_marshal()
+    if y is None:
+        y = torch.empty((_rows(x, "x")[0], _rows(Wq, "Wq")[0]), dtype=torch.bfloat16, device=x.device)
+    if ws is None:
+        M, K = _rows(x, "x")
+        ws = workspace(DG_OP_GEMV_I8, M, _rows(Wq, "Wq")[0], K, device=x.device)
+    if choice is not None and not isinstance(choice, Choice):
+        choice = Choice.make(*choice)
+    st = m.i8(x, Wq, sw, y, ws, None if choice is None else ctypes.addressof(choice))
+    if st:
+        raise DGError(st, "dg_gemv_i8_rowscale")
+    return y
+
+
+def dg_moe_sort(ids, E, offsets=None, pos=None, slots=None, stream=None):
+    """(offsets [E + 1], pos [M, topk], slots [M * topk], int32): the live (token, slot) pairs of ids [M, topk]
+    int32 in the order of their experts -- where each expert's rows begin, each slot's row (-1: not live),
+    each row's slot (-1 behind the last)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_moe_sort(ids, E, offsets, pos, slots)
+    m = _marshal or _load_marshal()
+    i32 = {"dtype": torch.int32, "device": ids.device}
+    if offsets is None:
+        offsets = torch.empty((max(E, 0) + 1,), **i32)
+    if pos is None:
+        pos = torch.empty(_rows(ids, "ids"), **i32)
+    if slots is None:
+        slots = torch.empty((_rows(ids, "ids").numel(),), **i32)
+    st = m.sort(ids, E, offsets, pos, slots)
+    if st:
+        raise DGError(st, "dg_moe_sort")
+    return offsets, pos, slots
+
+
+def dg_moe_gather(x, pos, xs=None, stream=None):
+    """xs [P, K]: x [M, K] (any dtype) with each token's row at the rows pos [M, topk] of its slots.  Rows that no
+    slot names stay as they are (of a buffer made here, P = M * topk: unset)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_moe_gather(x, pos, xs)
+    m = _marshal or _load_marshal()
+    if xs is None:
+        xs = torch.empty((_rows(pos, "pos").numel(), _rows(x, "x")[1]), dtype=x.dtype, device=x.device)
+    st = m.gather(x, pos, xs)
+    if st:
+        raise DGError(st, "dg_moe_gather")
+    return xs
+
+
+def dg_moe_combine(z, pos, w=None, y=None, stream=None):
+    """y [M, N] bf16 = sum over the slots k of w[m, k] z[pos[m, k]] (w None: 1), z [P, N] bf16, w fp32.  Without
+    weights it is the gradient of dg_moe_gather."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_moe_combine(z, pos, w, y)
+    m = _marshal or _load_marshal()
+    if y is None:
+        y = torch.empty((_rows(pos, "pos")[0], _rows(z, "z")[1]), dtype=torch.bfloat16, device=z.device)
+    st = m.combine(z, pos, w, y)
+    if st:
+        raise DGError(st, "dg_moe_combine")
+    return y
+
+
+def dg_moe_combine_grad(dy, z, pos, w, dz=None, dw=None, stream=None):
+    """(dz [P, N] bf16, dw [M, topk] fp32): the gradients of dg_moe_combine(z, pos, w), given dy [M, N].  Rows of dz
+    that no slot names stay as they are (of a buffer made here: 0)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_moe_combine_grad(dy, z, pos, w, dz, dw)
+    m = _marshal or _load_marshal()
+    if dz is None:
+        dz = torch.zeros(_rows(z, "z"), dtype=torch.bfloat16, device=z.device)
+    if dw is None:
+        dw = torch.empty(_rows(pos, "pos"), dtype=torch.float32, device=z.device)
+    st = m.combine_grad(dy, z, pos, w, dz, dw)
+    if st:
+        raise DGError(st, "dg_moe_combine_grad")
+    return dz, dw
+
+
+def dg_logits_adjust(logits, tokens=None, lengths=None, prompt_lengths=None, repetition=None, frequency=None,
+                     presence=None, bias_ids=None, bias=None, mask=None, out=None, stream=None):
+    """logits [M, V] (bf16 or fp32, any row stride) with penalties for used tokens [M, L] int32 (the first
+    prompt_lengths[m] of lengths[m] are the prompt's), biases [M, B] of the entries bias_ids [M, B], and -inf
+    where bit v of mask [M, ceil(V / 32)] int32 is 0.  Into out; None: in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return dg_logits_adjust(logits, tokens, lengths, prompt_lengths, repetition, frequency, presence, bias_ids,
+                                    bias, mask, out)
+    m = _marshal or _load_marshal()
+    if out is None:
+        out = logits
+    st = m.adjust(logits, out, tokens, lengths, prompt_lengths, repetition, frequency, presence, bias_ids, bias, mask)
+    if st:
+        raise DGError(st, "dg_logits_adjust")
+    return out
+
+
 def dg_gate_up_silu(x, W_gu, out=None, ws=None, choice=None, stream=None):
     """out[M,N_half] = silu(x . W_gu[0::2]^T) * (x . W_gu[1::2]^T)."""
     M, K = x.shape
@@ -634,7 +772,8 @@ def dg_table_check(path: str, arch: str, driver_version: int, runtime_version: i
     return int(s), int(n.value), buf.value.decode()
 
 
-_OP_NAMES = ("gemv_bf16", "gate_up_silu", "head_fp8_argmax", "moe_w1_silu", "moe_w2", "gemv_a8w8", "gemv_a4w4")
+_OP_NAMES = ("gemv_bf16", "gate_up_silu", "head_fp8_argmax", "moe_w1_silu", "moe_w2", "gemv_a8w8", "gemv_a4w4",
+             "gemv_i8")
 
 
 def _bucket(M: int) -> int:

@@ -16,6 +16,7 @@
 #include "dg_cc_bulk.cuh"
 #include "dg_cc_dense.cuh"
 #include "dg_fp4.cuh"
+#include "dg_i8.cuh"
 #include "dg_internal.h"
 #include "dg_moe.cuh"
 
@@ -270,6 +271,9 @@ void default_choice(dg_op op, int M, int N, int K, dg_choice* out)
     case DG_OP_GEMV_A4W4:
         out->variant = DG_VAR_TC;          // block-scaled e2m1 MMA
         break;
+    case DG_OP_GEMV_I8:
+        out->variant = DG_VAR_TC;          // integers as binary16
+        break;
     default:
         break;
     }
@@ -366,6 +370,9 @@ size_t dg_workspace_bytes(dg_op op, int M, int N, int K, int topk)
         break;
     case DG_OP_GEMV_A4W4:
         if (M > 0 && K > 0) b = a4_workspace_bytes(M, K);
+        break;
+    case DG_OP_GEMV_I8:
+        if (M > 0 && K > 0) b = i8_workspace_bytes(M, K);
         break;
     default:
         break;
@@ -794,6 +801,37 @@ dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw,
                         reinterpret_cast<cudaStream_t>(stream));
 }
 
+constexpr int kMaxLen = fp4::kMaxLen;      // largest rows and columns of a matrix
+
+dg_status dg_quant_i8_rowscale(const void* x, int8_t* q, float* s, int M, int K, dg_stream_t stream)
+{
+    if (!x || !q || !s || M < 1 || K < 1) return DG_ERR_INVALID_ARG;
+    if (K % 16 != 0 || M > kMaxLen || K > kMaxLen) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(s)) return DG_ERR_ALIGNMENT;
+    dg_status st;
+    const DeviceInfo* dev = current_device(&st);
+    if (!dev) return st;
+    st = launch_i8_quant(dev, false, x, q, s, M, K, false, reinterpret_cast<cudaStream_t>(stream));
+    if (st == DG_OK) weights_written(reinterpret_cast<cudaStream_t>(stream));
+    return st;
+}
+
+dg_status dg_gemv_i8_rowscale(const void* x, const int8_t* Wq, const float* sw, void* y, int M, int N, int K, void* ws,
+                              size_t ws_bytes, dg_stream_t stream, const dg_choice* choice)
+{
+    if (M < 1 || M > kMaxDenseRows || N < 1 || K < 1) return DG_ERR_INVALID_ARG;
+    if (K % 16 != 0 || K > i8::kMaxK || N > kMaxLen) return DG_ERR_UNSUPPORTED_SHAPE;
+    const void* ptrs[] = {x, Wq, sw, y};
+    dg_status s = check_common(ptrs, 4, ws, ws_bytes, dg_workspace_bytes(DG_OP_GEMV_I8, M, N, K, 0));
+    if (s != DG_OK) return s;
+    const DeviceInfo* dev = current_device(&s);
+    if (!dev) return s;
+    dg_choice c;
+    if ((s = resolve_choice(DG_OP_GEMV_I8, M, N, K, choice, &c)) != DG_OK) return s;
+    if (c.variant != DG_VAR_TC) return DG_ERR_BAD_VARIANT;
+    return launch_i8_linear(dev, c, x, Wq, sw, y, M, N, K, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
 // Logits of either type: a pointer on its element's boundary, rows ld >= n elements apart.
 static dg_status check_logits(const void* logits, int type, int64_t ld, int M, int n)
 {
@@ -822,6 +860,88 @@ dg_status dg_moe_route(const void* logits, int logits_type, int64_t ld, const fl
     if (!current_device(&s)) return s;
     return launch_route(*p, logits, bias, ids, w, M, E, ld, logits_type == DG_LOGITS_F32,
                         reinterpret_cast<cudaStream_t>(stream));
+}
+
+dg_status dg_moe_sort(const int32_t* ids, int32_t* offsets, int32_t* pos, int32_t* slots, int M, int topk, int E,
+                      dg_stream_t stream)
+{
+    if (!ids || !offsets || !pos || !slots || M < 1 || topk < 1 || E < 1) return DG_ERR_INVALID_ARG;
+    if (topk > 32 || E > 1024 || static_cast<long long>(M) * topk > (1 << 30)) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (misaligned(ids, 4) || misaligned(offsets, 4) || misaligned(pos, 4) || misaligned(slots, 4)) return DG_ERR_ALIGNMENT;
+    dg_status s;
+    if (!current_device(&s)) return s;
+    return launch_moe_sort(ids, offsets, pos, slots, M, topk, E, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Rows of N bf16 at positions [M, topk].
+static dg_status check_rows(const void* const* ptrs, int n, const int32_t* pos, int M, int topk, int P, int N)
+{
+    for (int i = 0; i < n; ++i)
+        if (!ptrs[i]) return DG_ERR_INVALID_ARG;
+    if (!pos || M < 1 || topk < 1 || P < 1 || N < 1) return DG_ERR_INVALID_ARG;
+    if (topk > 32 || N % 8 != 0) return DG_ERR_UNSUPPORTED_SHAPE;
+    for (int i = 0; i < n; ++i)
+        if (!aligned16(ptrs[i])) return DG_ERR_ALIGNMENT;
+    return misaligned(pos, 4) ? DG_ERR_ALIGNMENT : DG_OK;
+}
+
+dg_status dg_moe_gather(const void* x, const int32_t* pos, void* xs, int M, int topk, int P, int64_t row_bytes,
+                        dg_stream_t stream)
+{
+    if (row_bytes < 1) return DG_ERR_INVALID_ARG;
+    if (row_bytes % 16 != 0 || row_bytes > (1 << 30)) return DG_ERR_UNSUPPORTED_SHAPE;
+    const void* ptrs[] = {x, xs};
+    dg_status s = check_rows(ptrs, 2, pos, M, topk, P, 8);
+    if (s != DG_OK) return s;
+    if (!current_device(&s)) return s;
+    return launch_moe_gather(x, pos, xs, M, topk, P, row_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dg_status dg_moe_combine(const void* z, const int32_t* pos, const float* w, void* y, int M, int topk, int P, int N,
+                         dg_stream_t stream)
+{
+    const void* ptrs[] = {z, y};
+    dg_status s = check_rows(ptrs, 2, pos, M, topk, P, N);
+    if (s != DG_OK) return s;
+    if (misaligned(w, 4)) return DG_ERR_ALIGNMENT;
+    if (!current_device(&s)) return s;
+    return launch_moe_combine(z, pos, w, y, M, topk, P, N, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dg_status dg_moe_combine_grad(const void* dy, const void* z, const int32_t* pos, const float* w, void* dz, float* dw,
+                              int M, int topk, int P, int N, dg_stream_t stream)
+{
+    const void* ptrs[] = {dy, z, dz};
+    dg_status s = check_rows(ptrs, 3, pos, M, topk, P, N);
+    if (s != DG_OK) return s;
+    if (!w || !dw) return DG_ERR_INVALID_ARG;
+    if (misaligned(w, 4) || misaligned(dw, 4)) return DG_ERR_ALIGNMENT;
+    if (!current_device(&s)) return s;
+    return launch_moe_combine_grad(dy, z, pos, w, dz, dw, M, topk, P, N, reinterpret_cast<cudaStream_t>(stream));
+}
+
+dg_status dg_logits_adjust(const void* logits, int logits_type, int64_t ld, void* out, int64_t ld_out,
+                           const dg_logits_edits* e, int M, int V, dg_stream_t stream)
+{
+    dg_status s = check_logits(logits, logits_type, ld, M, V);
+    if (s != DG_OK) return s;
+    if ((s = check_logits(out, logits_type, ld_out, M, V)) != DG_OK) return s;
+    if (!e || (out == logits && ld_out != ld && M > 1)) return DG_ERR_INVALID_ARG;
+    if (e->n_tokens < 0 || e->n_bias < 0 || (e->n_tokens > 0) != (e->tokens != nullptr) ||
+        (e->n_bias > 0) != (e->bias != nullptr) || (e->n_bias > 0) != (e->bias_ids != nullptr))
+        return DG_ERR_INVALID_ARG;
+    if (!e->tokens && (e->lengths || e->prompt_lengths || e->repetition || e->frequency || e->presence))
+        return DG_ERR_INVALID_ARG;
+    if ((e->tokens && e->ld_tokens < e->n_tokens) || (e->mask && e->ld_mask < (V - 1) / 32 + 1)) return DG_ERR_INVALID_ARG;
+    if (V > (1 << 24) || e->n_tokens > (1 << 24) || e->n_bias > 1024) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (misaligned(e->tokens, 4) || misaligned(e->lengths, 4) || misaligned(e->prompt_lengths, 4) || misaligned(e->repetition, 4) ||
+        misaligned(e->frequency, 4) || misaligned(e->presence, 4) || misaligned(e->bias_ids, 4) || misaligned(e->bias, 4) ||
+        misaligned(e->mask, 4))
+        return DG_ERR_ALIGNMENT;
+    const DeviceInfo* dev = current_device(&s);
+    if (!dev) return s;
+    return launch_logits_adjust(dev, logits, logits_type == DG_LOGITS_F32, ld, out, ld_out, *e, M, V,
+                                reinterpret_cast<cudaStream_t>(stream));
 }
 
 dg_status dg_logprobs(const void* logits, int logits_type, int64_t ld, const int64_t* tokens, float scale, int n_top,

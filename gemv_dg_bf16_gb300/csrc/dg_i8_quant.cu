@@ -1,0 +1,104 @@
+// dg_i8_quant.cu -- rows of bf16 to 8-bit integer codes with one scale a row
+// (dg_quant_i8_rowscale, and ahead of dg_gemv_i8_rowscale with the codes as binary16).
+//
+// W warps share a row and hold it in registers, 16 bytes a lane and load: one pass over
+// memory, the maximum by shuffles (and shared memory where W > 1), the codes from the registers.
+// Rows longer than W * 4096 elements are read again for the codes.  A warp a row where the rows
+// fill the GPU; few rows take four warps each, whose loads are then a quarter as many in a line.
+#include "dg_i8.cuh"
+#include "dg_internal.h"
+
+namespace dg {
+namespace {
+
+constexpr int kVec = 16;                    // 16-byte loads a thread holds
+
+struct QuantArgs {
+    const uint16_t* x;
+    uint8_t* q;                             // int8 codes, or binary16 codes
+    float* s;
+    int M, K, early;
+};
+
+template <bool HALF>
+__device__ __forceinline__ void put8(uint8_t* q, size_t at, uint4 v, const i8::RowScale& o)
+{
+    if constexpr (HALF)
+        *reinterpret_cast<uint4*>(q + 2 * at) = i8::halves8(v, o);
+    else
+        *reinterpret_cast<uint2*>(q + at) = i8::codes8(v, o);
+}
+
+template <int W, bool HALF>
+__global__ void __launch_bounds__(W < 4 ? 128 : W * 32) i8_quant_kernel(QuantArgs a)
+{
+    constexpr int kRows = W < 4 ? 4 / W : 1;                    // rows per CTA
+    __shared__ uint32_t part[W];
+    if (a.early) pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * kRows + warp / W;
+    if (row >= a.M) return;                                     // (W > 1: a CTA has one row)
+    const int nv = a.K / 8, first = (warp % W) * 32 + lane;
+    const uint16_t* x = a.x + row * a.K;
+    uint4 raw[kVec];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int v = first + i * W * 32;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (v < nv) raw[i] = ld_stream_after(x + 8 * static_cast<size_t>(v));
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) m = __vmaxu2(m, i8::amax8(raw[i]));
+#pragma unroll 1
+    for (int v = first + kVec * W * 32; v < nv; v += W * 32)
+        m = __vmaxu2(m, i8::amax8(ld_stream_after(x + 8 * static_cast<size_t>(v))));
+    m = max(m & 0xffffu, m >> 16);
+    m = __reduce_max_sync(kFull, m);
+    if constexpr (W > 1) {
+        if (lane == 0) part[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W; ++i) m = max(m, part[i]);
+    }
+    const i8::RowScale o = i8::row_scale(m);
+    const size_t at = static_cast<size_t>(row) * a.K;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int v = first + i * W * 32;
+        if (v < nv) put8<HALF>(a.q, at + 8 * static_cast<size_t>(v), raw[i], o);
+    }
+#pragma unroll 1
+    for (int v = first + kVec * W * 32; v < nv; v += W * 32)
+        put8<HALF>(a.q, at + 8 * static_cast<size_t>(v), ld_stream_after(x + 8 * static_cast<size_t>(v)), o);
+    if (first == 0) a.s[row] = o.s;
+}
+
+template <bool HALF>
+const void* quant_fn(int w)
+{
+    return w == 1   ? reinterpret_cast<const void*>(&i8_quant_kernel<1, HALF>)
+           : w == 4 ? reinterpret_cast<const void*>(&i8_quant_kernel<4, HALF>)
+                    : reinterpret_cast<const void*>(&i8_quant_kernel<16, HALF>);
+}
+
+}  // namespace
+
+dg_status launch_i8_quant(const DeviceInfo* dev, bool half, const void* x, void* q, float* s, int M, int K, bool early,
+                          cudaStream_t stream)
+{
+    int w = K <= 4096 ? 1 : K <= 16384 ? 4 : 16;
+    if (w == 1 && M < 8 * dev->sm_count && K > 1024) w = 4;
+    const int rows = w == 1 ? 4 : 1;
+    QuantArgs a{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q), s, M, K, early ? 1 : 0};
+    void* args[] = {&a};
+    if (launch_kernel(half ? quant_fn<true>(w) : quant_fn<false>(w), static_cast<unsigned>((M - 1) / rows + 1),
+                      w == 1 ? 128u : static_cast<unsigned>(w * 32), 0, stream, args, Early::kNothing) != cudaSuccess) {
+        cudaGetLastError();
+        return DG_ERR_CUDA;
+    }
+    return DG_OK;
+}
+
+}  // namespace dg

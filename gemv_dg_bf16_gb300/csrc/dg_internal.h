@@ -36,6 +36,8 @@ int tc_nsplit(const DeviceInfo* dev, int N, int K, int M, bool fixed);
 // the tensor-core kernels can keep resident, so that no launch -- inside a stream
 // capture or not -- queries the driver for its K-split.
 void tc_capacity_init(const DeviceInfo* dev);
+// Clusters of `size` (1..8) such CTAs that are resident at once, two or one a SM.
+int tc_cluster_capacity(const DeviceInfo* dev, bool two_per_sm, int size);
 size_t tc_workspace_bytes(int M, int N, int K);
 
 dg_status launch_tc(bool gate_up, const DeviceInfo* dev, const dg_choice& c, const void* x, const void* W,
@@ -68,6 +70,26 @@ size_t a4_workspace_bytes(int M, int K);
 dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const void* x, const void* Wq,
                        const void* sw, const float* gx, const float* gw, void* y, int M, int N, int K, void* ws,
                        size_t ws_bytes, cudaStream_t stream);
+
+// 8-bit integers with a scale a row: the quantisation (dg_i8_quant.cu; half: codes as binary16, for
+// the linear, which waits for them: `early`) and the linear (dg_i8_linear.cu).
+dg_status launch_i8_quant(const DeviceInfo* dev, bool half, const void* x, void* q, float* s, int M, int K, bool early,
+                          cudaStream_t stream);
+size_t i8_workspace_bytes(int M, int K);
+dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw,
+                           void* y, int M, int N, int K, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+// Pairs sorted by expert, rows there and back (dg_moe_sort.cu); edits of logits (dg_logits.cu).
+dg_status launch_moe_sort(const int32_t* ids, int32_t* offsets, int32_t* pos, int32_t* slots, int M, int topk, int E,
+                          cudaStream_t stream);
+dg_status launch_moe_gather(const void* x, const int32_t* pos, void* xs, int M, int topk, int P, int64_t row_bytes,
+                            cudaStream_t stream);
+dg_status launch_moe_combine(const void* z, const int32_t* pos, const float* w, void* y, int M, int topk, int P, int N,
+                             cudaStream_t stream);
+dg_status launch_moe_combine_grad(const void* dy, const void* z, const int32_t* pos, const float* w, void* dz, float* dw,
+                                  int M, int topk, int P, int N, cudaStream_t stream);
+dg_status launch_logits_adjust(const DeviceInfo* dev, const void* logits, bool f32, long long ld, void* out,
+                               long long ld_out, const dg_logits_edits& e, int M, int V, cudaStream_t stream);
 
 // Routing of tokens to experts (dg_route.cu) and log-probabilities (dg_logprobs.cu).
 dg_status launch_route(const dg_route_params& p, const void* logits, const float* bias, int32_t* ids, float* w,

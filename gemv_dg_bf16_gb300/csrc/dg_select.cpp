@@ -165,6 +165,7 @@ const char* op_name(int op)
     case DG_OP_MOE_W2: return "moe_w2";
     case DG_OP_GEMV_A8W8: return "gemv_a8w8";
     case DG_OP_GEMV_A4W4: return "gemv_a4w4";
+    case DG_OP_GEMV_I8: return "gemv_i8";
     default: return nullptr;
     }
 }
@@ -189,6 +190,16 @@ std::string check_choice(int op, const dg_choice& c)
 {
     if (op == DG_OP_GEMV_A8W8 && c.variant != DG_VAR_TC) return "the A8W8 linear runs on the tensor cores only";
     if (op == DG_OP_GEMV_A4W4 && c.variant != DG_VAR_TC) return "the A4W4 linear runs on the tensor cores only";
+    if (op == DG_OP_GEMV_I8) {
+        if (c.variant != DG_VAR_TC) return "the 8-bit integer linear runs on the tensor cores only";
+        const int g = c.params[1];
+        if (c.params[0] != 0 && (c.params[0] < 2 || c.params[0] > 8)) return "pipeline stages must be 2..8";
+        if (g != 0 && g != 16 && g != 32 && g != 64 && g != 128) return "tokens a CTA must be 16, 32, 64 or 128";
+        if (c.params[2] < 0 || c.params[2] > 8) return "K ranges must be 0..8";
+        for (int i = 3; i < 6; ++i)
+            if (c.params[i] != 0) return "unused tensor-core parameter set";
+        return "";
+    }
     if (c.variant == DG_VAR_TC) {
         if (c.params[0] != 0 && (c.params[0] < 2 || c.params[0] > 8)) return "pipeline stages must be 2..8";
         const bool dense = op == DG_OP_GEMV_BF16 || op == DG_OP_GATE_UP_SILU || op == DG_OP_GEMV_A8W8 ||
@@ -430,7 +441,7 @@ using namespace dg;
 
 extern "C" {
 
-int dg_selection_space(void) { return 12; }
+int dg_selection_space(void) { return 13; }
 
 const char* dg_build_id(void) { return build_id(); }
 

@@ -105,7 +105,11 @@ std::vector<dg_choice> candidates(int op, const dg_choice& def)
             if (same_choice(o, c)) return;
         out.push_back(c);
     };
-    if (def.variant == DG_VAR_TC) {
+    if (op == DG_OP_GEMV_I8) {                 // every cut gives the same bits
+        for (int tg : {0, 16, 32, 64, 128})
+            for (int ns : {0, 1, 2, 3, 4, 6, 8}) add(mk(DG_VAR_TC, 0, tg, ns));
+        for (int st = 2; st <= 8; ++st) add(mk(DG_VAR_TC, st));
+    } else if (def.variant == DG_VAR_TC) {
         for (int st = 2; st <= 8; ++st) {
             dg_choice c = mk(DG_VAR_TC, st);
             c.params[1] = def.params[1];       // the K-split rule is part of the arithmetic
@@ -191,6 +195,9 @@ struct Problem {
                                            s_, &c);
         case DG_OP_GEMV_A4W4:
             return dg_gemv_a4w4_blockscale(x.p, w, s.p, nullptr, nullptr, out.p, M, N, K, topk, ws.p, ws_bytes, s_, &c);
+        case DG_OP_GEMV_I8:
+            return dg_gemv_i8_rowscale(x.p, static_cast<const int8_t*>(w), static_cast<const float*>(s.p), out.p, M, N, K,
+                                       ws.p, ws_bytes, s_, &c);
         default:
             return DG_ERR_INVALID_ARG;
         }
@@ -221,6 +228,7 @@ dg_status setup(Problem& P, const DeviceInfo* dev)
     case DG_OP_MOE_W2:
         wbytes = size_t(P.E) * N * K; xbytes = size_t(M) * P.topk * K * 2; P.out_bytes = size_t(M) * N * 2; break;
     case DG_OP_GEMV_A4W4: wbytes = size_t(N) * K / 2; xbytes = size_t(M) * K * 2; P.out_bytes = size_t(M) * N * 2; break;
+    case DG_OP_GEMV_I8:
     case DG_OP_GEMV_A8W8: wbytes = size_t(N) * K; xbytes = size_t(M) * K * 2; P.out_bytes = size_t(M) * N * 2; break;
     default: return DG_ERR_INVALID_ARG;
     }
@@ -245,6 +253,10 @@ dg_status setup(Problem& P, const DeviceInfo* dev)
         const size_t nsc = size_t((N + 127) / 128) * ((K + 127) / 128);
         if (!P.s.alloc(nsc * 4)) return DG_ERR_CUDA;
         fill_f32<<<64, 256>>>(static_cast<float*>(P.s.p), nsc, 31, 1e-4f, 3e-4f);
+    }
+    if (P.op == DG_OP_GEMV_I8) {                    // (random bytes above: any byte is a code)
+        if (!P.s.alloc(size_t(N) * 4)) return DG_ERR_CUDA;
+        fill_f32<<<64, 256>>>(static_cast<float*>(P.s.p), size_t(N), 37, 1e-4f, 3e-4f);
     }
     if (P.op == DG_OP_GEMV_A4W4) {                  // (random code bytes above: any byte is two codes)
         const size_t n = dg_fp4_scale_bytes(N, K, P.topk);

@@ -1123,6 +1123,8 @@ void tc_capacity_init(const DeviceInfo* dev)
     }
 }
 
+int tc_cluster_capacity(const DeviceInfo* dev, bool two_per_sm, int size) { return cluster_capacity(dev, two_per_sm, size); }
+
 int tc_nsplit(const DeviceInfo* dev, int N, int K, int M, bool fixed)
 {
     const int tiles = (N + kTileRows - 1) / kTileRows;

@@ -18,7 +18,14 @@
  *                       microscaled 4-bit (e2m1) weights and activations, MX or NV block
  *                       scales, the activation quantisation inside the call (M <= 512);
  *                       dg_quant_fp4_blockscale / dg_dequant_fp4_blockscale convert
+ *   dg_gemv_i8_rowscale 8-bit integer weights and activations with a scale for each weight row
+ *                       and each token, the activation quantisation inside the call (M <= 512);
+ *                       dg_quant_i8_rowscale converts
  *   dg_moe_route        router logits to the expert ids and gate weights of the MoE calls
+ *   dg_moe_sort         (token, slot) pairs sorted by expert; dg_moe_gather takes the tokens'
+ *                       rows there, dg_moe_combine adds the experts' rows up with their gate weights,
+ *                       dg_moe_combine_grad is its gradient
+ *   dg_logits_adjust    penalties for used tokens, biases and grammar masks on logits
  *   dg_logprobs         log-probability, rank, entropy and top alternatives over logits
  *
  * plus dg_select, which maps (op, M, N, K) to a kernel variant through a
@@ -86,7 +93,8 @@ typedef enum {
     DG_OP_MOE_W2 = 4,
     DG_OP_GEMV_A8W8 = 5,
     DG_OP_GEMV_A4W4 = 6,
-    DG_OP_COUNT = 7
+    DG_OP_GEMV_I8 = 7,
+    DG_OP_COUNT = 8
 } dg_op;
 
 /* Kernel families.  One family serves one (op, M) bucket; variants inside a
@@ -159,6 +167,7 @@ const char* dg_status_str(dg_status s);
  *   MOE_W1:          N = I (expert intermediate), K = hidden, topk
  *   MOE_W2:          N = Nout (hidden), K = I, topk
  *   GEMV_A4W4:       N rows of W, K (either format)
+ *   GEMV_I8:         N rows of W, K
  * Always >= 16 (the device status word). */
 size_t dg_workspace_bytes(dg_op op, int M, int N, int K, int topk);
 
@@ -403,6 +412,29 @@ dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw,
                                   void* y, int M, int N, int K, int fmt, void* ws, size_t ws_bytes,
                                   dg_stream_t stream, const dg_choice* choice);
 
+/* Rows of bf16 to 8-bit integers with one scale a row, in binary32 (each step one correctly
+ * rounded operation, so codes and scales are defined to the last bit):
+ *   A = max(max_k |x[m,k]|, 2^-100),  q[m,k] = rint(x[m,k] * (127 / A)) in -127..127 (ties to even),
+ *   s[m] = A / 127
+ * A row with an infinity or a NaN gets codes 0 and scale NaN; an all-zero row gets codes 0.
+ * For weights the rows are output channels.  x [M, K] bf16, q [M, K] int8, s [M] fp32;
+ * K % 16 == 0, M and K up to 2^31 - 256.  Asynchronous on `stream`; a linear launched after it may read
+ * q and s as its weights. */
+dg_status dg_quant_i8_rowscale(const void* x, int8_t* q, float* s, int M, int K, dg_stream_t stream);
+
+/* Decode linear on 8-bit integers with a scale for each token and each output channel:
+ *   qx, sx  = dg_quant_i8_rowscale(x)                              (inside the call)
+ *   y[m, n] = bf16_rn( float(sum_k qx[m,k] Wq[n,k]) * (sx[m] * sw[n]) )
+ * The sum is the exact integer (32 bits), the conversion and the two products are rounded to
+ * binary32: y is defined to the last bit, whatever variant runs and however many rows share the
+ * call.  x [M, K] bf16, Wq [N, K] int8 (any value, -128 too), sw [N] fp32, y [M, N] bf16.
+ * 1 <= M <= 512, K % 16 == 0, K <= 131072, N up to 2^31 - 256.  Tensor cores only (DG_VAR_TC:
+ * params[0] stages of the weights' ring (2..8; 0 = derived), [1] most tokens a CTA takes (16, 32, 64,
+ * 128; 0 = derived), [2] ranges K is cut into (1..8; 0 = derived)).  A token with a non-finite activation
+ * gets NaN outputs.  ws: the status word, and the codes and scales of the activations. */
+dg_status dg_gemv_i8_rowscale(const void* x, const int8_t* Wq, const float* sw, void* y, int M, int N, int K, void* ws,
+                              size_t ws_bytes, dg_stream_t stream, const dg_choice* choice);
+
 /* Element type of the logits that dg_moe_route and dg_logprobs read.  For these two calls the
  * pointers need their element's alignment only, and row m of the logits starts at
  * logits + m * ld elements (ld >= the row's length). */
@@ -440,6 +472,74 @@ typedef struct {
 } dg_route_params;
 dg_status dg_moe_route(const void* logits, int logits_type, int64_t ld, const float* bias, const dg_route_params* p,
                        int32_t* ids, float* w, int M, int E, dg_stream_t stream);
+
+/* (token, slot) pairs sorted by expert, for batches that dg_moe_w1_silu does not take.  Slot
+ * (m, k) is live as in the MoE calls: 0 <= ids[m, k] < E and no earlier slot of token m names the
+ * same expert.  Live slots are ordered by expert, those of one expert by m, then k:
+ *   offsets[e] .. offsets[e + 1] - 1   the rows of expert e (offsets[E]: all live slots)
+ *   pos[m, k]    the row of slot (m, k); -1 where it is not live
+ *   slots[p]     the slot m * topk + k of row p; -1 from row offsets[E] on
+ * ids [M, topk] int32 (dg_moe_route's), offsets [E + 1], pos [M, topk], slots [M * topk] int32,
+ * none of them overlapping.  1 <= topk <= 32, 1 <= E <= 1024, M >= 1, M * topk <= 2^30. */
+dg_status dg_moe_sort(const int32_t* ids, int32_t* offsets, int32_t* pos, int32_t* slots, int M, int topk, int E,
+                      dg_stream_t stream);
+
+/* xs[pos[m, k]] = x[m]: every token's row at the rows of its slots.  Rows of row_bytes bytes of
+ * any type (a multiple of 16); x [M] rows, xs [P] rows.  Positions outside [0, P) are skipped, rows of
+ * xs that no slot names stay as they are; the positions inside are distinct (dg_moe_sort's are).
+ * The gradient of x is dg_moe_combine of the gradient of xs without weights.
+ * 1 <= topk <= 32, M and P >= 1, row_bytes <= 2^30. */
+dg_status dg_moe_gather(const void* x, const int32_t* pos, void* xs, int M, int topk, int P, int64_t row_bytes,
+                        dg_stream_t stream);
+
+/* y[m] = bf16_rn( sum_k w[m, k] * z[pos[m, k]] ): the experts' rows added up with the gate
+ * weights, in binary32, slots in ascending order by fused multiply-add from 0.  Positions
+ * outside [0, P) add nothing; a token without any gets 0.  z [P, N] bf16, w [M, topk] fp32
+ * (NULL: 1), y [M, N] bf16.  N % 8 == 0, 1 <= topk <= 32, M and P >= 1. */
+dg_status dg_moe_combine(const void* z, const int32_t* pos, const float* w, void* y, int M, int topk, int P, int N,
+                         dg_stream_t stream);
+
+/* The gradients of dg_moe_combine with respect to z and w, given that of y:
+ *   dz[pos[m, k]] = bf16_rn( w[m, k] * dy[m] )      rows that no slot names stay as they are
+ *   dw[m, k]      = sum_n dy[m, n] * z[pos[m, k], n]  in binary32, in a fixed order; 0 where pos is outside
+ * dy [M, N], z and dz [P, N] bf16, w and dw [M, topk] fp32.  N % 8 == 0, 1 <= topk <= 32, M and P >= 1. */
+dg_status dg_moe_combine_grad(const void* dy, const void* z, const int32_t* pos, const float* w, void* dz, float* dw,
+                              int M, int topk, int P, int N, dg_stream_t stream);
+
+/* What dg_logits_adjust does to logits x [M, V], for each row m and entry v, in binary32 with one
+ * rounding to the logits' type at the end (each step one rounded operation, in this order):
+ *   used tokens   tokens[m, 0 .. lengths[m] - 1]: the prompt's, prompt_lengths[m] of them, then those that
+ *                 the sequence has made.  With c(v) how often v is among the latter:
+ *     repetition  v anywhere in the list:  x = x > 0 ? x / repetition[m] : x * repetition[m]
+ *     frequency   c(v) > 0:                x = x - frequency[m] * c(v)
+ *     presence    c(v) > 0:                x = x - presence[m]
+ *   biases        v among bias_ids[m]:     x = x + the sum of its biases in the list's order
+ *   mask          bit v of the row is 0:   x = -inf  (bit v % 32 of word v / 32; every row may be all 0)
+ * Ids outside [0, V) are ignored (-1 pads a list).  Entries that none of it names keep their bits.
+ * tokens [M, n_tokens] int32, rows ld_tokens elements apart; lengths and prompt_lengths [M] int32
+ * (NULL: n_tokens, and 0), taken into 0 .. n_tokens and 0 .. lengths[m]; repetition (> 0), frequency,
+ * presence [M] fp32, each or NULL; bias_ids int32 and bias fp32 [M, n_bias], both or neither;
+ * mask [M, ceil(V / 32)] 32-bit words, rows ld_mask words apart, or NULL.
+ * Without tokens (NULL, n_tokens 0) lengths, prompt_lengths and the three penalties are NULL. */
+typedef struct {
+    const int32_t* tokens;
+    const int32_t* lengths;
+    const int32_t* prompt_lengths;
+    const float* repetition;
+    const float* frequency;
+    const float* presence;
+    const int32_t* bias_ids;
+    const float* bias;
+    const int32_t* mask;
+    int64_t ld_tokens, ld_mask;
+    int32_t n_tokens, n_bias;
+} dg_logits_edits;
+
+/* out = logits with the edits; out == logits (and ld_out == ld) works in place, where only what changes
+ * is written; otherwise the two do not overlap.  logits and out [M, V] of one type (ld, ld_out), on
+ * their element's boundary.  1 <= V <= 2^24, M >= 1, 0 <= n_tokens <= 2^24, 0 <= n_bias <= 1024. */
+dg_status dg_logits_adjust(const void* logits, int logits_type, int64_t ld, void* out, int64_t ld_out,
+                           const dg_logits_edits* edits, int M, int V, dg_stream_t stream);
 
 /* Log-probabilities over logits (those of dg_head_fp8_argmax, or a prompt's).  With
  * z = scale * x (scale > 0: one over the temperature) and lse = log sum exp z:
