@@ -56,7 +56,8 @@ def _gpu(e):
 @pytest.mark.parametrize("dtype", [BF, torch.float32])
 @pytest.mark.parametrize("M,V,L,B,mask", [(1, 1, 3, 1, True), (1, 31, 9, 2, True), (3, 33, 0, 0, True), (2, 500, 40, 0, False), (5, 517, 0, 9, False),
                                           (4, 2048, 100, 30, True), (7, 4099, 300, 17, True), (1, 40003, 2000, 50, True), (40, 20000, 64, 5, True),
-                                          (330, 1003, 20, 3, True), (2, 100003, 900, 300, False)])
+                                          (330, 1003, 20, 3, True), (2, 100003, 900, 300, False), (1400, 1003, 20, 3, True), (1300, 2000, 5, 70, False),
+                                          (90, 24000, 300, 1024, True), (700, 3001, 500, 0, True), (40, 40001, 0, 9, True), (3, 2001, 9000, 5, True)])
 def test_every_entry(dtype, M, V, L, B, mask):
     x, e = _x(M, V, dtype, M + V), _edits(M, V, L, B, mask, M + V)
     want = R.adjust(R.f32(x), **e)
