@@ -272,7 +272,8 @@ void default_choice(dg_op op, int M, int N, int K, dg_choice* out)
         out->variant = DG_VAR_TC;          // block-scaled e2m1 MMA
         break;
     case DG_OP_GEMV_I8:
-        out->variant = DG_VAR_TC;          // integers as binary16
+        // dp4a for few tokens whose codes fit in shared memory, else integers as binary16
+        out->variant = i8_cc_takes(M, K) ? DG_VAR_CC_WARP : DG_VAR_TC;
         break;
     default:
         break;
@@ -828,6 +829,7 @@ dg_status dg_gemv_i8_rowscale(const void* x, const int8_t* Wq, const float* sw, 
     if (!dev) return s;
     dg_choice c;
     if ((s = resolve_choice(DG_OP_GEMV_I8, M, N, K, choice, &c)) != DG_OK) return s;
+    if (c.variant == DG_VAR_CC_WARP) return launch_i8_cc(dev, c, x, Wq, sw, y, M, N, K, reinterpret_cast<cudaStream_t>(stream));
     if (c.variant != DG_VAR_TC) return DG_ERR_BAD_VARIANT;
     return launch_i8_linear(dev, c, x, Wq, sw, y, M, N, K, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -6,18 +6,19 @@
 // binary16 numbers, exactly (dg_i8.cuh).  The activations are quantised to binary16 codes
 // ahead (i8_quant_kernel); the weights stay bytes until they are in the SM.
 //
-// Swap-AB: a CTA owns a tile of 128 weight rows (the MMA's M), a group of up to MP tokens (its
-// N) and a range of 128-element blocks of K.
+// Swap-AB: a CTA owns a tile of 128 weight rows (the MMA's M), a group of up to MP tokens (its N) and a range of
+// 128-element blocks of K.
 //   warp 0      streams the weights: 128 x 128 bytes a stage by TMA (128-byte swizzle)
 //   warp 1      allocates tensor memory; one elected lane issues tcgen05.mma, 8 of K = 16 a block
-//   warps 2-5   convert: a lane takes one weight row's 128 bytes from shared memory, turns
-//               them into binary16 and stores them in tensor memory, where the MMA reads A
-//               (two buffers of 64 columns)
-//   warps 6-9   epilogue: every 1024 elements the accumulator (two of them) is taken out of tensor
+//   warps 2-9   convert: a lane takes one weight row's 128 bytes from shared memory, turns
+//               them into binary16 and stores them in tensor memory, where the MMA reads A; four
+//               warps take the even blocks, four the odd ones, each with a buffer of 64 columns
+//   warps 10-13 epilogue: every 1024 elements the accumulator (two of them) is taken out of tensor
 //               memory, as integers, and added up; then scaled and stored, or folded
-//   warp 10     streams the activations: two MP x 64 boxes of binary16 a stage
-// The CTAs of a K split form a cluster: each parks its integers in shared memory, and each folds a
-// share of the tokens over all ranks.
+//   warp 14     streams the activations: two boxes of 64 elements, binary16, a stage
+// The CTAs of a K split form a cluster; each folds a share of the tokens, and the others write their integers of
+// these into its shared memory.  Outputs leave through shared memory, where all the warps but three share them: by the
+// epilogue warps alone, a token at a time, 128 tokens took 5 us a tile.
 // Every wait is bounded: on timeout the kernel flags DG_DEVERR_WAIT_TIMEOUT and winds down.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -34,14 +35,16 @@ namespace {
 constexpr int kTileRows = 128;                     // MMA M
 constexpr int kBlock = 128;                        // K elements a stage: one swizzled row of bytes
 constexpr int kWBox = kTileRows * kBlock;          // 16 KB
-constexpr int kThreads = 352;
-constexpr int kMaxRanks = 8;
+constexpr int kThreads = 480;
+constexpr int kConvert = 2, kEpilogue = 10, kStreamX = 14;     // first warps of the roles
 constexpr int kSegBlocks = i8::kSegment / kBlock;
 constexpr int kACols = kBlock / 2;                 // tensor-memory columns of a converted block
+constexpr int kMaxRanks = 8;
 
 struct I8Args {
     int N, K, M;
-    int nsplit, nkb, groups;
+    int nkb, groups, mp;                           // blocks of K, token groups, tokens of a group (a multiple of 16)
+    int nsplit, share;                             // ranks of a K split; tokens that each folds (a multiple of 4)
     int sw_stages, sx_stages;
     const float* sx;                               // [M], written ahead
     const float* sw;                               // [N]
@@ -69,11 +72,17 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t local_addr, uint32_t ra
     return r;
 }
 
-__device__ __forceinline__ int4 ld_dsmem_s32x4(uint32_t addr)
+// Four integers into the shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_cluster(uint32_t addr, int a, int b, int c, int d)
 {
-    int4 v;
-    asm("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
+    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Both barriers' phases complete (the two tests in flight at once; then the bounded waits).
+__device__ __forceinline__ bool wait_both(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, volatile int* abort_flag)
+{
+    const bool r0 = tc::bar_try(b0, p0), r1 = tc::bar_try(b1, p1);
+    return (r0 || tc::bar_wait(b0, p0, abort_flag)) && (r1 || tc::bar_wait(b1, p1, abort_flag));
 }
 
 // kind::f16 with binary16 A (tensor memory) and B (shared memory), fp32 accumulate, M = 128, N = n.
@@ -92,51 +101,36 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, u
         : "memory");
 }
 
-// Four consecutive rows n.. of token t.
-__device__ __forceinline__ void store4(const I8Args& a, int t, int n, int4 v, float sx)
-{
-    uint16_t* dst = a.y + static_cast<size_t>(t) * a.N + n;
-    const int s[4] = {v.x, v.y, v.z, v.w};
-    if (n + 3 < a.N && (a.N % 4) == 0) {
-        uint16_t h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = i8::output(s[i], sx, a.sw[n + i]);
-        *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16));
-    } else {
-        for (int i = 0; i < 4; ++i)
-            if (n + i < a.N) dst[i] = i8::output(s[i], sx, a.sw[n + i]);
-    }
-}
-
+// MP: the most tokens of a group that this instance takes.
 template <int MP>
 __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, I8Args a)
 {
-    constexpr int kXBox = MP * 128, kXStage = 2 * kXBox;
     constexpr uint32_t kA0 = 2 * MP < 64 ? 64 : 2 * MP;             // first column of the converted blocks
     constexpr uint32_t kCols = MP <= 64 ? 256 : 512;               // two accumulators, two converted blocks
     static_assert(kA0 + 2 * kACols <= kCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int SW = a.sw_stages, SX = a.sx_stages;
+    const int SW = a.sw_stages, SX = a.sx_stages, xbox = a.mp * 128, xstage = 2 * xbox;
     uint8_t* xring = smem + SW * kWBox;
-    float* sxs = reinterpret_cast<float*>(xring + SX * kXStage);    // [MP]
+    float* sxs = reinterpret_cast<float*>(xring + SX * xstage);     // [MP]
     uint64_t* bars = reinterpret_cast<uint64_t*>(sxs + MP);
-    const int nbars = 2 * SW + 2 * SX + 8;
+    const int nbars = 2 * SW + 2 * SX + 6;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + nbars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-    const uint32_t wfull = tc::su32(bars), wempty = wfull + 8 * SW, xfull = wempty + 8 * SW, xempty = xfull + 8 * SX;
-    const uint32_t afull = xempty + 8 * SX, aempty = afull + 16, dfull = aempty + 16, dempty = dfull + 16;
+    // done[i % SX]: block i is multiplied, its activations' slot and its converted weights' buffer are free
+    const uint32_t wfull = tc::su32(bars), wempty = wfull + 8 * SW, xfull = wempty + 8 * SW, done = xfull + 8 * SX;
+    const uint32_t afull = done + 8 * SX, dfull = afull + 16, dempty = dfull + 16;
+    int* fold = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + nbars * 8 + 16);   // [rank][share / 4][row][4]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool clustered = a.nsplit > 1;
-    const int split = clustered ? static_cast<int>(cluster_rank()) : 0;
-    const int unit = static_cast<int>(blockIdx.x) / a.nsplit;
-    // groups of one tile run side by side, so the tile's weights come from memory once
-    const int tile = unit / a.groups, group = unit - tile * a.groups;
-    const int t0 = group * MP, rows_here = min(MP, a.M - t0);
-    const int kb0 = static_cast<int>(static_cast<long long>(split) * a.nkb / a.nsplit);
-    const int nkb = static_cast<int>(static_cast<long long>(split + 1) * a.nkb / a.nsplit) - kb0;
+    const bool split = a.nsplit > 1;
+    const int rank = split ? static_cast<int>(cluster_rank()) : 0;
+    // groups of one tile run side by side, so that its weights come from memory once
+    const int unit = static_cast<int>(blockIdx.x) / a.nsplit, tile = unit / a.groups, group = unit % a.groups;
+    const int t0 = group * a.mp, rows_here = min(a.mp, a.M - t0);
+    const int kb0 = static_cast<int>(static_cast<long long>(rank) * a.nkb / a.nsplit);
+    const int n = static_cast<int>(static_cast<long long>(rank + 1) * a.nkb / a.nsplit) - kb0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < SW; ++s) {
@@ -145,11 +139,10 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
         }
         for (int s = 0; s < SX; ++s) {
             tc::bar_init(xfull + 8 * s, 1);
-            tc::bar_init(xempty + 8 * s, 1);
+            tc::bar_init(done + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             tc::bar_init(afull + 8 * b, 4);
-            tc::bar_init(aempty + 8 * b, 1);
             tc::bar_init(dfull + 8 * b, 1);
             tc::bar_init(dempty + 8 * b, 4);                        // one per epilogue warp
         }
@@ -167,6 +160,10 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
     tc::fence_after();
     const uint32_t tmem = *tmem_holder;
     pdl_launch_dependents();
+    if (split) {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // (waited for in front of the first remote access)
+    }
 
     // After a wait that ran out: the copies in flight of a ring whose last `issued` loads went round
     // `stages` slots are waited for, again with a limit, before the CTA may leave.
@@ -178,67 +175,91 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
 
     const int q = warp & 3;                                         // tensor-memory lane quarter
     const uint32_t tlane = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    int tot[MP];
     if (warp == 0) {
         if (tc::elect_one()) {
-            const uint64_t once = a.groups == 1 ? tc::policy_evict_first() : 0;
-            int i = 0;
-            for (; i < nkb; ++i) {                                  // weights: nothing to wait for
-                const int s = i % SW;
-                if (i >= SW && !tc::bar_wait(wempty + 8 * s, static_cast<uint32_t>(i / SW - 1) & 1u, abort_flag)) break;
+            const uint64_t once = tc::policy_evict_first();
+            int s = 0, i = 0;
+            uint32_t round = 0;
+            for (; i < n; ++i) {                                    // weights: nothing to wait for
+                if (round > 0 && !tc::bar_wait(wempty + 8 * s, (round - 1) & 1u, abort_flag)) break;
                 tc::bar_expect_tx(wfull + 8 * s, kWBox);
                 if (a.groups == 1)
                     tc::tma_2d_hint(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, tile * kTileRows, wfull + 8 * s, once);
                 else
                     tc::tma_2d(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, tile * kTileRows, wfull + 8 * s);
+                if (++s == SW) {
+                    s = 0;
+                    ++round;
+                }
             }
             if (*abort_flag) drain(wfull, i, SW);
         }
+        __syncwarp();                                               // (a lane in pdl_wait() holds up the whole warp)
         pdl_wait();
-    } else if (warp == 10) {
+    } else if (warp == kStreamX) {
         pdl_wait();
         if (tc::elect_one()) {
-            int i = 0;
-            for (; i < nkb; ++i) {
-                const int s = i % SX;
-                if (i >= SX && !tc::bar_wait(xempty + 8 * s, static_cast<uint32_t>(i / SX - 1) & 1u, abort_flag)) break;
-                const uint32_t dst = tc::su32(xring + s * kXStage);
-                tc::bar_expect_tx(xfull + 8 * s, kXStage);
+            int s = 0, i = 0;
+            uint32_t round = 0;
+            for (; i < n; ++i) {
+                if (round > 0 && !tc::bar_wait(done + 8 * s, (round - 1) & 1u, abort_flag)) break;
+                const uint32_t dst = tc::su32(xring + s * xstage);
+                tc::bar_expect_tx(xfull + 8 * s, static_cast<uint32_t>(xstage));
                 tc::tma_2d(dst, &tmX, (kb0 + i) * kBlock, t0, xfull + 8 * s);
-                tc::tma_2d(dst + kXBox, &tmX, (kb0 + i) * kBlock + 64, t0, xfull + 8 * s);
+                tc::tma_2d(dst + xbox, &tmX, (kb0 + i) * kBlock + 64, t0, xfull + 8 * s);
+                if (++s == SX) {
+                    s = 0;
+                    ++round;
+                }
             }
             if (*abort_flag) drain(xfull, i, SX);
         }
     } else if (warp == 1) {
         if (tc::elect_one()) {
-            for (int i = 0; i < nkb; ++i) {
-                const int s = i % SX, b = i & 1, seg = i / kSegBlocks, d = seg & 1, in = i % kSegBlocks;
-                if (!tc::bar_wait(xfull + 8 * s, static_cast<uint32_t>(i / SX) & 1u, abort_flag)) break;
-                if (!tc::bar_wait(afull + 8 * b, static_cast<uint32_t>(i / 2) & 1u, abort_flag)) break;
+            const uint32_t idesc = idesc_f16(a.mp);
+            const uint64_t half = static_cast<uint64_t>(xbox / 16);
+            int s = 0;
+            uint32_t round = 0;
+            for (int i = 0; i < n; ++i) {
+                const int b = i & 1, seg = i / kSegBlocks, d = seg & 1, in = i % kSegBlocks;
+                if (!wait_both(xfull + 8 * s, round & 1u, afull + 8 * b, static_cast<uint32_t>(i / 2) & 1u, abort_flag)) break;
                 if (in == 0 && seg >= 2 && !tc::bar_wait(dempty + 8 * d, static_cast<uint32_t>(seg / 2 - 1) & 1u, abort_flag)) break;
                 tc::fence_after();
-                const uint64_t x0 = tc::sw128_desc(tc::su32(xring + s * kXStage));
+                const uint64_t x0 = tc::sw128_desc(tc::su32(xring + s * xstage));
 #pragma unroll
                 for (int kk = 0; kk < kBlock / 16; ++kk)
                     mma_f16_ta(tmem + static_cast<uint32_t>(d * MP), tmem + kA0 + static_cast<uint32_t>(b * kACols + kk * 8),
-                               x0 + static_cast<uint64_t>((kk / 4) * (kXBox / 16) + (kk % 4) * 2), idesc_f16(MP), (in > 0 || kk > 0) ? 1u : 0u);
-                tc::commit(xempty + 8 * s);
-                tc::commit(aempty + 8 * b);
-                if (in == kSegBlocks - 1 || i == nkb - 1) tc::commit(dfull + 8 * d);
+                               x0 + (kk < 4 ? 0 : half) + static_cast<uint64_t>((kk % 4) * 2), idesc, (in > 0 || kk > 0) ? 1u : 0u);
+                tc::commit(done + 8 * s);
+                if (in == kSegBlocks - 1 || i == n - 1) tc::commit(dfull + 8 * d);
+                if (++s == SX) {
+                    s = 0;
+                    ++round;
+                }
             }
         }
+        __syncwarp();
         pdl_wait();
-    } else if (warp < 6) {
+    } else if (warp < kEpilogue) {
         // Convert: this lane's weight row, 16 bytes at a time from their swizzled places.
-        const int row = q * 32 + lane;
-        for (int i = 0; i < nkb; ++i) {
-            const int s = i % SW, b = i & 1;
-            if (!tc::bar_wait(wfull + 8 * s, static_cast<uint32_t>(i / SW) & 1u, abort_flag)) break;
+        const int row = q * 32 + lane, b = (warp - kConvert) / 4;
+        int s = b % SW, x = b;                                      // x: the activations' slot of block i - 2
+        uint32_t round = 0, xround = 0;
+#pragma unroll 1
+        for (int i = b; i < n; i += 2) {
+            if (!tc::bar_wait(wfull + 8 * s, round & 1u, abort_flag)) break;
             const uint8_t* src = smem + s * kWBox;
             uint4 raw[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + tc::sw128_offset(row, c));
-            if (i >= 2 && !tc::bar_wait(aempty + 8 * b, static_cast<uint32_t>(i / 2 - 1) & 1u, abort_flag)) break;
+            if (i >= 2) {
+                if (!tc::bar_wait(done + 8 * x, xround & 1u, abort_flag)) break;
+                x += 2;
+                if (x >= SX) {
+                    x -= SX;
+                    ++xround;
+                }
+            }
             tc::fence_after();
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
@@ -259,15 +280,21 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::bar_arrive(afull + 8 * b);
+            s += 2;
+            if (s >= SW) {
+                s -= SW;
+                ++round;
+            }
         }
         pdl_wait();
     } else {
         pdl_wait();
-        for (int t = threadIdx.x - 192; t < rows_here; t += 128) sxs[t] = ld_cg_f32(a.sx + t0 + t);
+        for (int t = threadIdx.x - kEpilogue * 32; t < rows_here; t += 128) sxs[t] = ld_cg_f32(a.sx + t0 + t);
         asm volatile("bar.sync 1, 128;" ::: "memory");
+        int tot[MP];
 #pragma unroll
         for (int j = 0; j < MP; ++j) tot[j] = 0;
-        const int nseg = (nkb + kSegBlocks - 1) / kSegBlocks;
+        const int nseg = (n + kSegBlocks - 1) / kSegBlocks;
         bool good = true;
 #pragma unroll 1
         for (int seg = 0; seg < nseg; ++seg) {
@@ -277,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
                 break;
             }
             tc::fence_after();
+            // (columns past mp hold what the other accumulator or nobody left there: they are not stored)
 #pragma unroll
             for (int c = 0; c < MP / 16; ++c) {
                 uint32_t v[16];
@@ -288,43 +316,51 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
             __syncwarp();
             if (lane == 0) tc::bar_arrive(dempty + 8 * d);
         }
-        good = good && !*abort_flag;
-        const int row = q * 32 + lane, n = tile * kTileRows + row;
-        if (good && !clustered) {
-            // A lane holds one weight row, a warp 32 of them: 64 bytes of one token's output a store.
-            const float sw = n < a.N ? a.sw[n] : 0.0f;
-            uint16_t* dst = a.y + static_cast<size_t>(t0) * a.N + n;
+        __syncwarp();
+        if (split) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");     // every rank has begun
+        // This row's integers, four tokens at a time, to the rank that folds them.
+        const int row = q * 32 + lane;
+        if (good && !*abort_flag) {
 #pragma unroll
-            for (int j = 0; j < MP; ++j)
-                if (j < rows_here && n < a.N) dst[static_cast<size_t>(j) * a.N] = i8::output(tot[j], sxs[j], sw);
-        } else if (good) {
-            int* P = reinterpret_cast<int*>(smem);                  // [token][row] in the idle weight ring
-#pragma unroll
-            for (int j = 0; j < MP; ++j)
-                if (j < rows_here) P[j * kTileRows + row] = tot[j];
-        }
-    }
-    if (clustered) {
-        cluster_sync_all();                                         // every rank's integers are in place
-        if (warp >= 6 && warp < 10 && !*abort_flag) {
-            const int lo = rows_here * split / a.nsplit, hi = rows_here * (split + 1) / a.nsplit;
-            uint32_t peer[kMaxRanks];
-#pragma unroll
-            for (int r = 0; r < kMaxRanks; ++r) peer[r] = r < a.nsplit ? map_to_rank(tc::su32(smem), r) : 0u;
-            const int n = tile * kTileRows + lane * 4;
-#pragma unroll 1
-            for (int t = lo + warp - 6; t < hi; t += 4) {
-                int4 p[kMaxRanks];
-#pragma unroll
-                for (int r = 0; r < kMaxRanks; ++r)
-                    p[r] = r < a.nsplit ? ld_dsmem_s32x4(peer[r] + static_cast<uint32_t>((t * kTileRows + lane * 4) * 4)) : make_int4(0, 0, 0, 0);
-                int4 v = p[0];
-#pragma unroll
-                for (int r = 1; r < kMaxRanks; ++r) v = make_int4(v.x + p[r].x, v.y + p[r].y, v.z + p[r].z, v.w + p[r].w);
-                store4(a, t0 + t, n, v, sxs[t]);
+            for (int j = 0; j < MP; j += 4) {
+                if (j >= a.mp) break;
+                const int to = split ? j / a.share : 0, at = ((rank * a.share + j - to * a.share) / 4 * kTileRows + row) * 4;
+                if (split)
+                    st_cluster(map_to_rank(tc::su32(fold + at), static_cast<uint32_t>(to)), tot[j], tot[j + 1], tot[j + 2], tot[j + 3]);
+                else
+                    *reinterpret_cast<int4*>(reinterpret_cast<int*>(smem) + (j / 4 * kTileRows + row) * 4) = make_int4(tot[j], tot[j + 1], tot[j + 2], tot[j + 3]);
             }
         }
-        cluster_sync_all();                                         // no rank leaves while others read its integers
+    }
+    if (split) {
+        if (warp < kEpilogue || warp >= kStreamX) {
+            __syncwarp();
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");            // (the arrival at the start)
+        }
+        cluster_sync_all();                                         // every rank's integers are in place; the last remote access
+    } else {
+        __syncthreads();
+    }
+    if (warp >= kConvert && warp < kStreamX && !*abort_flag) {
+        // A warp takes 32 rows of four tokens: a lane adds up a row's over the ranks.
+        const int lo = rank * a.share, quads = (max(0, min(rows_here - lo, a.share)) + 3) / 4;
+        const int* P = split ? fold : reinterpret_cast<const int*>(smem);
+#pragma unroll 1
+        for (int z = warp - kConvert; z < quads * 4; z += kStreamX - kConvert) {
+            const int t = lo + z / 4 * 4, row = z % 4 * 32 + lane, nrow = tile * kTileRows + row;
+            int4 v = make_int4(0, 0, 0, 0);
+            for (int r = 0; r < a.nsplit; ++r) {
+                const int4 p = *reinterpret_cast<const int4*>(P + ((r * a.share / 4 + z / 4) * kTileRows + row) * 4);
+                v = make_int4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
+            }
+            if (nrow >= a.N) continue;
+            const float sw = a.sw[nrow];
+            const int sum[4] = {v.x, v.y, v.z, v.w};
+            uint16_t* dst = a.y + static_cast<size_t>(t0 + t) * a.N + nrow;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t + j < rows_here) dst[static_cast<size_t>(j) * a.N] = i8::output(sum[j], sxs[t + j], sw);
+        }
     }
     tc::fence_before();
     __syncthreads();
@@ -363,25 +399,34 @@ bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, 
 
 const void* kernel_of(int mp)
 {
-    switch (mp) {
-    case 16: return reinterpret_cast<const void*>(&i8_tc_kernel<16>);
-    case 32: return reinterpret_cast<const void*>(&i8_tc_kernel<32>);
-    case 64: return reinterpret_cast<const void*>(&i8_tc_kernel<64>);
-    case 128: return reinterpret_cast<const void*>(&i8_tc_kernel<128>);
-    default: return nullptr;
-    }
+    return mp <= 16   ? reinterpret_cast<const void*>(&i8_tc_kernel<16>)
+           : mp <= 32 ? reinterpret_cast<const void*>(&i8_tc_kernel<32>)
+           : mp <= 64 ? reinterpret_cast<const void*>(&i8_tc_kernel<64>)
+                      : reinterpret_cast<const void*>(&i8_tc_kernel<128>);
 }
 
-size_t smem_bytes(int mp, int sw, int sx)
+// fold: bytes for the integers of a K split.
+size_t smem_bytes(int mp, int sw, int sx, size_t fold)
 {
-    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * mp * 256 + mp * 4 + (2 * sw + 2 * sx + 8) * 8 + 16;
+    const size_t most = mp <= 16 ? 16 : mp <= 32 ? 32 : mp <= 64 ? 64 : 128;
+    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * mp * 256 + most * 4 + (2 * sw + 2 * sx + 6) * 8 + 16 + fold;
+}
+
+size_t code_bytes(int M, int K) { return (static_cast<size_t>(M) * K * 2 + 255) / 256 * 256; }
+size_t scale_bytes(int M) { return (static_cast<size_t>(M) * 4 + 255) / 256 * 256; }
+
+// Tokens of a group: equal groups of up to `most`, rounded up to the MMA's 16.
+int group_tokens(int M, int most)
+{
+    const int groups = (M - 1) / most + 1;
+    return ((M - 1) / groups + 16) / 16 * 16;
 }
 
 }  // namespace
 
 size_t i8_workspace_bytes(int M, int K)
 {
-    return kWsData + (static_cast<size_t>(M) * K * 2 + 255) / 256 * 256 + (static_cast<size_t>(M) * 4 + 255) / 256 * 256;
+    return kWsData + code_bytes(M, K) + scale_bytes(M);
 }
 
 dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw, void* y,
@@ -391,43 +436,60 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     for (int i = 0; i < 6; ++i)
         if (c.params[i] < 0 || (i > 2 && c.params[i] != 0)) return DG_ERR_BAD_VARIANT;
     const int tiles = (N - 1) / kTileRows + 1, nkb = (K - 1) / kBlock + 1;
-    const int mp = c.params[1] > 0 ? c.params[1] : (M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128);
-    const void* fn = kernel_of(mp);
-    if (!fn) return DG_ERR_BAD_VARIANT;
-    const int groups = (M - 1) / mp + 1;
-    int ns = c.params[2];
-    if (ns == 0) {
-        const bool two = mp <= 32;
-        const long long units = static_cast<long long>(tiles) * groups;
-        ns = 1;
-        for (int r = 2; r <= kMaxRanks && 2 * r <= nkb; ++r)
-            if (units <= tc_cluster_capacity(dev, two, r)) ns = r;
+    if (c.params[1] % 16 != 0 || c.params[1] > 128 || c.params[2] > kMaxRanks) return DG_ERR_BAD_VARIANT;
+    int mp, groups, ns;
+    long long units;
+    // most: tokens of a group.  A K split takes the ranks that are resident at once.
+    auto cut = [&](int most) {
+        mp = c.params[1] > 0 ? c.params[1] : group_tokens(M, most);
+        if (mp > (M + 15) / 16 * 16) mp = (M + 15) / 16 * 16;
+        groups = (M - 1) / mp + 1;
+        units = static_cast<long long>(tiles) * groups;
+        ns = c.params[2] > 0 ? c.params[2] : 1;
+        if (c.params[2] == 0)
+            for (int r = 2; r <= kMaxRanks && 2 * r <= nkb; ++r)
+                if (units <= tc_cluster_capacity(dev, mp <= 32, r)) ns = r;
+        if (ns > nkb) ns = nkb;
+    };
+    cut(128);
+    if (ns > 1 && mp > 112) {                                       // no room for more tokens' integers
+        if (c.params[1] == 0)
+            cut(64);
+        else if (c.params[2] == 0)
+            ns = 1;
     }
-    if (ns < 1 || ns > kMaxRanks) return DG_ERR_BAD_VARIANT;
-    if (ns > nkb) ns = nkb;
-    const long long grid = static_cast<long long>(tiles) * groups * ns;
+    const void* fn = kernel_of(mp);
+    const long long grid = units * ns;
     if (grid > 0x7fffffffll) return DG_ERR_UNSUPPORTED_SHAPE;
-    const int stw = c.params[0] > 0 ? c.params[0] : mp <= 64 ? 5 : 4, stx = mp <= 16 ? 4 : 3;
+    const int share = ns > 1 ? (mp / 4 + ns - 1) / ns * 4 : mp;
+    const size_t fold = ns > 1 ? static_cast<size_t>(ns) * share * kTileRows * 4 : 0;
+    // Two CTAs an SM up to 32 tokens, so that the next launch's first weights come under this one's tail.
+    const size_t budget = mp <= 32 ? 112 * 1024 : kMaxDynSmem;
+    int stw = c.params[0] > 0 ? c.params[0] : 5, stx = stw + 2;
+    while (stx > 3 && smem_bytes(mp, stw, stx, fold) > budget) --stx;
+    while (c.params[0] == 0 && stw > 3 && smem_bytes(mp, stw, stx, fold) > budget) --stw;
     if (stw < 2 || stw > 8) return DG_ERR_BAD_VARIANT;
-    if (ns > 1 && static_cast<size_t>(stw) * kWBox < static_cast<size_t>(mp) * kTileRows * 4) return DG_ERR_BAD_VARIANT;
-    size_t smem = smem_bytes(mp, stw, stx);
+    // Without a split the outputs go through the weights' ring.
+    if (ns == 1 && static_cast<size_t>(stw) * kWBox < static_cast<size_t>(mp) * kTileRows * 4) return DG_ERR_BAD_VARIANT;
+    size_t smem = smem_bytes(mp, stw, stx, fold);
     // Never more CTAs on an SM than its 512 tensor-memory columns hold.
     const size_t least = mp <= 64 ? 77 * 1024 : 115 * 1024;
     if (smem < least) smem = least;
     if (smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
     if (occupancy(fn, kThreads, smem) < 1) return DG_ERR_UNSUPPORTED_SHAPE;
     uint8_t* qws = static_cast<uint8_t*>(ws) + kWsData;
-    float* sxws = reinterpret_cast<float*>(qws + (static_cast<size_t>(M) * K * 2 + 255) / 256 * 256);
     I8Args a{};
     a.N = N;
     a.K = K;
     a.M = M;
-    a.nsplit = ns;
     a.nkb = nkb;
     a.groups = groups;
+    a.mp = mp;
+    a.nsplit = ns;
+    a.share = share;
     a.sw_stages = stw;
     a.sx_stages = stx;
-    a.sx = sxws;
+    a.sx = reinterpret_cast<float*>(qws + code_bytes(M, K));
     a.sw = sw;
     a.y = static_cast<uint16_t*>(y);
     a.ws = static_cast<uint8_t*>(ws);
@@ -435,7 +497,7 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     if (!encode_2d(&tmW, Wq, static_cast<uint64_t>(K), static_cast<uint64_t>(N), kBlock, kTileRows, false) ||
         !encode_2d(&tmX, qws, static_cast<uint64_t>(K), static_cast<uint64_t>(M), 64, static_cast<uint32_t>(mp), true))
         return DG_ERR_CUDA;
-    const dg_status st = launch_i8_quant(dev, true, x, qws, sxws, M, K, true, stream);
+    const dg_status st = launch_i8_quant(dev, true, x, qws, const_cast<float*>(a.sx), M, K, true, stream);
     if (st != DG_OK) return st;
     void* args[] = {&tmW, &tmX, &a};
     cudaLaunchConfig_t cfg = {};

@@ -76,6 +76,12 @@ dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const
 dg_status launch_i8_quant(const DeviceInfo* dev, bool half, const void* x, void* q, float* s, int M, int K, bool early,
                           cudaStream_t stream);
 size_t i8_workspace_bytes(int M, int K);
+// The same for few tokens on the CUDA cores (dg_i8_cc.cu): whether a call has room, and the launcher.
+bool i8_cc_takes(int M, int K);
+dg_status launch_i8_cc(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw, void* y,
+                       int M, int N, int K, cudaStream_t stream);
+dg_status launch_i8_mw(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw, void* y,
+                       int M, int N, int K, cudaStream_t stream);
 dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw,
                            void* y, int M, int N, int K, void* ws, size_t ws_bytes, cudaStream_t stream);
 

@@ -191,10 +191,15 @@ std::string check_choice(int op, const dg_choice& c)
     if (op == DG_OP_GEMV_A8W8 && c.variant != DG_VAR_TC) return "the A8W8 linear runs on the tensor cores only";
     if (op == DG_OP_GEMV_A4W4 && c.variant != DG_VAR_TC) return "the A4W4 linear runs on the tensor cores only";
     if (op == DG_OP_GEMV_I8) {
-        if (c.variant != DG_VAR_TC) return "the 8-bit integer linear runs on the tensor cores only";
+        if (c.variant == DG_VAR_CC_WARP) {
+            for (int p : c.params)
+                if (p != 0) return "unused parameter set";
+            return "";
+        }
+        if (c.variant != DG_VAR_TC) return "no such variant of the 8-bit integer linear";
         const int g = c.params[1];
         if (c.params[0] != 0 && (c.params[0] < 2 || c.params[0] > 8)) return "pipeline stages must be 2..8";
-        if (g != 0 && g != 16 && g != 32 && g != 64 && g != 128) return "tokens a CTA must be 16, 32, 64 or 128";
+        if (g < 0 || g > 128 || g % 16 != 0) return "tokens of a group must be a multiple of 16 up to 128";
         if (c.params[2] < 0 || c.params[2] > 8) return "K ranges must be 0..8";
         for (int i = 3; i < 6; ++i)
             if (c.params[i] != 0) return "unused tensor-core parameter set";

@@ -105,8 +105,9 @@ std::vector<dg_choice> candidates(int op, const dg_choice& def)
             if (same_choice(o, c)) return;
         out.push_back(c);
     };
-    if (op == DG_OP_GEMV_I8) {                 // every cut gives the same bits
-        for (int tg : {0, 16, 32, 64, 128})
+    if (op == DG_OP_GEMV_I8) {                 // every variant and cut gives the same bits
+        add(mk(DG_VAR_CC_WARP, 0));
+        for (int tg : {0, 16, 32, 64, 96, 128})
             for (int ns : {0, 1, 2, 3, 4, 6, 8}) add(mk(DG_VAR_TC, 0, tg, ns));
         for (int st = 2; st <= 8; ++st) add(mk(DG_VAR_TC, st));
     } else if (def.variant == DG_VAR_TC) {

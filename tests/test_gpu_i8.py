@@ -77,18 +77,40 @@ def test_linear_of_ragged_and_long_shapes(M, N, K):
     _check(_x(M, K, M), *_w(N, K, N + K))
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 9, 16])
+@pytest.mark.parametrize("N,K", [(1, 16), (7, 48), (129, 144), (300, 1040), (1300, 4096), (2050, 2064), (40, 12288)])
+def test_every_family_gives_the_same_bits(M, N, K):
+    x, (w, sw) = _x(M, K, M * 7 + N), _w(N, K, N + K)
+    for variant, most in ((dg.DG_VAR_CC_WARP, 4), (dg.DG_VAR_TC, 512)):
+        if M <= most:
+            _check(x, w, sw, choice=dg.Choice.make(variant))
+
+
+def test_tokens_without_room_are_refused():
+    x, (w, sw) = _x(17, 64, 1), _w(8, 64, 2)
+    for x, K, variant in ((x, 64, dg.DG_VAR_CC_WARP), (_x(5, 64, 1), 64, dg.DG_VAR_CC_WARP), (_x(4, 65536, 1), 65536, dg.DG_VAR_CC_WARP)):
+        w, sw = _w(8, K, 2)
+        with pytest.raises(dg.DGError) as e:
+            dg.dg_gemv_i8_rowscale(x.cuda(), w.cuda(), sw.cuda(), choice=dg.Choice.make(variant))
+        assert e.value.status == dg.DG_ERR_UNSUPPORTED_SHAPE
+        _check(x, w, sw)
+
+
 def test_every_cut_gives_the_same_bits():
-    for M, N, K in ((3, 260, 2064), (40, 384, 3088), (150, 130, 1296)):
+    """Any cut of K and of the tokens, any stages."""
+    for M, N, K in ((3, 260, 2064), (40, 384, 3088), (150, 130, 1296), (512, 1000, 400)):
         x, (w, sw) = _x(M, K, M), _w(N, K, N)
         xc, wc, sc = x.cuda(), w.cuda(), sw.cuda()
         want = R.i8_linear(R.f32(x), w.numpy(), sw.numpy())
-        for tg in (0, 16, 32, 64, 128):
+        ws = dg.workspace(dg.DG_OP_GEMV_I8, M, N, K)
+        for tg in (0, 16, 32, 48, 64, 80, 112, 128):
             for ns in (0, 1, 2, 3, 5, 8):
-                for st in (0, 2, 4):
-                    if st == 2 and ns != 1 and tg in (0, 128):
-                        continue                                  # (a split parks its tile in the ring: refused)
-                    y = dg.dg_gemv_i8_rowscale(xc, wc, sc, choice=dg.Choice.make(dg.DG_VAR_TC, st, tg, ns))
+                for st in (0, 2, 3):
+                    if (st and (tg or M) > 32 * st) or (tg == 128 and M > 112 and ns > 1):
+                        continue                                  # (no room for the sums on their way out: refused)
+                    y = dg.dg_gemv_i8_rowscale(xc, wc, sc, ws=ws, choice=dg.Choice.make(dg.DG_VAR_TC, st, tg, ns))
                     np.testing.assert_array_equal(_bits(y), want, err_msg=str((M, tg, ns, st)))
+        assert dg.dg_device_status(ws) == 0
 
 
 @pytest.mark.parametrize("K", [1024, 8192, 131072])
@@ -226,7 +248,8 @@ def test_batch_invariant_mode_changes_no_bits():
 def test_bad_choices_are_refused():
     x, (w, sw) = _x(2, 64, 1), _w(8, 64, 2)
     xc, wc, sc = x.cuda(), w.cuda(), sw.cuda()
-    for bad in ((dg.DG_VAR_CC_WARP,), (dg.DG_VAR_TC, 1), (dg.DG_VAR_TC, 9), (dg.DG_VAR_TC, 0, 48), (dg.DG_VAR_TC, 0, 0, 9), (dg.DG_VAR_TC, 0, -16)):
+    for bad in ((dg.DG_VAR_CC_BULK,), (dg.DG_VAR_CC_WARP, 4, 8), (dg.DG_VAR_TC, 1), (dg.DG_VAR_TC, 9), (dg.DG_VAR_TC, 0, 40), (dg.DG_VAR_TC, 0, 144), (dg.DG_VAR_TC, 0, 0, 9), (dg.DG_VAR_TC, 0, 0, -1), (dg.DG_VAR_TC, 0, -16),
+                (dg.DG_VAR_MMA, 1), (dg.DG_VAR_TC, 0, 0, 0, 1)):
         with pytest.raises(dg.DGError) as e:
             dg.dg_gemv_i8_rowscale(xc, wc, sc, choice=dg.Choice.make(*bad))
         assert e.value.status == dg.DG_ERR_BAD_VARIANT, bad

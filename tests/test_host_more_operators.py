@@ -77,8 +77,9 @@ def test_logits_argument_errors():
 
 
 def test_i8_select_and_table(tmp_path):
-    for M in (1, 16, 100, 300, 512):
-        assert dg.dg_select(dg.DG_OP_GEMV_I8, M, 4096, 4096).variant == dg.DG_VAR_TC
+    for M, K, v in ((1, 4096, dg.DG_VAR_CC_WARP), (4, 4096, dg.DG_VAR_CC_WARP), (5, 4096, dg.DG_VAR_TC), (512, 4096, dg.DG_VAR_TC),
+                    (4, 32768, dg.DG_VAR_CC_WARP), (4, 65536, dg.DG_VAR_TC), (1, 131072, dg.DG_VAR_CC_WARP)):
+        assert dg.dg_select(dg.DG_OP_GEMV_I8, M, 4096, K).variant == v, (M, K)
 
     def check(pick):
         doc = {"format": "libdecodegemm-table",
@@ -88,9 +89,9 @@ def test_i8_select_and_table(tmp_path):
         p = tmp_path / "t.json"
         p.write_text(json.dumps(doc))
         return dg.dg_table_check(str(p), "sm_103", 13000, 13000)[0]
-    assert check({"variant": 3, "params": [4, 32, 8]}) == 0
-    for bad in ({"variant": 1, "params": [4, 8]}, {"variant": 3, "params": [9]}, {"variant": 3, "params": [0, 48]}, {"variant": 3, "params": [0, 0, 9]},
-                {"variant": 3, "params": [0, 0, 0, 1]}, {"variant": 3, "params": [-1]}):
+    assert check({"variant": 3, "params": [4, 32, 8]}) == 0 and check({"variant": 1, "params": []}) == 0
+    for bad in ({"variant": 1, "params": [4, 8]}, {"variant": 3, "params": [9]}, {"variant": 3, "params": [0, 40]}, {"variant": 3, "params": [0, 144]}, {"variant": 3, "params": [0, 0, 9]},
+                {"variant": 3, "params": [0, 0, 0, 1]}, {"variant": 3, "params": [-1]}, {"variant": 4, "params": []}):
         assert check(bad) == 6, bad
     assert B._OP_NAMES[dg.DG_OP_GEMV_I8] == "gemv_i8"
 
