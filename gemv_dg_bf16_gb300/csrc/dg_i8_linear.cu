@@ -6,19 +6,20 @@
 // binary16 numbers, exactly (dg_i8.cuh).  The activations are quantised to binary16 codes
 // ahead (i8_quant_kernel); the weights stay bytes until they are in the SM.
 //
-// Swap-AB: a CTA owns a tile of 128 weight rows (the MMA's M), a group of up to MP tokens (its N) and a range of
-// 128-element blocks of K.
+// Swap-AB: a unit is a tile of 128 weight rows (the MMA's M) with a group of up to MP tokens (its N), taken in
+// 128-element blocks of K.  Few units: a cluster of CTAs each, with a range of K a rank.  Many: persistent CTAs, one an
+// SM, take one after the other, the next one's blocks under the epilogue of the last.
 //   warp 0      streams the weights: 128 x 128 bytes a stage by TMA (128-byte swizzle)
 //   warp 1      allocates tensor memory; one elected lane issues tcgen05.mma, 8 of K = 16 a block
 //   warps 2-9   convert: a lane takes one weight row's 128 bytes from shared memory, turns
 //               them into binary16 and stores them in tensor memory, where the MMA reads A; four
-//               warps take the even blocks, four the odd ones, each with a buffer of 64 columns
+//               warps take the even blocks, four the odd ones, into a ring of 3 or 4 buffers of 64 columns (with
+//               two, each conversion waited for an MMA: 790 cycles a block at 128 tokens)
 //   warps 10-13 epilogue: every 1024 elements the accumulator (two of them) is taken out of tensor
 //               memory, as integers, and added up; then scaled and stored, or folded
 //   warp 14     streams the activations: two boxes of 64 elements, binary16, a stage
-// The CTAs of a K split form a cluster; each folds a share of the tokens, and the others write their integers of
-// these into its shared memory.  Outputs leave through shared memory, where all the warps but three share them: by the
-// epilogue warps alone, a token at a time, 128 tokens took 5 us a tile.
+// Each rank of a K split folds a share of the tokens, and the others write their integers of these into its
+// shared memory.
 // Every wait is bounded: on timeout the kernel flags DG_DEVERR_WAIT_TIMEOUT and winds down.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -40,10 +41,12 @@ constexpr int kConvert = 2, kEpilogue = 10, kStreamX = 14;     // first warps of
 constexpr int kSegBlocks = i8::kSegment / kBlock;
 constexpr int kACols = kBlock / 2;                 // tensor-memory columns of a converted block
 constexpr int kMaxRanks = 8;
+constexpr int kDone = 8;                           // blocks whose completion is told apart: more than are in flight
 
 struct I8Args {
     int N, K, M;
     int nkb, groups, mp;                           // blocks of K, token groups, tokens of a group (a multiple of 16)
+    int units;
     int nsplit, share;                             // ranks of a K split; tokens that each folds (a multiple of 4)
     int sw_stages, sx_stages;
     const float* sx;                               // [M], written ahead
@@ -101,36 +104,51 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, u
         : "memory");
 }
 
+// Whether a condition holds in all of the 128 epilogue threads (a barrier for them).
+__device__ __forceinline__ bool all_of(bool p)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(p))
+        : "memory");
+    return r != 0;
+}
+
 // MP: the most tokens of a group that this instance takes.
 template <int MP>
 __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, I8Args a)
 {
     constexpr uint32_t kA0 = 2 * MP < 64 ? 64 : 2 * MP;             // first column of the converted blocks
-    constexpr uint32_t kCols = MP <= 64 ? 256 : 512;               // two accumulators, two converted blocks
-    static_assert(kA0 + 2 * kACols <= kCols, "tensor memory");
+    constexpr uint32_t kCols = MP <= 32 ? 256 : 512;               // two accumulators, kBufs converted blocks
+    constexpr int kBufs = MP <= 32 ? 3 : 4;
+    static_assert(kA0 + kBufs * kACols <= kCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int SW = a.sw_stages, SX = a.sx_stages, xbox = a.mp * 128, xstage = 2 * xbox;
     uint8_t* xring = smem + SW * kWBox;
-    float* sxs = reinterpret_cast<float*>(xring + SX * xstage);     // [MP]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sxs + MP);
-    const int nbars = 2 * SW + 2 * SX + 6;
+    float* sxs = reinterpret_cast<float*>(xring + SX * xstage);     // [2][MP]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sxs + 2 * MP);
+    const int nbars = 2 * SW + SX + kDone + kBufs + 4 + (SX + kBufs) % 2;       // (even: 16 bytes)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + nbars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-    // done[i % SX]: block i is multiplied, its activations' slot and its converted weights' buffer are free
+    // done[i % kDone]: block i is multiplied, its activations' slot and its converted weights' buffer are free
     const uint32_t wfull = tc::su32(bars), wempty = wfull + 8 * SW, xfull = wempty + 8 * SW, done = xfull + 8 * SX;
-    const uint32_t afull = done + 8 * SX, dfull = afull + 16, dempty = dfull + 16;
+    const uint32_t afull = done + 8 * kDone, dfull = afull + 8 * kBufs, dempty = dfull + 16;
     int* fold = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + nbars * 8 + 16);   // [rank][share / 4][row][4]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool split = a.nsplit > 1;
     const int rank = split ? static_cast<int>(cluster_rank()) : 0;
-    // groups of one tile run side by side, so that its weights come from memory once
-    const int unit = static_cast<int>(blockIdx.x) / a.nsplit, tile = unit / a.groups, group = unit % a.groups;
-    const int t0 = group * a.mp, rows_here = min(a.mp, a.M - t0);
+    // Units `first`, first + stride, ...; groups of one tile run side by side, so that its weights come from memory once.
+    const int first = static_cast<int>(blockIdx.x) / a.nsplit, stride = split ? a.units : static_cast<int>(gridDim.x);
     const int kb0 = static_cast<int>(static_cast<long long>(rank) * a.nkb / a.nsplit);
-    const int n = static_cast<int>(static_cast<long long>(rank + 1) * a.nkb / a.nsplit) - kb0;
+    const int nk = static_cast<int>(static_cast<long long>(rank + 1) * a.nkb / a.nsplit) - kb0;     // blocks of a unit
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < SW; ++s) {
@@ -139,10 +157,10 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
         }
         for (int s = 0; s < SX; ++s) {
             tc::bar_init(xfull + 8 * s, 1);
-            tc::bar_init(done + 8 * s, 1);
         }
+        for (int s = 0; s < kDone; ++s) tc::bar_init(done + 8 * s, 1);
+        for (int s = 0; s < kBufs; ++s) tc::bar_init(afull + 8 * s, 4);
         for (int b = 0; b < 2; ++b) {
-            tc::bar_init(afull + 8 * b, 4);
             tc::bar_init(dfull + 8 * b, 1);
             tc::bar_init(dempty + 8 * b, 4);                        // one per epilogue warp
         }
@@ -178,63 +196,82 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
     if (warp == 0) {
         if (tc::elect_one()) {
             const uint64_t once = tc::policy_evict_first();
-            int s = 0, i = 0;
+            int s = 0, issued = 0;
             uint32_t round = 0;
-            for (; i < n; ++i) {                                    // weights: nothing to wait for
-                if (round > 0 && !tc::bar_wait(wempty + 8 * s, (round - 1) & 1u, abort_flag)) break;
-                tc::bar_expect_tx(wfull + 8 * s, kWBox);
-                if (a.groups == 1)
-                    tc::tma_2d_hint(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, tile * kTileRows, wfull + 8 * s, once);
-                else
-                    tc::tma_2d(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, tile * kTileRows, wfull + 8 * s);
-                if (++s == SW) {
-                    s = 0;
-                    ++round;
+            for (int u = first; u < a.units && !*abort_flag; u += stride) {
+                const int row = u / a.groups * kTileRows;
+                for (int i = 0; i < nk; ++i) {                      // weights: nothing to wait for
+                    if (round > 0 && !tc::bar_wait(wempty + 8 * s, (round - 1) & 1u, abort_flag)) break;
+                    tc::bar_expect_tx(wfull + 8 * s, kWBox);
+                    if (a.groups == 1)
+                        tc::tma_2d_hint(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, row, wfull + 8 * s, once);
+                    else
+                        tc::tma_2d(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, row, wfull + 8 * s);
+                    ++issued;
+                    if (++s == SW) {
+                        s = 0;
+                        ++round;
+                    }
                 }
             }
-            if (*abort_flag) drain(wfull, i, SW);
+            if (*abort_flag) drain(wfull, issued, SW);
         }
         __syncwarp();                                               // (a lane in pdl_wait() holds up the whole warp)
         pdl_wait();
     } else if (warp == kStreamX) {
         pdl_wait();
         if (tc::elect_one()) {
-            int s = 0, i = 0;
+            int s = 0, issued = 0;
             uint32_t round = 0;
-            for (; i < n; ++i) {
-                if (round > 0 && !tc::bar_wait(done + 8 * s, (round - 1) & 1u, abort_flag)) break;
-                const uint32_t dst = tc::su32(xring + s * xstage);
-                tc::bar_expect_tx(xfull + 8 * s, static_cast<uint32_t>(xstage));
-                tc::tma_2d(dst, &tmX, (kb0 + i) * kBlock, t0, xfull + 8 * s);
-                tc::tma_2d(dst + xbox, &tmX, (kb0 + i) * kBlock + 64, t0, xfull + 8 * s);
-                if (++s == SX) {
-                    s = 0;
-                    ++round;
+            for (int u = first; u < a.units && !*abort_flag; u += stride) {
+                const int t0 = u % a.groups * a.mp;
+                for (int i = 0; i < nk; ++i) {
+                    const int before = issued - SX;                 // the block that had the slot
+                    if (before >= 0 && !tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag)) break;
+                    const uint32_t dst = tc::su32(xring + s * xstage);
+                    tc::bar_expect_tx(xfull + 8 * s, static_cast<uint32_t>(xstage));
+                    tc::tma_2d(dst, &tmX, (kb0 + i) * kBlock, t0, xfull + 8 * s);
+                    tc::tma_2d(dst + xbox, &tmX, (kb0 + i) * kBlock + 64, t0, xfull + 8 * s);
+                    ++issued;
+                    if (++s == SX) {
+                        s = 0;
+                        ++round;
+                    }
                 }
             }
-            if (*abort_flag) drain(xfull, i, SX);
+            if (*abort_flag) drain(xfull, issued, SX);
         }
     } else if (warp == 1) {
         if (tc::elect_one()) {
             const uint32_t idesc = idesc_f16(a.mp);
-            const uint64_t half = static_cast<uint64_t>(xbox / 16);
-            int s = 0;
-            uint32_t round = 0;
-            for (int i = 0; i < n; ++i) {
-                const int b = i & 1, seg = i / kSegBlocks, d = seg & 1, in = i % kSegBlocks;
-                if (!wait_both(xfull + 8 * s, round & 1u, afull + 8 * b, static_cast<uint32_t>(i / 2) & 1u, abort_flag)) break;
-                if (in == 0 && seg >= 2 && !tc::bar_wait(dempty + 8 * d, static_cast<uint32_t>(seg / 2 - 1) & 1u, abort_flag)) break;
-                tc::fence_after();
-                const uint64_t x0 = tc::sw128_desc(tc::su32(xring + s * xstage));
+            const uint64_t half = static_cast<uint64_t>(xbox / 16), ring = tc::sw128_desc(tc::su32(xring));
+            int s = 0, b = 0, seg = 0, block = 0;
+            uint32_t round = 0, bround = 0;
+            for (int u = first; u < a.units && !*abort_flag; u += stride) {
+                for (int i = 0, in = 0; i < nk; ++i, ++block) {     // in: blocks of the segment so far
+                    const int d = seg & 1;
+                    if (!wait_both(xfull + 8 * s, round & 1u, afull + 8 * b, bround & 1u, abort_flag)) break;
+                    if (in == 0 && seg >= 2 && !tc::bar_wait(dempty + 8 * d, static_cast<uint32_t>(seg / 2 - 1) & 1u, abort_flag)) break;
+                    tc::fence_after();
+                    const uint64_t x0 = ring + static_cast<uint64_t>(s * (xstage / 16));
 #pragma unroll
-                for (int kk = 0; kk < kBlock / 16; ++kk)
-                    mma_f16_ta(tmem + static_cast<uint32_t>(d * MP), tmem + kA0 + static_cast<uint32_t>(b * kACols + kk * 8),
-                               x0 + (kk < 4 ? 0 : half) + static_cast<uint64_t>((kk % 4) * 2), idesc, (in > 0 || kk > 0) ? 1u : 0u);
-                tc::commit(done + 8 * s);
-                if (in == kSegBlocks - 1 || i == n - 1) tc::commit(dfull + 8 * d);
-                if (++s == SX) {
-                    s = 0;
-                    ++round;
+                    for (int kk = 0; kk < kBlock / 16; ++kk)
+                        mma_f16_ta(tmem + static_cast<uint32_t>(d * MP), tmem + kA0 + static_cast<uint32_t>(b * kACols + kk * 8),
+                                   x0 + (kk < 4 ? 0 : half) + static_cast<uint64_t>((kk % 4) * 2), idesc, (in > 0 || kk > 0) ? 1u : 0u);
+                    tc::commit(done + 8 * (block % kDone));
+                    if (++in == kSegBlocks || i == nk - 1) {
+                        tc::commit(dfull + 8 * d);
+                        in = 0;
+                        ++seg;
+                    }
+                    if (++s == SX) {
+                        s = 0;
+                        ++round;
+                    }
+                    if (++b == kBufs) {
+                        b = 0;
+                        ++bround;
+                    }
                 }
             }
         }
@@ -242,24 +279,19 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
         pdl_wait();
     } else if (warp < kEpilogue) {
         // Convert: this lane's weight row, 16 bytes at a time from their swizzled places.
-        const int row = q * 32 + lane, b = (warp - kConvert) / 4;
-        int s = b % SW, x = b;                                      // x: the activations' slot of block i - 2
-        uint32_t round = 0, xround = 0;
+        const int row = q * 32 + lane, set = (warp - kConvert) / 4;
+        const long long blocks = static_cast<long long>(nk) * ((a.units - first + stride - 1) / stride);
+        int s = set, b = set;                                       // (SW is even: the slots of a set are its own)
+        uint32_t round = 0;
 #pragma unroll 1
-        for (int i = b; i < n; i += 2) {
+        for (int i = set; i < blocks; i += 2) {
             if (!tc::bar_wait(wfull + 8 * s, round & 1u, abort_flag)) break;
             const uint8_t* src = smem + s * kWBox;
             uint4 raw[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + tc::sw128_offset(row, c));
-            if (i >= 2) {
-                if (!tc::bar_wait(done + 8 * x, xround & 1u, abort_flag)) break;
-                x += 2;
-                if (x >= SX) {
-                    x -= SX;
-                    ++xround;
-                }
-            }
+            const int before = i - kBufs;                           // the block that had the buffer
+            if (before >= 0 && !tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag)) break;
             tc::fence_after();
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
@@ -285,51 +317,81 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
                 s -= SW;
                 ++round;
             }
+            b += 2;
+            if (b >= kBufs) b -= kBufs;
         }
         pdl_wait();
     } else {
         pdl_wait();
-        for (int t = threadIdx.x - kEpilogue * 32; t < rows_here; t += 128) sxs[t] = ld_cg_f32(a.sx + t0 + t);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        int tot[MP];
-#pragma unroll
-        for (int j = 0; j < MP; ++j) tot[j] = 0;
-        const int nseg = (n + kSegBlocks - 1) / kSegBlocks;
+        const int row = q * 32 + lane, nseg = (nk + kSegBlocks - 1) / kSegBlocks;
+        int seg = 0;
         bool good = true;
 #pragma unroll 1
-        for (int seg = 0; seg < nseg; ++seg) {
-            const int d = seg & 1;
-            if (!tc::bar_wait(dfull + 8 * d, static_cast<uint32_t>(seg / 2) & 1u, abort_flag)) {
-                good = false;
-                break;
-            }
-            tc::fence_after();
-            // (columns past mp hold what the other accumulator or nobody left there: they are not stored)
+        for (int u = first, k = 0; u < a.units && good; u += stride, ++k) {
+            const int t0 = u % a.groups * a.mp, rows_here = min(a.mp, a.M - t0), nrow = u / a.groups * kTileRows + row;
+            const float sw = a.sw[min(nrow, a.N - 1)];
+            float* sxt = sxs + (k & 1) * MP;
+            for (int t = threadIdx.x - kEpilogue * 32; t < rows_here; t += 128) sxt[t] = ld_cg_f32(a.sx + t0 + t);
+            int tot[MP];
 #pragma unroll
-            for (int c = 0; c < MP / 16; ++c) {
-                uint32_t v[16];
-                tc::tmem_ld16(tlane + static_cast<uint32_t>(d * MP + c * 16), v);
+            for (int j = 0; j < MP; ++j) tot[j] = 0;
+#pragma unroll 1
+            for (int e = 0; e < nseg; ++e, ++seg) {
+                const int d = seg & 1;
+                if (!tc::bar_wait(dfull + 8 * d, static_cast<uint32_t>(seg / 2) & 1u, abort_flag)) {
+                    good = false;
+                    break;
+                }
+                tc::fence_after();
+                // (columns past mp hold what nobody wrote: they are not stored)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) tot[c * 16 + j] += __float2int_rn(__uint_as_float(v[j]));
+                for (int c = 0; c < MP / 16; ++c) {
+                    uint32_t v[16];
+                    tc::tmem_ld16(tlane + static_cast<uint32_t>(d * MP + c * 16), v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) tot[c * 16 + j] += __float2int_rn(__uint_as_float(v[j]));
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(dempty + 8 * d);
             }
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(dempty + 8 * d);
+            // A wait that ran out ends the loop in all 128 threads or in none (they meet here, and the scales are there).
+            good = all_of(good && !*abort_flag);
+            if (!good) break;
+            if (split) {
+                // This row's integers, four tokens at a time, to the rank that folds them.
+                __syncwarp();
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");        // every rank has begun
+                int to = 0, at = rank * a.share;
+                uint32_t peer = map_to_rank(tc::su32(fold), 0);
+#pragma unroll
+                for (int j = 0; j < MP; j += 4) {
+                    if (j >= a.mp) break;
+                    if (at == (rank + 1) * a.share) {
+                        at = rank * a.share;
+                        peer = map_to_rank(tc::su32(fold), static_cast<uint32_t>(++to));
+                    }
+                    st_cluster(peer + static_cast<uint32_t>((at * kTileRows + row * 4) * 4), tot[j], tot[j + 1], tot[j + 2], tot[j + 3]);
+                    at += 4;
+                }
+            } else if (nrow < a.N) {
+                // A lane holds one weight row, a warp 32 of them: 64 bytes of one token's output a store.
+                uint16_t* dst = a.y + static_cast<size_t>(t0) * a.N + nrow;
+                if (rows_here == MP) {
+#pragma unroll
+                    for (int j = 0; j < MP; ++j) dst[static_cast<size_t>(j) * a.N] = i8::output(tot[j], sxt[j], sw);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < MP; ++j) {
+                        const uint16_t v = i8::output(tot[j], sxt[j], sw);
+                        if (j < rows_here) dst[static_cast<size_t>(j) * a.N] = v;
+                    }
+                }
+            }
         }
-        __syncwarp();
-        if (split) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");     // every rank has begun
-        // This row's integers, four tokens at a time, to the rank that folds them.
-        const int row = q * 32 + lane;
-        if (good && !*abort_flag) {
-#pragma unroll
-            for (int j = 0; j < MP; j += 4) {
-                if (j >= a.mp) break;
-                const int to = split ? j / a.share : 0, at = ((rank * a.share + j - to * a.share) / 4 * kTileRows + row) * 4;
-                if (split)
-                    st_cluster(map_to_rank(tc::su32(fold + at), static_cast<uint32_t>(to)), tot[j], tot[j + 1], tot[j + 2], tot[j + 3]);
-                else
-                    *reinterpret_cast<int4*>(reinterpret_cast<int*>(smem) + (j / 4 * kTileRows + row) * 4) = make_int4(tot[j], tot[j + 1], tot[j + 2], tot[j + 3]);
-            }
+        if (split && !good) {
+            __syncwarp();
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         }
     }
     if (split) {
@@ -338,28 +400,26 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
             asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");            // (the arrival at the start)
         }
         cluster_sync_all();                                         // every rank's integers are in place; the last remote access
-    } else {
-        __syncthreads();
-    }
-    if (warp >= kConvert && warp < kStreamX && !*abort_flag) {
-        // A warp takes 32 rows of four tokens: a lane adds up a row's over the ranks.
-        const int lo = rank * a.share, quads = (max(0, min(rows_here - lo, a.share)) + 3) / 4;
-        const int* P = split ? fold : reinterpret_cast<const int*>(smem);
+        if (warp >= kConvert && warp < kStreamX && !*abort_flag) {
+            // A warp takes 32 rows, the same ones of every third four tokens: a lane adds up a row's over the ranks.
+            const int t0 = first % a.groups * a.mp, lo = rank * a.share, rows_here = min(a.mp, a.M - t0);
+            const int quads = (max(0, min(rows_here - lo, a.share)) + 3) / 4;
+            const int row = (warp - kConvert) % 4 * 32 + lane, nrow = first / a.groups * kTileRows + row;
+            const float sw = a.sw[min(nrow, a.N - 1)];
 #pragma unroll 1
-        for (int z = warp - kConvert; z < quads * 4; z += kStreamX - kConvert) {
-            const int t = lo + z / 4 * 4, row = z % 4 * 32 + lane, nrow = tile * kTileRows + row;
-            int4 v = make_int4(0, 0, 0, 0);
-            for (int r = 0; r < a.nsplit; ++r) {
-                const int4 p = *reinterpret_cast<const int4*>(P + ((r * a.share / 4 + z / 4) * kTileRows + row) * 4);
-                v = make_int4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
-            }
-            if (nrow >= a.N) continue;
-            const float sw = a.sw[nrow];
-            const int sum[4] = {v.x, v.y, v.z, v.w};
-            uint16_t* dst = a.y + static_cast<size_t>(t0 + t) * a.N + nrow;
+            for (int z = (warp - kConvert) / 4; z < quads; z += 3) {
+                int4 v = make_int4(0, 0, 0, 0);
+                for (int r = 0; r < a.nsplit; ++r) {
+                    const int4 p = *reinterpret_cast<const int4*>(fold + ((r * a.share + z * 4) * kTileRows + row * 4));
+                    v = make_int4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
+                }
+                if (nrow >= a.N) continue;
+                const int t = lo + z * 4, sum[4] = {v.x, v.y, v.z, v.w};
+                uint16_t* dst = a.y + static_cast<size_t>(t0 + t) * a.N + nrow;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (t + j < rows_here) dst[static_cast<size_t>(j) * a.N] = i8::output(sum[j], sxs[t + j], sw);
+                for (int j = 0; j < 4; ++j)
+                    if (t + j < rows_here) dst[static_cast<size_t>(j) * a.N] = i8::output(sum[j], sxs[t + j], sw);
+            }
         }
     }
     tc::fence_before();
@@ -409,7 +469,7 @@ const void* kernel_of(int mp)
 size_t smem_bytes(int mp, int sw, int sx, size_t fold)
 {
     const size_t most = mp <= 16 ? 16 : mp <= 32 ? 32 : mp <= 64 ? 64 : 128;
-    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * mp * 256 + most * 4 + (2 * sw + 2 * sx + 6) * 8 + 16 + fold;
+    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * mp * 256 + most * 8 + (2 * sw + sx + kDone + 10) * 8 + 16 + fold;
 }
 
 size_t code_bytes(int M, int K) { return (static_cast<size_t>(M) * K * 2 + 255) / 256 * 256; }
@@ -459,21 +519,24 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
             ns = 1;
     }
     const void* fn = kernel_of(mp);
-    const long long grid = units * ns;
-    if (grid > 0x7fffffffll) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (units * ns > 0x7fffffffll || units * nkb / dev->sm_count > 0x3fffffff) return DG_ERR_UNSUPPORTED_SHAPE;
+    const long long grid = ns > 1 || units < dev->sm_count ? units * ns : dev->sm_count;
     const int share = ns > 1 ? (mp / 4 + ns - 1) / ns * 4 : mp;
     const size_t fold = ns > 1 ? static_cast<size_t>(ns) * share * kTileRows * 4 : 0;
     // Two CTAs an SM up to 32 tokens, so that the next launch's first weights come under this one's tail.
     const size_t budget = mp <= 32 ? 112 * 1024 : kMaxDynSmem;
-    int stw = c.params[0] > 0 ? c.params[0] : 5, stx = stw + 2;
-    while (stx > 3 && smem_bytes(mp, stw, stx, fold) > budget) --stx;
-    while (c.params[0] == 0 && stw > 3 && smem_bytes(mp, stw, stx, fold) > budget) --stw;
-    if (stw < 2 || stw > 8) return DG_ERR_BAD_VARIANT;
-    // Without a split the outputs go through the weights' ring.
-    if (ns == 1 && static_cast<size_t>(stw) * kWBox < static_cast<size_t>(mp) * kTileRows * 4) return DG_ERR_BAD_VARIANT;
+    // An even number of weights' stages: a slot then belongs to one converting set, which sees its phases in turn.  (A set
+    // that waits for a slot's next phase while the one before, the other set's, is not complete would pass at once.)
+    int stw = c.params[0] > 0 ? c.params[0] : 6;
+    if (stw < 2 || stw > 8 || stw % 2 != 0) return DG_ERR_BAD_VARIANT;
+    int stx = kDone - 1;
+    while (stx > 4 && smem_bytes(mp, stw, stx, fold) > budget) --stx;
+    while (c.params[0] == 0 && stw > 4 && smem_bytes(mp, stw, stx, fold) > budget) stw -= 2;
+    while (stx > 2 && smem_bytes(mp, stw, stx, fold) > budget) --stx;
+    while (c.params[0] == 0 && stw > 2 && smem_bytes(mp, stw, stx, fold) > budget) stw -= 2;
     size_t smem = smem_bytes(mp, stw, stx, fold);
     // Never more CTAs on an SM than its 512 tensor-memory columns hold.
-    const size_t least = mp <= 64 ? 77 * 1024 : 115 * 1024;
+    const size_t least = mp <= 32 ? 77 * 1024 : 115 * 1024;
     if (smem < least) smem = least;
     if (smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
     if (occupancy(fn, kThreads, smem) < 1) return DG_ERR_UNSUPPORTED_SHAPE;
@@ -485,6 +548,7 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     a.nkb = nkb;
     a.groups = groups;
     a.mp = mp;
+    a.units = static_cast<int>(units);
     a.nsplit = ns;
     a.share = share;
     a.sw_stages = stw;

@@ -198,7 +198,7 @@ std::string check_choice(int op, const dg_choice& c)
         }
         if (c.variant != DG_VAR_TC) return "no such variant of the 8-bit integer linear";
         const int g = c.params[1];
-        if (c.params[0] != 0 && (c.params[0] < 2 || c.params[0] > 8)) return "pipeline stages must be 2..8";
+        if (c.params[0] != 0 && (c.params[0] < 2 || c.params[0] > 8 || c.params[0] % 2 != 0)) return "pipeline stages must be 2, 4, 6 or 8";
         if (g < 0 || g > 128 || g % 16 != 0) return "tokens of a group must be a multiple of 16 up to 128";
         if (c.params[2] < 0 || c.params[2] > 8) return "K ranges must be 0..8";
         for (int i = 3; i < 6; ++i)
