@@ -812,7 +812,7 @@ dg_status dg_quant_i8_rowscale(const void* x, int8_t* q, float* s, int M, int K,
     dg_status st;
     const DeviceInfo* dev = current_device(&st);
     if (!dev) return st;
-    st = launch_i8_quant(dev, false, x, q, s, M, K, false, reinterpret_cast<cudaStream_t>(stream));
+    st = launch_i8_quant(dev, x, q, s, M, K, 0, reinterpret_cast<cudaStream_t>(stream));
     if (st == DG_OK) weights_written(reinterpret_cast<cudaStream_t>(stream));
     return st;
 }

@@ -74,6 +74,16 @@ __device__ __forceinline__ uint4 halves8(uint4 v, const RowScale& o)
     return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
+// Where the linear's activations have element k (of K) of token t: per group of mp tokens and block of 128 elements two
+// boxes of 64 elements, mp rows of 128 bytes, each in the swizzled order in which the MMA reads shared memory -- so
+// that a block is one contiguous copy.
+__device__ __forceinline__ size_t tile_offset(int t, int k, int mp, int K)
+{
+    const int group = t / mp, row = t - group * mp, nkb = (K + 127) / 128;
+    return ((static_cast<size_t>(group) * nkb + k / 128) * 2 + (k >> 6 & 1)) * static_cast<size_t>(mp * 128) +
+           static_cast<size_t>((row >> 3) * 1024 + (row & 7) * 128 + (((k >> 3) & 7) ^ (row & 7)) * 16);
+}
+
 // Four code bytes -> two pairs of binary16: 0x6400 | (q + 128) is 1152 + q.
 __device__ __forceinline__ void to_halves(uint32_t codes, uint32_t& lo, uint32_t& hi)
 {

@@ -17,7 +17,7 @@
 //               two, each conversion waited for an MMA: 790 cycles a block at 128 tokens)
 //   warps 10-13 epilogue: every 1024 elements the accumulator (two of them) is taken out of tensor
 //               memory, as integers, and added up; then scaled and stored, or folded
-//   warp 14     streams the activations: two boxes of 64 elements, binary16, a stage
+//   warp 14     streams the activations: a block of binary16 codes a stage, which the quantisation left in one piece
 // Each rank of a K split folds a share of the tokens, and the others write their integers of these into its
 // shared memory.
 // Every wait is bounded: on timeout the kernel flags DG_DEVERR_WAIT_TIMEOUT and winds down.
@@ -49,6 +49,7 @@ struct I8Args {
     int units;
     int nsplit, share;                             // ranks of a K split; tokens that each folds (a multiple of 4)
     int sw_stages, sx_stages;
+    const uint8_t* x;                              // the activations' codes in tiles (i8::tile_offset), written ahead
     const float* sx;                               // [M], written ahead
     const float* sw;                               // [N]
     uint16_t* y;
@@ -122,7 +123,7 @@ __device__ __forceinline__ bool all_of(bool p)
 // MP: the most tokens of a group that this instance takes.
 template <int MP>
 __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
-    i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, I8Args a)
+    i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, I8Args a)
 {
     constexpr uint32_t kA0 = 2 * MP < 64 ? 64 : 2 * MP;             // first column of the converted blocks
     constexpr uint32_t kCols = MP <= 32 ? 256 : 512;               // two accumulators, kBufs converted blocks
@@ -133,7 +134,8 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
     const int SW = a.sw_stages, SX = a.sx_stages, xbox = a.mp * 128, xstage = 2 * xbox;
     uint8_t* xring = smem + SW * kWBox;
     float* sxs = reinterpret_cast<float*>(xring + SX * xstage);     // [2][MP]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sxs + 2 * MP);
+    uint16_t* stage = reinterpret_cast<uint16_t*>(sxs + 2 * MP);    // [2][16 tokens][128 rows] of outputs
+    uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 2 * 16 * kTileRows);
     const int nbars = 2 * SW + SX + kDone + kBufs + 4 + (SX + kBufs) % 2;       // (even: 16 bytes)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + nbars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -224,14 +226,13 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
             int s = 0, issued = 0;
             uint32_t round = 0;
             for (int u = first; u < a.units && !*abort_flag; u += stride) {
-                const int t0 = u % a.groups * a.mp;
-                for (int i = 0; i < nk; ++i) {
+                const uint8_t* src = a.x + (static_cast<size_t>(u % a.groups) * a.nkb + kb0) * xstage;
+                for (int i = 0; i < nk; ++i, src += xstage) {
                     const int before = issued - SX;                 // the block that had the slot
                     if (before >= 0 && !tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag)) break;
                     const uint32_t dst = tc::su32(xring + s * xstage);
                     tc::bar_expect_tx(xfull + 8 * s, static_cast<uint32_t>(xstage));
-                    tc::tma_2d(dst, &tmX, (kb0 + i) * kBlock, t0, xfull + 8 * s);
-                    tc::tma_2d(dst + xbox, &tmX, (kb0 + i) * kBlock + 64, t0, xfull + 8 * s);
+                    tc::bulk_load(dst, src, static_cast<uint32_t>(xstage), xfull + 8 * s);
                     ++issued;
                     if (++s == SX) {
                         s = 0;
@@ -343,13 +344,14 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
                     break;
                 }
                 tc::fence_after();
-                // (columns past mp hold what nobody wrote: they are not stored)
 #pragma unroll
                 for (int c = 0; c < MP / 16; ++c) {
-                    uint32_t v[16];
-                    tc::tmem_ld16(tlane + static_cast<uint32_t>(d * MP + c * 16), v);
+                    if (c < MP / 16 - 1 || a.mp == MP) {            // (an instance serves mp = MP and, from 64 on, MP - 16)
+                        uint32_t v[16];
+                        tc::tmem_ld16(tlane + static_cast<uint32_t>(d * MP + c * 16), v);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) tot[c * 16 + j] += __float2int_rn(__uint_as_float(v[j]));
+                        for (int j = 0; j < 16; ++j) tot[c * 16 + j] += __float2int_rn(__uint_as_float(v[j]));
+                    }
                 }
                 tc::fence_before();
                 __syncwarp();
@@ -374,18 +376,43 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
                     st_cluster(peer + static_cast<uint32_t>((at * kTileRows + row * 4) * 4), tot[j], tot[j + 1], tot[j + 2], tot[j + 3]);
                     at += 4;
                 }
-            } else if (nrow < a.N) {
-                // A lane holds one weight row, a warp 32 of them: 64 bytes of one token's output a store.
-                uint16_t* dst = a.y + static_cast<size_t>(t0) * a.N + nrow;
-                if (rows_here == MP) {
+            } else if (a.N % 8 == 0 && nrow - row + kTileRows <= a.N) {
+                // Sixteen tokens at a time go through shared memory, [token][row] in turn in two places, and leave 16 bytes a
+                // lane, 256 of a token's outputs side by side.  (Straight from the lanes, 64 bytes a store, 128 tokens took 3.9 us.)
 #pragma unroll
-                    for (int j = 0; j < MP; ++j) dst[static_cast<size_t>(j) * a.N] = i8::output(tot[j], sxt[j], sw);
-                } else {
+                for (int c = 0; c < MP / 16; ++c) {
+                    if (c * 16 >= rows_here) break;
+                    uint16_t* st = stage + (c & 1) * 16 * kTileRows;
+                    uint16_t v[16];                                 // (all read before the first is written: the compiler keeps their order)
 #pragma unroll
-                    for (int j = 0; j < MP; ++j) {
-                        const uint16_t v = i8::output(tot[j], sxt[j], sw);
-                        if (j < rows_here) dst[static_cast<size_t>(j) * a.N] = v;
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 sx = *reinterpret_cast<const float4*>(sxt + c * 16 + j);
+                        v[j] = i8::output(tot[c * 16 + j], sx.x, sw);
+                        v[j + 1] = i8::output(tot[c * 16 + j + 1], sx.y, sw);
+                        v[j + 2] = i8::output(tot[c * 16 + j + 2], sx.z, sw);
+                        v[j + 3] = i8::output(tot[c * 16 + j + 3], sx.w, sw);
                     }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) st[j * kTileRows + row] = v[j];
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int z = threadIdx.x - kEpilogue * 32 + h * 128, t = c * 16 + z / 16;
+                        if (t < rows_here)
+                            *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(t0 + t) * a.N + (nrow - row) + z % 16 * 8) = *reinterpret_cast<const uint4*>(st + z * 8);
+                    }
+                }
+            } else if (nrow < a.N) {
+                uint16_t* dst = a.y + static_cast<size_t>(t0) * a.N + nrow;
+#pragma unroll
+                for (int c = 0; c < MP; c += 16) {
+                    if (c >= rows_here) break;
+                    uint16_t v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = i8::output(tot[c + j], sxt[c + j], sw);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < rows_here) dst[static_cast<size_t>(c + j) * a.N] = v[j];
                 }
             }
         }
@@ -414,11 +441,13 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
                     v = make_int4(v.x + p.x, v.y + p.y, v.z + p.z, v.w + p.w);
                 }
                 if (nrow >= a.N) continue;
-                const int t = lo + z * 4, sum[4] = {v.x, v.y, v.z, v.w};
+                const int t = lo + z * 4;
+                const float4 sx = *reinterpret_cast<const float4*>(sxs + t);
+                const uint16_t out[4] = {i8::output(v.x, sx.x, sw), i8::output(v.y, sx.y, sw), i8::output(v.z, sx.z, sw), i8::output(v.w, sx.w, sw)};
                 uint16_t* dst = a.y + static_cast<size_t>(t0 + t) * a.N + nrow;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (t + j < rows_here) dst[static_cast<size_t>(j) * a.N] = i8::output(sum[j], sxs[t + j], sw);
+                    if (t + j < rows_here) dst[static_cast<size_t>(j) * a.N] = out[j];
             }
         }
     }
@@ -436,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-// 2-D tiled map, 128-byte swizzle, over bytes or binary16.
-bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer, bool half)
+// 2-D tiled map over bytes, 128-byte swizzle.
+bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer)
 {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
@@ -449,11 +478,10 @@ bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, 
     });
     if (!g_encode) return false;
     const cuuint64_t dims[2] = {inner, outer};
-    const cuuint64_t strides[1] = {inner * (half ? 2 : 1)};
+    const cuuint64_t strides[1] = {inner};
     const cuuint32_t box[2] = {box_inner, box_outer};
     const cuuint32_t estr[2] = {1, 1};
-    return g_encode(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr),
-                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -462,17 +490,19 @@ const void* kernel_of(int mp)
     return mp <= 16   ? reinterpret_cast<const void*>(&i8_tc_kernel<16>)
            : mp <= 32 ? reinterpret_cast<const void*>(&i8_tc_kernel<32>)
            : mp <= 64 ? reinterpret_cast<const void*>(&i8_tc_kernel<64>)
+           : mp <= 96 ? reinterpret_cast<const void*>(&i8_tc_kernel<96>)
                       : reinterpret_cast<const void*>(&i8_tc_kernel<128>);
 }
 
 // fold: bytes for the integers of a K split.
 size_t smem_bytes(int mp, int sw, int sx, size_t fold)
 {
-    const size_t most = mp <= 16 ? 16 : mp <= 32 ? 32 : mp <= 64 ? 64 : 128;
-    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * mp * 256 + most * 8 + (2 * sw + sx + kDone + 10) * 8 + 16 + fold;
+    const size_t most = mp <= 16 ? 16 : mp <= 32 ? 32 : mp <= 64 ? 64 : mp <= 96 ? 96 : 128;
+    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * mp * 256 + most * 8 + 2 * 16 * kTileRows * 2 + (2 * sw + sx + kDone + 10) * 8 + 16 + fold;
 }
 
-size_t code_bytes(int M, int K) { return (static_cast<size_t>(M) * K * 2 + 255) / 256 * 256; }
+// Rows of the last group of up to 128 tokens and elements of the last block are there in full.
+size_t code_bytes(int M, int K) { return (static_cast<size_t>(M) + 127) * ((static_cast<size_t>(K) + kBlock - 1) / kBlock * kBlock) * 2; }
 size_t scale_bytes(int M) { return (static_cast<size_t>(M) * 4 + 255) / 256 * 256; }
 
 // Tokens of a group: equal groups of up to `most`, rounded up to the MMA's 16.
@@ -499,7 +529,8 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     if (c.params[1] % 16 != 0 || c.params[1] > 128 || c.params[2] > kMaxRanks) return DG_ERR_BAD_VARIANT;
     int mp, groups, ns;
     long long units;
-    // most: tokens of a group.  A K split takes the ranks that are resident at once.
+    // most: tokens of a group.  A K split takes the ranks that are resident at once; where two CTAs share an SM, at most
+    // 263 of the 304 (12288 x 4096 at 16 tokens: two ranks 14.5 us, three 16.9).
     auto cut = [&](int most) {
         mp = c.params[1] > 0 ? c.params[1] : group_tokens(M, most);
         if (mp > (M + 15) / 16 * 16) mp = (M + 15) / 16 * 16;
@@ -508,7 +539,7 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
         ns = c.params[2] > 0 ? c.params[2] : 1;
         if (c.params[2] == 0)
             for (int r = 2; r <= kMaxRanks && 2 * r <= nkb; ++r)
-                if (units <= tc_cluster_capacity(dev, mp <= 32, r)) ns = r;
+                if (units <= tc_cluster_capacity(dev, mp <= 32, r) && (mp > 32 || units * r <= 2 * dev->sm_count * 13 / 15)) ns = r;
         if (ns > nkb) ns = nkb;
     };
     cut(128);
@@ -523,15 +554,16 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     const long long grid = ns > 1 || units < dev->sm_count ? units * ns : dev->sm_count;
     const int share = ns > 1 ? (mp / 4 + ns - 1) / ns * 4 : mp;
     const size_t fold = ns > 1 ? static_cast<size_t>(ns) * share * kTileRows * 4 : 0;
-    // Two CTAs an SM up to 32 tokens, so that the next launch's first weights come under this one's tail.
-    const size_t budget = mp <= 32 ? 112 * 1024 : kMaxDynSmem;
+    // A K split of up to 32 tokens has two CTAs an SM, or leaves room for the next launch's, whose first weights then come
+    // under this one's tail (12288 x 4096 at 16 tokens: two ranks 14.5 us, with deep rings and one CTA an SM 20.0).
+    // Elsewhere the rings are as deep as an SM holds (19456 x 8192 at 16 tokens: 4 stages 537 ns a block, 8 391).
+    const size_t budget = mp <= 32 && ns > 1 ? 112 * 1024 : kMaxDynSmem;
     // An even number of weights' stages: a slot then belongs to one converting set, which sees its phases in turn.  (A set
     // that waits for a slot's next phase while the one before, the other set's, is not complete would pass at once.)
-    int stw = c.params[0] > 0 ? c.params[0] : 6;
-    if (stw < 2 || stw > 8 || stw % 2 != 0) return DG_ERR_BAD_VARIANT;
-    int stx = kDone - 1;
-    while (stx > 4 && smem_bytes(mp, stw, stx, fold) > budget) --stx;
-    while (c.params[0] == 0 && stw > 4 && smem_bytes(mp, stw, stx, fold) > budget) stw -= 2;
+    if (c.params[0] > 8 || c.params[0] % 2 != 0) return DG_ERR_BAD_VARIANT;
+    // Activations wait behind the weights that are on their way: their ring is as long as the weights', or as there is room.
+    int stw = c.params[0] > 0 ? c.params[0] : mp <= 32 ? 8 : 6, stx = kDone - 1;
+    while (c.params[0] == 0 && stw > 4 && smem_bytes(mp, stw, stw < kDone ? stw : kDone - 1, fold) > budget) stw -= 2;
     while (stx > 2 && smem_bytes(mp, stw, stx, fold) > budget) --stx;
     while (c.params[0] == 0 && stw > 2 && smem_bytes(mp, stw, stx, fold) > budget) stw -= 2;
     size_t smem = smem_bytes(mp, stw, stx, fold);
@@ -553,17 +585,16 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     a.share = share;
     a.sw_stages = stw;
     a.sx_stages = stx;
+    a.x = qws;
     a.sx = reinterpret_cast<float*>(qws + code_bytes(M, K));
     a.sw = sw;
     a.y = static_cast<uint16_t*>(y);
     a.ws = static_cast<uint8_t*>(ws);
-    CUtensorMap tmW, tmX;
-    if (!encode_2d(&tmW, Wq, static_cast<uint64_t>(K), static_cast<uint64_t>(N), kBlock, kTileRows, false) ||
-        !encode_2d(&tmX, qws, static_cast<uint64_t>(K), static_cast<uint64_t>(M), 64, static_cast<uint32_t>(mp), true))
-        return DG_ERR_CUDA;
-    const dg_status st = launch_i8_quant(dev, true, x, qws, const_cast<float*>(a.sx), M, K, true, stream);
+    CUtensorMap tmW;
+    if (!encode_2d(&tmW, Wq, static_cast<uint64_t>(K), static_cast<uint64_t>(N), kBlock, kTileRows)) return DG_ERR_CUDA;
+    const dg_status st = launch_i8_quant(dev, x, qws, const_cast<float*>(a.sx), M, K, mp, stream);
     if (st != DG_OK) return st;
-    void* args[] = {&tmW, &tmX, &a};
+    void* args[] = {&tmW, &a};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kThreads);

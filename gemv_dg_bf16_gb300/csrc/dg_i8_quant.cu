@@ -1,5 +1,5 @@
 // dg_i8_quant.cu -- rows of bf16 to 8-bit integer codes with one scale a row
-// (dg_quant_i8_rowscale, and ahead of dg_gemv_i8_rowscale with the codes as binary16).
+// (dg_quant_i8_rowscale, and ahead of dg_gemv_i8_rowscale with the codes as binary16, in tiles).
 //
 // W warps share a row and hold it in registers, 16 bytes a lane and load: one pass over
 // memory, the maximum by shuffles (and shared memory where W > 1), the codes from the registers.
@@ -15,18 +15,20 @@ constexpr int kVec = 16;                    // 16-byte loads a thread holds
 
 struct QuantArgs {
     const uint16_t* x;
-    uint8_t* q;                             // int8 codes, or binary16 codes
+    uint8_t* q;                             // int8 codes [M, K], or binary16 codes in tiles
     float* s;
     int M, K, early;
+    int mp;                                 // tiles: tokens of a group
 };
 
+// Eight codes of a row from element k on.  Tiles are what the linear loads at once (i8::tile_offset).
 template <bool HALF>
-__device__ __forceinline__ void put8(uint8_t* q, size_t at, uint4 v, const i8::RowScale& o)
+__device__ __forceinline__ void put8(const QuantArgs& a, long long row, int k, uint4 v, const i8::RowScale& o)
 {
     if constexpr (HALF)
-        *reinterpret_cast<uint4*>(q + 2 * at) = i8::halves8(v, o);
+        *reinterpret_cast<uint4*>(a.q + i8::tile_offset(static_cast<int>(row), k, a.mp, a.K)) = i8::halves8(v, o);
     else
-        *reinterpret_cast<uint2*>(q + at) = i8::codes8(v, o);
+        *reinterpret_cast<uint2*>(a.q + row * a.K + k) = i8::codes8(v, o);
 }
 
 template <int W, bool HALF>
@@ -63,15 +65,16 @@ __global__ void __launch_bounds__(W < 4 ? 128 : W * 32) i8_quant_kernel(QuantArg
         for (int i = 0; i < W; ++i) m = max(m, part[i]);
     }
     const i8::RowScale o = i8::row_scale(m);
-    const size_t at = static_cast<size_t>(row) * a.K;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
         const int v = first + i * W * 32;
-        if (v < nv) put8<HALF>(a.q, at + 8 * static_cast<size_t>(v), raw[i], o);
+        if (v < nv) put8<HALF>(a, row, 8 * v, raw[i], o);
     }
 #pragma unroll 1
     for (int v = first + kVec * W * 32; v < nv; v += W * 32)
-        put8<HALF>(a.q, at + 8 * static_cast<size_t>(v), ld_stream_after(x + 8 * static_cast<size_t>(v)), o);
+        put8<HALF>(a, row, 8 * v, ld_stream_after(x + 8 * static_cast<size_t>(v)), o);
+    if constexpr (HALF)                                         // zeros to the end of the last block
+        for (int v = nv + first; v < (a.K + 127) / 128 * 16; v += W * 32) put8<true>(a, row, 8 * v, make_uint4(0, 0, 0, 0), o);
     if (first == 0) a.s[row] = o.s;
 }
 
@@ -85,15 +88,14 @@ const void* quant_fn(int w)
 
 }  // namespace
 
-dg_status launch_i8_quant(const DeviceInfo* dev, bool half, const void* x, void* q, float* s, int M, int K, bool early,
-                          cudaStream_t stream)
+dg_status launch_i8_quant(const DeviceInfo* dev, const void* x, void* q, float* s, int M, int K, int mp, cudaStream_t stream)
 {
     int w = K <= 4096 ? 1 : K <= 16384 ? 4 : 16;
     if (w == 1 && M < 8 * dev->sm_count && K > 1024) w = 4;
     const int rows = w == 1 ? 4 : 1;
-    QuantArgs a{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q), s, M, K, early ? 1 : 0};
+    QuantArgs a{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q), s, M, K, mp > 0, mp};
     void* args[] = {&a};
-    if (launch_kernel(half ? quant_fn<true>(w) : quant_fn<false>(w), static_cast<unsigned>((M - 1) / rows + 1),
+    if (launch_kernel(mp > 0 ? quant_fn<true>(w) : quant_fn<false>(w), static_cast<unsigned>((M - 1) / rows + 1),
                       w == 1 ? 128u : static_cast<unsigned>(w * 32), 0, stream, args, Early::kNothing) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;

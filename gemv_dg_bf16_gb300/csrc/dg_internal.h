@@ -71,10 +71,9 @@ dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const
                        const void* sw, const float* gx, const float* gw, void* y, int M, int N, int K, void* ws,
                        size_t ws_bytes, cudaStream_t stream);
 
-// 8-bit integers with a scale a row: the quantisation (dg_i8_quant.cu; half: codes as binary16, for
-// the linear, which waits for them: `early`) and the linear (dg_i8_linear.cu).
-dg_status launch_i8_quant(const DeviceInfo* dev, bool half, const void* x, void* q, float* s, int M, int K, bool early,
-                          cudaStream_t stream);
+// 8-bit integers with a scale a row: the quantisation (dg_i8_quant.cu; mp > 0: codes as binary16 in tiles of
+// mp tokens, for the linear, which may begin early as it waits for them) and the linear (dg_i8_linear.cu).
+dg_status launch_i8_quant(const DeviceInfo* dev, const void* x, void* q, float* s, int M, int K, int mp, cudaStream_t stream);
 size_t i8_workspace_bytes(int M, int K);
 // The same for few tokens on the CUDA cores (dg_i8_cc.cu): whether a call has room, and the launcher.
 bool i8_cc_takes(int M, int K);
