@@ -2,9 +2,10 @@
 //
 // A row of bf16 values with largest magnitude amax >= 0 becomes, in binary32 (every step one
 // correctly rounded operation, so that codes and scales are defined to the last bit):
-//   A = max(amax, 2^-100),  r = 127 / A,  s = A / 127,  q = round-to-nearest-even(x * r)
-// |q| <= 127: fl(amax * fl(127 / amax)) is within 2^-23 of 127.  The floor keeps r finite; an
-// all-zero row has codes 0.  A row that holds an infinity or a NaN has codes 0 and scale NaN.
+//   A = max(amax, 2^-100),  r = 127 * (1 / A),  s = A * fl(1 / 127),  q = round-to-nearest-even(x * r)
+// |q| <= 127: amax * r is within 2^-21 of 127 (1 / A may be subnormal, where it has 22 bits at least).  The
+// floor keeps r finite; an all-zero row has codes 0.  A row that holds an infinity or a NaN has codes 0
+// and scale NaN.
 //
 // Products are exact.  An 8-bit integer is exact in binary16, a product of two in binary32, and a
 // sum of at most 1024 of them is at most 1024 * 127 * 128 < 2^24, so that a chain of f16 MMAs
@@ -41,8 +42,8 @@ __device__ __forceinline__ RowScale row_scale(uint32_t bits)
     RowScale o;
     o.live = bits < 0x7f80u;
     const float a = fmaxf(__uint_as_float(bits << 16), 0x1p-100f);
-    o.r = __fdiv_rn(127.0f, a);
-    o.s = o.live ? __fdiv_rn(a, 127.0f) : __uint_as_float(0x7fffffffu);
+    o.r = __fmul_rn(127.0f, __frcp_rn(a));
+    o.s = o.live ? __fmul_rn(a, 1.0f / 127.0f) : __uint_as_float(0x7fffffffu);
     return o;
 }
 

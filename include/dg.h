@@ -414,8 +414,8 @@ dg_status dg_gemv_a4w4_blockscale(const void* x, const void* Wq, const void* sw,
 
 /* Rows of bf16 to 8-bit integers with one scale a row, in binary32 (each step one correctly
  * rounded operation, so codes and scales are defined to the last bit):
- *   A = max(max_k |x[m,k]|, 2^-100),  q[m,k] = rint(x[m,k] * (127 / A)) in -127..127 (ties to even),
- *   s[m] = A / 127
+ *   A = max(max_k |x[m,k]|, 2^-100),  q[m,k] = rint(x[m,k] * (127 * (1 / A))) in -127..127 (ties to
+ *   even),  s[m] = A * (1 / 127), the constant rounded to binary32
  * A row with an infinity or a NaN gets codes 0 and scale NaN; an all-zero row gets codes 0.
  * For weights the rows are output channels.  x [M, K] bf16, q [M, K] int8, s [M] fp32;
  * K % 16 == 0, M and K up to 2^31 - 256.  Asynchronous on `stream`; a linear launched after it may read

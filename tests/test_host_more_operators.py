@@ -146,11 +146,12 @@ def test_dimensions(shape):
 # ---------------------------------------------------------------- the references themselves
 
 def test_reference_codes_and_linear():
-    q, s = R.i8_codes(np.array([[127, 0.5, 1.5, -2.5], [0, 0, 0, 0], [np.inf, 1, 0, 0], [254, 1, -3, 2]], np.float32))
-    assert q.tolist() == [[127, 0, 2, -2], [0] * 4, [0] * 4, [127, 0, -2, 1]]
-    assert s[0] == 1 and s[3] == 2 and np.isnan(s[2]) and 0 < s[1] < 1e-30
-    y = R.i8_linear(np.array([[127, 1]], np.float32), np.array([[1, -128], [2, 3]], np.int8), np.array([1, 0.5], np.float32))
-    assert torch.from_numpy(y).view(BF).tolist() == [[-1.0, 128.0]]     # 257 / 2 to bf16
+    q, s = R.i8_codes(np.array([[64, 0.25, -3, 1], [0, 0, 0, 0], [np.inf, 1, 0, 0], [256, 4, -12, 1]], np.float32))
+    assert q.tolist() == [[127, 0, -6, 2], [0] * 4, [0] * 4, [127, 2, -6, 0]]
+    assert abs(s[0] * 127 / 64 - 1) < 2e-7 and s[3] == 4 * s[0] and np.isnan(s[2]) and 0 < s[1] < 1e-30
+    y = R.i8_linear(np.array([[64, 1]], np.float32), np.array([[1, -128], [2, 3]], np.int8), np.array([1, 0.5], np.float32))
+    s0 = float(s[0])
+    assert torch.from_numpy(y).view(BF).tolist() == [[float(torch.tensor((127 - 256) * s0).to(BF)), float(torch.tensor((254 + 6) * s0 * 0.5).to(BF))]]
 
 
 def test_reference_sort():
