@@ -79,8 +79,6 @@ size_t i8_workspace_bytes(int M, int K);
 bool i8_cc_takes(int M, int K);
 dg_status launch_i8_cc(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw, void* y,
                        int M, int N, int K, cudaStream_t stream);
-dg_status launch_i8_mw(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw, void* y,
-                       int M, int N, int K, cudaStream_t stream);
 dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw,
                            void* y, int M, int N, int K, void* ws, size_t ws_bytes, cudaStream_t stream);
 

@@ -39,8 +39,9 @@
  *   by the caller.  bf16 values travel as their 16-bit patterns, e4m3 values as
  *   their 8-bit codes (OCP 8-bit float E4M3, "fn" variant: no infinities,
  *   S.1111.111 is NaN, largest magnitude 448).
- * - Every pointer must be 16-byte aligned and K must be a multiple of 8
- *   (bf16 weights) or 16 (e4m3 weights); otherwise DG_ERR_ALIGNMENT /
+ * - Every pointer must be 16-byte aligned (what dg_moe_route, dg_logprobs and dg_logits_adjust take, and
+ *   the sort's ids, positions and gate weights: on their element's boundary) and K must be a multiple of 8 (bf16 weights) or 16 (e4m3 and 8-bit
+ *   integer weights); otherwise DG_ERR_ALIGNMENT /
  *   DG_ERR_UNSUPPORTED_SHAPE is returned before anything is launched.
  * - Calls are asynchronous on `stream` and make no host synchronisation.
  *   Argument errors are returned synchronously and launch nothing.
@@ -179,7 +180,7 @@ dg_status dg_device_status(const void* ws, int32_t* host_out, dg_stream_t stream
  * launched with programmatic dependent launch, so it can be scheduled while the
  * preceding kernel on the stream finishes; before waiting for that kernel it
  * touches nothing but weights (streams them into L2 or shared memory).  Of this
- * library dg_quant_fp4_blockscale and dg_dequant_fp4_blockscale write what may be
+ * library dg_quant_fp4_blockscale, dg_dequant_fp4_blockscale and dg_quant_i8_rowscale write what may be
  * weights: no kernel begins before they have completed, and the next one on their
  * stream that reads weights early is launched without the overlap.  Other outputs of this library are no weights of a call on
  * the same stream while the flag is on.  A preceding kernel that does not signal early (any
@@ -503,7 +504,7 @@ dg_status dg_moe_combine(const void* z, const int32_t* pos, const float* w, void
 /* The gradients of dg_moe_combine with respect to z and w, given that of y:
  *   dz[pos[m, k]] = bf16_rn( w[m, k] * dy[m] )      rows that no slot names stay as they are
  *   dw[m, k]      = sum_n dy[m, n] * z[pos[m, k], n]  in binary32, in a fixed order; 0 where pos is outside
- * dy [M, N], z and dz [P, N] bf16, w and dw [M, topk] fp32.  N % 8 == 0, 1 <= topk <= 32, M and P >= 1. */
+ * The positions inside are distinct (of two slots with one position, either's dz may be there).  dy [M, N], z and dz [P, N] bf16, w and dw [M, topk] fp32.  N % 8 == 0, 1 <= topk <= 32, M and P >= 1. */
 dg_status dg_moe_combine_grad(const void* dy, const void* z, const int32_t* pos, const float* w, void* dz, float* dw,
                               int M, int topk, int P, int N, dg_stream_t stream);
 
