@@ -9,17 +9,22 @@
 // Swap-AB: a unit is a tile of 128 weight rows (the MMA's M) with a group of up to MP tokens (its N), taken in
 // 128-element blocks of K.  Few units: a cluster of CTAs each, with a range of K a rank.  Many: persistent CTAs, one an
 // SM, take one after the other, the next one's blocks under the epilogue of the last.
-//   warp 0      streams the weights: 128 x 128 bytes a stage by TMA (128-byte swizzle)
-//   warp 1      allocates tensor memory; one elected lane issues tcgen05.mma, 8 of K = 16 a block
-//   warps 2-9   convert: a lane takes one weight row's 128 bytes from shared memory, turns
-//               them into binary16 and stores them in tensor memory, where the MMA reads A; four
-//               warps take the even blocks, four the odd ones, into a ring of 3 or 4 buffers of 64 columns (with
-//               two, each conversion waited for an MMA: 790 cycles a block at 128 tokens)
-//   warps 10-13 epilogue: every 1024 elements the accumulator (two of them) is taken out of tensor
-//               memory, as integers, and added up; then scaled and stored, or folded
-//   warp 14     streams the activations: a block of binary16 codes a stage, which the quantisation left in one piece
+//   weights      a warp streams 128 x 128 bytes a stage by TMA (128-byte swizzle)
+//   MMA          a warp allocates tensor memory; one elected lane issues tcgen05.mma, 8 of K = 16 a block
+//   conversion   two or three sets of four warps take the blocks in turn: a lane takes one weight row's 128 bytes from
+//                shared memory, turns them into binary16 and stores them in tensor memory, where the MMA reads A,
+//                in a ring of 3 or 4 buffers of 64 columns (with two, each conversion waited for an MMA: 790 cycles a
+//                block at 128 tokens)
+//   epilogue     four warps: every 1024 elements the accumulator (two of them) is taken out of tensor
+//                memory, as integers, and added up; then scaled and stored, or folded
+//   activations  a warp streams a block of binary16 codes a stage, which the quantisation left in one piece
 // Each rank of a K split folds a share of the tokens, and the others write their integers of these into its
 // shared memory.
+//
+// Groups of 64 tokens and more without a K split: a pair of CTAs has a unit of 256 weight rows, and one MMA
+// (cta_group::2) multiplies both CTAs' 128 rows of A with the N of both, of which each loads and holds half.  Of the
+// two the even one issues; what it waits for and what it frees goes through barriers of both.  What binds it at 128 tokens: the
+// MMAs take 512 cycles a block, its 32 KB 510 at the 64 bytes a clock that an SM takes in, and blocks come every 720.
 // Every wait is bounded: on timeout the kernel flags DG_DEVERR_WAIT_TIMEOUT and winds down.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -36,8 +41,13 @@ namespace {
 constexpr int kTileRows = 128;                     // MMA M
 constexpr int kBlock = 128;                        // K elements a stage: one swizzled row of bytes
 constexpr int kWBox = kTileRows * kBlock;          // 16 KB
-constexpr int kThreads = 480;
-constexpr int kConvert = 2, kEpilogue = 10, kStreamX = 14;     // first warps of the roles
+// Warps of the roles: weights, MMA, activations, then 4 for each converting set and 4 for the epilogue.
+template <bool PAIR>
+struct Roles {
+    static constexpr int kSets = PAIR ? 3 : 2;
+    static constexpr int kConvert = PAIR ? 4 : 2, kEpilogue = kConvert + 4 * kSets, kStreamX = PAIR ? 2 : kEpilogue + 4;
+    static constexpr int kThreads = PAIR ? 640 : 480;
+};
 constexpr int kSegBlocks = i8::kSegment / kBlock;
 constexpr int kACols = kBlock / 2;                 // tensor-memory columns of a converted block
 constexpr int kMaxRanks = 8;
@@ -89,20 +99,47 @@ __device__ __forceinline__ bool wait_both(uint32_t b0, uint32_t p0, uint32_t b1,
     return (r0 || tc::bar_wait(b0, p0, abort_flag)) && (r1 || tc::bar_wait(b1, p1, abort_flag));
 }
 
-// kind::f16 with binary16 A (tensor memory) and B (shared memory), fp32 accumulate, M = 128, N = n.
-__host__ __device__ constexpr uint32_t idesc_f16(int n)
+// kind::f16 with binary16 A (tensor memory) and B (shared memory), fp32 accumulate, M = m, N = n.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n)
 {
-    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// PAIR: two CTAs' A (128 rows each) with the N of both CTAs' B (a half each).
+template <bool PAIR>
 __device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+            ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+            ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+            : "memory");
+}
+
+// The barrier at this place (PAIR: in both CTAs) arrives when the MMAs issued so far have finished.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar)
+{
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+    else
+        tc::commit(bar);
+}
+
+// Arrival at a barrier of a CTA of the cluster.
+__device__ __forceinline__ void arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Whether a condition holds in all of the 128 epilogue threads (a barrier for them).
@@ -120,18 +157,19 @@ __device__ __forceinline__ bool all_of(bool p)
     return r != 0;
 }
 
-// MP: the most tokens of a group that this instance takes.
-template <int MP>
-__global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
+// MP: the most tokens of a group that this instance takes.  PAIR: clusters of two CTAs share a unit of 256 weight rows.
+template <int MP, bool PAIR>
+__global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, I8Args a)
 {
     constexpr uint32_t kA0 = 2 * MP < 64 ? 64 : 2 * MP;             // first column of the converted blocks
     constexpr uint32_t kCols = MP <= 32 ? 256 : 512;               // two accumulators, kBufs converted blocks
     constexpr int kBufs = MP <= 32 ? 3 : 4;
+    constexpr int kSets = Roles<PAIR>::kSets, kConvert = Roles<PAIR>::kConvert, kEpilogue = Roles<PAIR>::kEpilogue, kStreamX = Roles<PAIR>::kStreamX;
     static_assert(kA0 + kBufs * kACols <= kCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int SW = a.sw_stages, SX = a.sx_stages, xbox = a.mp * 128, xstage = 2 * xbox;
+    const int SW = a.sw_stages, SX = a.sx_stages, xbox = (PAIR ? a.mp / 2 : a.mp) * 128, xstage = 2 * xbox;
     uint8_t* xring = smem + SW * kWBox;
     float* sxs = reinterpret_cast<float*>(xring + SX * xstage);     // [2][MP]
     uint16_t* stage = reinterpret_cast<uint16_t*>(sxs + 2 * MP);    // [2][16 tokens][128 rows] of outputs
@@ -145,10 +183,11 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
     int* fold = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + nbars * 8 + 16);   // [rank][share / 4][row][4]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool split = a.nsplit > 1;
-    const int rank = split ? static_cast<int>(cluster_rank()) : 0;
+    const bool split = !PAIR && a.nsplit > 1;
+    const int rank = split ? static_cast<int>(cluster_rank()) : 0, half = PAIR ? static_cast<int>(cluster_rank()) : 0;
+    constexpr int kUnitRows = PAIR ? 2 * kTileRows : kTileRows;
     // Units `first`, first + stride, ...; groups of one tile run side by side, so that its weights come from memory once.
-    const int first = static_cast<int>(blockIdx.x) / a.nsplit, stride = split ? a.units : static_cast<int>(gridDim.x);
+    const int first = static_cast<int>(blockIdx.x) / (PAIR ? 2 : a.nsplit), stride = split ? a.units : static_cast<int>(gridDim.x) / (PAIR ? 2 : 1);
     const int kb0 = static_cast<int>(static_cast<long long>(rank) * a.nkb / a.nsplit);
     const int nk = static_cast<int>(static_cast<long long>(rank + 1) * a.nkb / a.nsplit) - kb0;     // blocks of a unit
 
@@ -161,22 +200,29 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
             tc::bar_init(xfull + 8 * s, 1);
         }
         for (int s = 0; s < kDone; ++s) tc::bar_init(done + 8 * s, 1);
-        for (int s = 0; s < kBufs; ++s) tc::bar_init(afull + 8 * s, 4);
+        for (int s = 0; s < kBufs; ++s) tc::bar_init(afull + 8 * s, PAIR ? 8 : 4);
         for (int b = 0; b < 2; ++b) {
             tc::bar_init(dfull + 8 * b, 1);
-            tc::bar_init(dempty + 8 * b, 4);                        // one per epilogue warp
+            tc::bar_init(dempty + 8 * b, PAIR ? 8 : 4);             // one per epilogue warp
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tmem_holder)),
-                     "r"(kCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tmem_holder)),
+                         "r"(kCols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tmem_holder)),
+                         "r"(kCols));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     tc::fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();                         // both CTAs' barriers and tensor memory are there
     tc::fence_after();
     const uint32_t tmem = *tmem_holder;
     pdl_launch_dependents();
@@ -195,104 +241,122 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
 
     const int q = warp & 3;                                         // tensor-memory lane quarter
     const uint32_t tlane = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    if (warp == 0) {
-        if (tc::elect_one()) {
-            const uint64_t once = tc::policy_evict_first();
-            int s = 0, issued = 0;
-            uint32_t round = 0;
-            for (int u = first; u < a.units && !*abort_flag; u += stride) {
-                const int row = u / a.groups * kTileRows;
-                for (int i = 0; i < nk; ++i) {                      // weights: nothing to wait for
-                    if (round > 0 && !tc::bar_wait(wempty + 8 * s, (round - 1) & 1u, abort_flag)) break;
-                    tc::bar_expect_tx(wfull + 8 * s, kWBox);
-                    if (a.groups == 1)
-                        tc::tma_2d_hint(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, row, wfull + 8 * s, once);
-                    else
-                        tc::tma_2d(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, row, wfull + 8 * s);
-                    ++issued;
-                    if (++s == SW) {
-                        s = 0;
-                        ++round;
+    if (warp < kConvert || (!PAIR && warp == kStreamX)) {
+        // PAIR: 5 warpgroups of 96 registers become 32 + 3 * 96 + 160.
+        if constexpr (PAIR) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        if (warp == 0) {
+            if (tc::elect_one()) {
+                const uint64_t once = tc::policy_evict_first();
+                int s = 0, issued = 0;
+                uint32_t round = 0;
+                for (int u = first; u < a.units && !*abort_flag; u += stride) {
+                    const int row = u / a.groups * kUnitRows + half * kTileRows;
+                    for (int i = 0; i < nk; ++i) {                      // weights: nothing to wait for
+                        if (round > 0 && !tc::bar_wait(wempty + 8 * s, (round - 1) & 1u, abort_flag)) break;
+                        tc::bar_expect_tx(wfull + 8 * s, kWBox);
+                        if (a.groups == 1)
+                            tc::tma_2d_hint(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, row, wfull + 8 * s, once);
+                        else
+                            tc::tma_2d(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, row, wfull + 8 * s);
+                        ++issued;
+                        if (++s == SW) {
+                            s = 0;
+                            ++round;
+                        }
                     }
                 }
+                if (*abort_flag) drain(wfull, issued, SW);
             }
-            if (*abort_flag) drain(wfull, issued, SW);
-        }
-        __syncwarp();                                               // (a lane in pdl_wait() holds up the whole warp)
-        pdl_wait();
-    } else if (warp == kStreamX) {
-        pdl_wait();
-        if (tc::elect_one()) {
-            int s = 0, issued = 0;
-            uint32_t round = 0;
-            for (int u = first; u < a.units && !*abort_flag; u += stride) {
-                const uint8_t* src = a.x + (static_cast<size_t>(u % a.groups) * a.nkb + kb0) * xstage;
-                for (int i = 0; i < nk; ++i, src += xstage) {
-                    const int before = issued - SX;                 // the block that had the slot
-                    if (before >= 0 && !tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag)) break;
-                    const uint32_t dst = tc::su32(xring + s * xstage);
-                    tc::bar_expect_tx(xfull + 8 * s, static_cast<uint32_t>(xstage));
-                    tc::bulk_load(dst, src, static_cast<uint32_t>(xstage), xfull + 8 * s);
-                    ++issued;
-                    if (++s == SX) {
-                        s = 0;
-                        ++round;
+            __syncwarp();                                               // (a lane in pdl_wait() holds up the whole warp)
+            pdl_wait();
+        } else if (warp == kStreamX) {
+            pdl_wait();
+            if (tc::elect_one()) {
+                int s = 0, issued = 0;
+                uint32_t round = 0;
+                for (int u = first; u < a.units && !*abort_flag; u += stride) {
+                    const int group = PAIR ? u % a.groups * 2 + half : u % a.groups;        // (PAIR: tiles of half a group)
+                    const uint8_t* src = a.x + (static_cast<size_t>(group) * a.nkb + kb0) * xstage;
+                    for (int i = 0; i < nk; ++i, src += xstage) {
+                        const int before = issued - SX;                 // the block that had the slot
+                        if (before >= 0 && !tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag)) break;
+                        const uint32_t dst = tc::su32(xring + s * xstage);
+                        tc::bar_expect_tx(xfull + 8 * s, static_cast<uint32_t>(xstage));
+                        tc::bulk_load(dst, src, static_cast<uint32_t>(xstage), xfull + 8 * s);
+                        ++issued;
+                        if (++s == SX) {
+                            s = 0;
+                            ++round;
+                        }
                     }
                 }
+                if (*abort_flag) drain(xfull, issued, SX);
             }
-            if (*abort_flag) drain(xfull, issued, SX);
-        }
-    } else if (warp == 1) {
-        if (tc::elect_one()) {
-            const uint32_t idesc = idesc_f16(a.mp);
-            const uint64_t half = static_cast<uint64_t>(xbox / 16), ring = tc::sw128_desc(tc::su32(xring));
-            int s = 0, b = 0, seg = 0, block = 0;
-            uint32_t round = 0, bround = 0;
-            for (int u = first; u < a.units && !*abort_flag; u += stride) {
-                for (int i = 0, in = 0; i < nk; ++i, ++block) {     // in: blocks of the segment so far
-                    const int d = seg & 1;
-                    if (!wait_both(xfull + 8 * s, round & 1u, afull + 8 * b, bround & 1u, abort_flag)) break;
-                    if (in == 0 && seg >= 2 && !tc::bar_wait(dempty + 8 * d, static_cast<uint32_t>(seg / 2 - 1) & 1u, abort_flag)) break;
-                    tc::fence_after();
-                    const uint64_t x0 = ring + static_cast<uint64_t>(s * (xstage / 16));
+        } else if (warp == 1) {
+            if (half == 0 && tc::elect_one()) {
+                const uint32_t idesc = idesc_f16(kUnitRows, a.mp);
+                const uint64_t box = static_cast<uint64_t>(xbox / 16), ring = tc::sw128_desc(tc::su32(xring));
+                int s = 0, b = 0, seg = 0, block = 0;
+                uint32_t round = 0, bround = 0;
+                for (int u = first; u < a.units && !*abort_flag; u += stride) {
+                    for (int i = 0, in = 0; i < nk; ++i, ++block) {     // in: blocks of the segment so far
+                        const int d = seg & 1;
+                        if constexpr (PAIR) {                           // (whoever converted has seen the activations too)
+                            if (!tc::bar_wait(afull + 8 * b, bround & 1u, abort_flag)) break;
+                            if (in == 0 && seg >= 2 && !tc::bar_wait(dempty + 8 * d, static_cast<uint32_t>(seg / 2 - 1) & 1u, abort_flag)) break;
+                        } else {
+                            if (!wait_both(xfull + 8 * s, round & 1u, afull + 8 * b, bround & 1u, abort_flag)) break;
+                            if (in == 0 && seg >= 2 && !tc::bar_wait(dempty + 8 * d, static_cast<uint32_t>(seg / 2 - 1) & 1u, abort_flag)) break;
+                        }
+                        tc::fence_after();
+                        const uint64_t x0 = ring + static_cast<uint64_t>(s * (xstage / 16));
 #pragma unroll
-                    for (int kk = 0; kk < kBlock / 16; ++kk)
-                        mma_f16_ta(tmem + static_cast<uint32_t>(d * MP), tmem + kA0 + static_cast<uint32_t>(b * kACols + kk * 8),
-                                   x0 + (kk < 4 ? 0 : half) + static_cast<uint64_t>((kk % 4) * 2), idesc, (in > 0 || kk > 0) ? 1u : 0u);
-                    tc::commit(done + 8 * (block % kDone));
-                    if (++in == kSegBlocks || i == nk - 1) {
-                        tc::commit(dfull + 8 * d);
-                        in = 0;
-                        ++seg;
-                    }
-                    if (++s == SX) {
-                        s = 0;
-                        ++round;
-                    }
-                    if (++b == kBufs) {
-                        b = 0;
-                        ++bround;
+                        for (int kk = 0; kk < kBlock / 16; ++kk)
+                            mma_f16_ta<PAIR>(tmem + static_cast<uint32_t>(d * MP), tmem + kA0 + static_cast<uint32_t>(b * kACols + kk * 8),
+                                             x0 + (kk < 4 ? 0 : box) + static_cast<uint64_t>((kk % 4) * 2), idesc, (in > 0 || kk > 0) ? 1u : 0u);
+                        commit<PAIR>(done + 8 * (block % kDone));
+                        if (++in == kSegBlocks || i == nk - 1) {
+                            commit<PAIR>(dfull + 8 * d);
+                            in = 0;
+                            ++seg;
+                        }
+                        if (++s == SX) {
+                            s = 0;
+                            ++round;
+                        }
+                        if (++b == kBufs) {
+                            b = 0;
+                            ++bround;
+                        }
                     }
                 }
             }
+            __syncwarp();
+            pdl_wait();
+        } else {
+            pdl_wait();
         }
-        __syncwarp();
-        pdl_wait();
     } else if (warp < kEpilogue) {
         // Convert: this lane's weight row, 16 bytes at a time from their swizzled places.
         const int row = q * 32 + lane, set = (warp - kConvert) / 4;
         const long long blocks = static_cast<long long>(nk) * ((a.units - first + stride - 1) / stride);
         int s = set, b = set;                                       // (SW is even: the slots of a set are its own)
         uint32_t round = 0;
+        int xs = set % SX;                                          // PAIR: the activations' slot and its phase
+        uint32_t xround = static_cast<uint32_t>(set / SX);
+        const uint32_t leader = PAIR ? map_to_rank(afull, 0) : afull;
 #pragma unroll 1
-        for (int i = set; i < blocks; i += 2) {
-            if (!tc::bar_wait(wfull + 8 * s, round & 1u, abort_flag)) break;
+        for (int i = set; i < blocks; i += kSets) {
+            // (a wait that ran out ends the loop in every lane)
+            if (!__all_sync(kFull, tc::bar_wait(wfull + 8 * s, round & 1u, abort_flag))) break;
             const uint8_t* src = smem + s * kWBox;
             uint4 raw[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + tc::sw128_offset(row, c));
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(wempty + 8 * s);          // (every lane has read its bytes)
             const int before = i - kBufs;                           // the block that had the buffer
-            if (before >= 0 && !tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag)) break;
+            if (before >= 0 && !__all_sync(kFull, tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag))) break;
             tc::fence_after();
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
@@ -307,29 +371,34 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
                 }
                 tc::tmem_st16(tlane + kA0 + static_cast<uint32_t>(b * kACols + h * 16), v);
             }
-            __syncwarp();
-            if (lane == 0) tc::bar_arrive(wempty + 8 * s);          // (every lane's bytes are in registers)
             tc::tmem_st_wait();
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::bar_arrive(afull + 8 * b);
-            s += 2;
+            if constexpr (PAIR) {
+                // The multiplying CTA hears of this CTA's half of the activations and of its weights at once.
+                if (lane == 0 && tc::bar_wait(xfull + 8 * xs, xround & 1u, abort_flag)) arrive_cluster(leader + 8 * b);
+                for (xs += kSets; xs >= SX; xs -= SX) ++xround;
+            } else {
+                if (lane == 0) tc::bar_arrive(afull + 8 * b);
+            }
+            s += kSets;
             if (s >= SW) {
                 s -= SW;
                 ++round;
             }
-            b += 2;
+            b += kSets;
             if (b >= kBufs) b -= kBufs;
         }
         pdl_wait();
     } else {
+        if constexpr (PAIR) asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         pdl_wait();
         const int row = q * 32 + lane, nseg = (nk + kSegBlocks - 1) / kSegBlocks;
         int seg = 0;
         bool good = true;
 #pragma unroll 1
         for (int u = first, k = 0; u < a.units && good; u += stride, ++k) {
-            const int t0 = u % a.groups * a.mp, rows_here = min(a.mp, a.M - t0), nrow = u / a.groups * kTileRows + row;
+            const int t0 = u % a.groups * a.mp, rows_here = min(a.mp, a.M - t0), nrow = u / a.groups * kUnitRows + half * kTileRows + row;
             const float sw = a.sw[min(nrow, a.N - 1)];
             float* sxt = sxs + (k & 1) * MP;
             for (int t = threadIdx.x - kEpilogue * 32; t < rows_here; t += 128) sxt[t] = ld_cg_f32(a.sx + t0 + t);
@@ -339,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
 #pragma unroll 1
             for (int e = 0; e < nseg; ++e, ++seg) {
                 const int d = seg & 1;
-                if (!tc::bar_wait(dfull + 8 * d, static_cast<uint32_t>(seg / 2) & 1u, abort_flag)) {
+                if (!__all_sync(kFull, tc::bar_wait(dfull + 8 * d, static_cast<uint32_t>(seg / 2) & 1u, abort_flag))) {
                     good = false;
                     break;
                 }
@@ -355,7 +424,12 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
                 }
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) tc::bar_arrive(dempty + 8 * d);
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        arrive_cluster(map_to_rank(dempty + 8 * d, 0));
+                    else
+                        tc::bar_arrive(dempty + 8 * d);
+                }
             }
             // A wait that ran out ends the loop in all 128 threads or in none (they meet here, and the scales are there).
             good = all_of(good && !*abort_flag);
@@ -422,12 +496,12 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
         }
     }
     if (split) {
-        if (warp < kEpilogue || warp >= kStreamX) {
+        if (warp < kEpilogue || warp >= kEpilogue + 4) {
             __syncwarp();
             asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");            // (the arrival at the start)
         }
         cluster_sync_all();                                         // every rank's integers are in place; the last remote access
-        if (warp >= kConvert && warp < kStreamX && !*abort_flag) {
+        if (warp >= kConvert && warp < kEpilogue + 4 && !*abort_flag) {
             // A warp takes 32 rows, the same ones of every third four tokens: a lane adds up a row's over the ranks.
             const int t0 = first % a.groups * a.mp, lo = rank * a.share, rows_here = min(a.mp, a.M - t0);
             const int quads = (max(0, min(rows_here - lo, a.share)) + 3) / 4;
@@ -453,10 +527,14 @@ __global__ void __launch_bounds__(kThreads, MP <= 32 ? 2 : 1)
     }
     tc::fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();                         // neither leaves while the other's MMAs or arrivals need it
     if (*abort_flag && threadIdx.x == 0) set_status(a.ws, DG_DEVERR_WAIT_TIMEOUT);
     if (warp == 1) {
         tc::fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
     }
 }
 
@@ -485,20 +563,24 @@ bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, 
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-const void* kernel_of(int mp)
+const void* kernel_of(int mp, bool pair)
 {
-    return mp <= 16   ? reinterpret_cast<const void*>(&i8_tc_kernel<16>)
-           : mp <= 32 ? reinterpret_cast<const void*>(&i8_tc_kernel<32>)
-           : mp <= 64 ? reinterpret_cast<const void*>(&i8_tc_kernel<64>)
-           : mp <= 96 ? reinterpret_cast<const void*>(&i8_tc_kernel<96>)
-                      : reinterpret_cast<const void*>(&i8_tc_kernel<128>);
+    if (pair)
+        return mp == 64   ? reinterpret_cast<const void*>(&i8_tc_kernel<64, true>)
+               : mp == 96 ? reinterpret_cast<const void*>(&i8_tc_kernel<96, true>)
+                          : reinterpret_cast<const void*>(&i8_tc_kernel<128, true>);
+    return mp <= 16   ? reinterpret_cast<const void*>(&i8_tc_kernel<16, false>)
+           : mp <= 32 ? reinterpret_cast<const void*>(&i8_tc_kernel<32, false>)
+           : mp <= 64 ? reinterpret_cast<const void*>(&i8_tc_kernel<64, false>)
+           : mp <= 96 ? reinterpret_cast<const void*>(&i8_tc_kernel<96, false>)
+                      : reinterpret_cast<const void*>(&i8_tc_kernel<128, false>);
 }
 
-// fold: bytes for the integers of a K split.
-size_t smem_bytes(int mp, int sw, int sx, size_t fold)
+// xt: tokens of a stage of activations; fold: bytes for the integers of a K split.
+size_t smem_bytes(int mp, int xt, int sw, int sx, size_t fold)
 {
     const size_t most = mp <= 16 ? 16 : mp <= 32 ? 32 : mp <= 64 ? 64 : mp <= 96 ? 96 : 128;
-    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * mp * 256 + most * 8 + 2 * 16 * kTileRows * 2 + (2 * sw + sx + kDone + 10) * 8 + 16 + fold;
+    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * xt * 256 + most * 8 + 2 * 16 * kTileRows * 2 + (2 * sw + sx + kDone + 10) * 8 + 16 + fold;
 }
 
 // Rows of the last group of up to 128 tokens and elements of the last block are there in full.
@@ -524,7 +606,7 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
 {
     if (ws_bytes < i8_workspace_bytes(M, K)) return DG_ERR_WORKSPACE_TOO_SMALL;
     for (int i = 0; i < 6; ++i)
-        if (c.params[i] < 0 || (i > 2 && c.params[i] != 0)) return DG_ERR_BAD_VARIANT;
+        if (c.params[i] < 0 || (i > 3 && c.params[i] != 0)) return DG_ERR_BAD_VARIANT;
     const int tiles = (N - 1) / kTileRows + 1, nkb = (K - 1) / kBlock + 1;
     if (c.params[1] % 16 != 0 || c.params[1] > 128 || c.params[2] > kMaxRanks) return DG_ERR_BAD_VARIANT;
     int mp, groups, ns;
@@ -549,29 +631,46 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
         else if (c.params[2] == 0)
             ns = 1;
     }
-    const void* fn = kernel_of(mp);
+    // A pair of CTAs for 256 rows where K is not split and a group has 64 tokens or more.  Each holds half of the
+    // activations, so that an SM takes in 32 KB a block at 128 tokens and not 48 (it takes 61 bytes a clock at most), and
+    // three sets convert: 24576 x 4096 at 512 tokens 82.9 us, single CTAs 93.8; at 256 46.5 / 51.4, 128 33.7 / 36.4, 64
+    // 28.8 / 30.1; 8192 x 8192 at 256 34.5 / 36.0.  Groups are rounded up to 32 tokens: 20480 x 5120 at 160 49.5 / 48.7.
+    const bool pair = c.params[3] == 2 || (c.params[3] == 0 && ns == 1 && mp >= 64 && (c.params[1] == 0 || mp % 32 == 0) && c.params[0] % 6 == 0);
+    if (pair) {
+        if (c.params[2] > 1 || (c.params[1] > 0 && (mp < 64 || mp % 32 != 0)) || c.params[0] % 6 != 0) return DG_ERR_BAD_VARIANT;
+        mp = mp <= 64 ? 64 : (mp + 31) / 32 * 32;
+        groups = (M - 1) / mp + 1;
+        units = static_cast<long long>((tiles + 1) / 2) * groups;
+        ns = 1;
+    }
+    const int xt = pair ? mp / 2 : mp;
+    const void* fn = kernel_of(mp, pair);
+    const int threads = pair ? Roles<true>::kThreads : Roles<false>::kThreads;
     if (units * ns > 0x7fffffffll || units * nkb / dev->sm_count > 0x3fffffff) return DG_ERR_UNSUPPORTED_SHAPE;
-    const long long grid = ns > 1 || units < dev->sm_count ? units * ns : dev->sm_count;
+    const int clusters = pair ? tc_cluster_capacity(dev, false, 2) : 0;
+    if (pair && clusters < 1) return DG_ERR_UNSUPPORTED_SHAPE;
+    const long long grid = pair ? 2 * (units < clusters ? units : clusters) : ns > 1 || units < dev->sm_count ? units * ns : dev->sm_count;
     const int share = ns > 1 ? (mp / 4 + ns - 1) / ns * 4 : mp;
     const size_t fold = ns > 1 ? static_cast<size_t>(ns) * share * kTileRows * 4 : 0;
     // A K split of up to 32 tokens has two CTAs an SM, or leaves room for the next launch's, whose first weights then come
     // under this one's tail (12288 x 4096 at 16 tokens: two ranks 14.5 us, with deep rings and one CTA an SM 20.0).
     // Elsewhere the rings are as deep as an SM holds (19456 x 8192 at 16 tokens: 4 stages 537 ns a block, 8 391).
     const size_t budget = mp <= 32 && ns > 1 ? 112 * 1024 : kMaxDynSmem;
-    // An even number of weights' stages: a slot then belongs to one converting set, which sees its phases in turn.  (A set
-    // that waits for a slot's next phase while the one before, the other set's, is not complete would pass at once.)
-    if (c.params[0] > 8 || c.params[0] % 2 != 0) return DG_ERR_BAD_VARIANT;
+    // A multiple of the converting sets as weights' stages: a slot then belongs to one set, which sees its phases in
+    // turn.  (A set that waits for a slot's next phase while the one before, another set's, is not complete would pass
+    // at once.)
+    if (c.params[0] > 8 || c.params[0] % 2 != 0 || c.params[3] > 2) return DG_ERR_BAD_VARIANT;
     // Activations wait behind the weights that are on their way: their ring is as long as the weights', or as there is room.
     int stw = c.params[0] > 0 ? c.params[0] : mp <= 32 ? 8 : 6, stx = kDone - 1;
-    while (c.params[0] == 0 && stw > 4 && smem_bytes(mp, stw, stw < kDone ? stw : kDone - 1, fold) > budget) stw -= 2;
-    while (stx > 2 && smem_bytes(mp, stw, stx, fold) > budget) --stx;
-    while (c.params[0] == 0 && stw > 2 && smem_bytes(mp, stw, stx, fold) > budget) stw -= 2;
-    size_t smem = smem_bytes(mp, stw, stx, fold);
+    while (c.params[0] == 0 && !pair && stw > 4 && smem_bytes(mp, xt, stw, stw < kDone ? stw : kDone - 1, fold) > budget) stw -= 2;
+    while (stx > 2 && smem_bytes(mp, xt, stw, stx, fold) > budget) --stx;
+    while (c.params[0] == 0 && !pair && stw > 2 && smem_bytes(mp, xt, stw, stx, fold) > budget) stw -= 2;
+    size_t smem = smem_bytes(mp, xt, stw, stx, fold);
     // Never more CTAs on an SM than its 512 tensor-memory columns hold.
     const size_t least = mp <= 32 ? 77 * 1024 : 115 * 1024;
     if (smem < least) smem = least;
     if (smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
-    if (occupancy(fn, kThreads, smem) < 1) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (occupancy(fn, threads, smem) < 1) return DG_ERR_UNSUPPORTED_SHAPE;
     uint8_t* qws = static_cast<uint8_t*>(ws) + kWsData;
     I8Args a{};
     a.N = N;
@@ -592,17 +691,17 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     a.ws = static_cast<uint8_t*>(ws);
     CUtensorMap tmW;
     if (!encode_2d(&tmW, Wq, static_cast<uint64_t>(K), static_cast<uint64_t>(N), kBlock, kTileRows)) return DG_ERR_CUDA;
-    const dg_status st = launch_i8_quant(dev, x, qws, const_cast<float*>(a.sx), M, K, mp, stream);
+    const dg_status st = launch_i8_quant(dev, x, qws, const_cast<float*>(a.sx), M, K, xt, stream);
     if (st != DG_OK) return st;
     void* args[] = {&tmW, &a};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(ns);
+    attr[0].val.clusterDim.x = static_cast<unsigned>(pair ? 2 : ns);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     if (launch_ordered(cfg, attr, 1, fn, args, Early::kWeights) != cudaSuccess) {

@@ -201,7 +201,10 @@ std::string check_choice(int op, const dg_choice& c)
         if (c.params[0] != 0 && (c.params[0] < 2 || c.params[0] > 8 || c.params[0] % 2 != 0)) return "pipeline stages must be 2, 4, 6 or 8";
         if (g < 0 || g > 128 || g % 16 != 0) return "tokens of a group must be a multiple of 16 up to 128";
         if (c.params[2] < 0 || c.params[2] > 8) return "K ranges must be 0..8";
-        for (int i = 3; i < 6; ++i)
+        if (c.params[3] < 0 || c.params[3] > 2) return "CTAs of a unit must be 0..2";
+        if (c.params[3] == 2 && ((g != 0 && (g < 64 || g % 32 != 0)) || c.params[2] > 1 || c.params[0] % 6 != 0))
+            return "a pair of CTAs takes 64, 96 or 128 tokens, all of K and 6 stages";
+        for (int i = 4; i < 6; ++i)
             if (c.params[i] != 0) return "unused tensor-core parameter set";
         return "";
     }

@@ -110,6 +110,7 @@ std::vector<dg_choice> candidates(int op, const dg_choice& def)
         for (int tg : {0, 16, 32, 64, 96, 128})
             for (int ns : {0, 1, 2, 3, 4, 6, 8}) add(mk(DG_VAR_TC, 0, tg, ns));
         for (int st = 2; st <= 8; st += 2) add(mk(DG_VAR_TC, st));
+        for (int ctas : {1, 2}) add(mk(DG_VAR_TC, 0, 0, 0, ctas));
     } else if (def.variant == DG_VAR_TC) {
         for (int st = 2; st <= 8; ++st) {
             dg_choice c = mk(DG_VAR_TC, st);

@@ -113,6 +113,22 @@ def test_every_cut_gives_the_same_bits():
         assert dg.dg_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (64, 256, 128), (100, 257, 1040), (129, 130, 1296), (512, 1000, 400), (200, 20000, 160),
+                                   (77, 4099, 2064), (300, 40000, 1168), (512, 20000, 2176)])
+def test_pairs_of_ctas_give_the_same_bits(M, N, K):
+    x, (w, sw) = _x(M, K, M), _w(N, K, N)
+    xc, wc, sc = x.cuda(), w.cuda(), sw.cuda()
+    want = R.i8_linear(R.f32(x), w.numpy(), sw.numpy())
+    ws = dg.workspace(dg.DG_OP_GEMV_I8, M, N, K)
+    for cut in ((0, 0, 0, 2), (6, 0, 1, 2), (0, 0, 0, 1), (0, 0, 1, 0), (0, 64, 0, 2), (0, 96, 1, 2), (0, 128, 0, 2)):
+        if cut[1] > (M + 15) // 16 * 16:
+            continue
+        for _ in range(3):
+            y = dg.dg_gemv_i8_rowscale(xc, wc, sc, ws=ws, choice=dg.Choice.make(dg.DG_VAR_TC, *cut))
+            np.testing.assert_array_equal(_bits(y), want, err_msg=str(cut))
+    assert dg.dg_device_status(ws) == 0
+
+
 @pytest.mark.parametrize("K", [1024, 8192, 131072])
 def test_largest_sums_are_exact(K):
     """All products of one sign at their largest: K * 127 * 128, past 2^24 from K = 1040 on, next to 2^31 at the longest."""
@@ -249,7 +265,8 @@ def test_bad_choices_are_refused():
     x, (w, sw) = _x(2, 64, 1), _w(8, 64, 2)
     xc, wc, sc = x.cuda(), w.cuda(), sw.cuda()
     for bad in ((dg.DG_VAR_CC_BULK,), (dg.DG_VAR_CC_WARP, 4, 8), (dg.DG_VAR_TC, 1), (dg.DG_VAR_TC, 3), (dg.DG_VAR_TC, 10), (dg.DG_VAR_TC, 0, 40), (dg.DG_VAR_TC, 0, 144), (dg.DG_VAR_TC, 0, 0, 9), (dg.DG_VAR_TC, 0, 0, -1), (dg.DG_VAR_TC, 0, -16),
-                (dg.DG_VAR_MMA, 1), (dg.DG_VAR_TC, 0, 0, 0, 1)):
+                (dg.DG_VAR_MMA, 1), (dg.DG_VAR_TC, 0, 0, 0, 3), (dg.DG_VAR_TC, 0, 0, 0, 0, 1), (dg.DG_VAR_TC, 4, 0, 0, 2),
+                (dg.DG_VAR_TC, 0, 48, 0, 2), (dg.DG_VAR_TC, 0, 0, 2, 2)):
         with pytest.raises(dg.DGError) as e:
             dg.dg_gemv_i8_rowscale(xc, wc, sc, choice=dg.Choice.make(*bad))
         assert e.value.status == dg.DG_ERR_BAD_VARIANT, bad

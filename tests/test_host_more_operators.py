@@ -89,9 +89,11 @@ def test_i8_select_and_table(tmp_path):
         p = tmp_path / "t.json"
         p.write_text(json.dumps(doc))
         return dg.dg_table_check(str(p), "sm_103", 13000, 13000)[0]
+    assert check({"variant": 3, "params": [0, 96, 0, 2]}) == 0 and check({"variant": 3, "params": [4, 32, 8, 1]}) == 0
     assert check({"variant": 3, "params": [4, 32, 8]}) == 0 and check({"variant": 1, "params": []}) == 0
     for bad in ({"variant": 1, "params": [4, 8]}, {"variant": 3, "params": [5]}, {"variant": 3, "params": [0, 40]}, {"variant": 3, "params": [0, 144]}, {"variant": 3, "params": [0, 0, 9]},
-                {"variant": 3, "params": [0, 0, 0, 1]}, {"variant": 3, "params": [-1]}, {"variant": 4, "params": []}):
+                {"variant": 3, "params": [0, 0, 0, 3]}, {"variant": 3, "params": [0, 0, 0, 0, 1]}, {"variant": 3, "params": [0, 48, 0, 2]},
+                {"variant": 3, "params": [4, 0, 0, 2]}, {"variant": 3, "params": [0, 0, 2, 2]}, {"variant": 3, "params": [-1]}, {"variant": 4, "params": []}):
         assert check(bad) == 6, bad
     assert B._OP_NAMES[dg.DG_OP_GEMV_I8] == "gemv_i8"
 
