@@ -42,7 +42,7 @@ __device__ __forceinline__ RowScale row_scale(uint32_t bits)
     RowScale o;
     o.live = bits < 0x7f80u;
     const float a = fmaxf(__uint_as_float(bits << 16), 0x1p-100f);
-    o.r = __fmul_rn(127.0f, __frcp_rn(a));
+    o.r = __fmul_rn(127.0f, __fdiv_rn(1.0f, a));
     o.s = o.live ? __fmul_rn(a, 1.0f / 127.0f) : __uint_as_float(0x7fffffffu);
     return o;
 }

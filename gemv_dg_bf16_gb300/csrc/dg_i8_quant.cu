@@ -3,15 +3,16 @@
 //
 // W warps share a row and hold it in registers, 16 bytes a lane and load: one pass over
 // memory, the maximum by shuffles (and shared memory where W > 1), the codes from the registers.
-// Rows longer than W * 4096 elements are read again for the codes.  A warp a row where the rows
+// Rows longer than 16 * 4096 elements are read again for the codes.  A warp a row where the rows
 // fill the GPU; few rows take four warps each, whose loads are then a quarter as many in a line.
+// Bytes bind many rows: 24576 x 4096 takes 44.7 us, 6.75 TB/s of reads and writes together.  128 KB of loads in flight an
+// SM are best: a warp has 16 of them in four CTAs of 104 registers (in five CTAs of 96 it took 48.8), or 8 where that is a
+// row of 2048 (24576 x 2048: 23.5 us, with 16 27.5).  Few rows are a launch and a chain of latencies: 16 x 4096 1.8 us.
 #include "dg_i8.cuh"
 #include "dg_internal.h"
 
 namespace dg {
 namespace {
-
-constexpr int kVec = 16;                    // 16-byte loads a thread holds
 
 struct QuantArgs {
     const uint16_t* x;
@@ -31,7 +32,8 @@ __device__ __forceinline__ void put8(const QuantArgs& a, long long row, int k, u
         *reinterpret_cast<uint2*>(a.q + row * a.K + k) = i8::codes8(v, o);
 }
 
-template <int W, bool HALF>
+// kVec: 16-byte loads a thread holds.
+template <int W, int kVec, bool HALF>
 __global__ void __launch_bounds__(W < 4 ? 128 : W * 32) i8_quant_kernel(QuantArgs a)
 {
     constexpr int kRows = W < 4 ? 4 / W : 1;                    // rows per CTA
@@ -79,11 +81,13 @@ __global__ void __launch_bounds__(W < 4 ? 128 : W * 32) i8_quant_kernel(QuantArg
 }
 
 template <bool HALF>
-const void* quant_fn(int w)
+const void* quant_fn(int w, int K)
 {
-    return w == 1   ? reinterpret_cast<const void*>(&i8_quant_kernel<1, HALF>)
-           : w == 4 ? reinterpret_cast<const void*>(&i8_quant_kernel<4, HALF>)
-                    : reinterpret_cast<const void*>(&i8_quant_kernel<16, HALF>);
+    if (w == 16) return reinterpret_cast<const void*>(&i8_quant_kernel<16, 16, HALF>);
+    if (w == 4) return reinterpret_cast<const void*>(&i8_quant_kernel<4, 16, HALF>);
+    if constexpr (!HALF)                                        // (the linear has too few rows for it)
+        if (K > 2048) return reinterpret_cast<const void*>(&i8_quant_kernel<1, 16, HALF>);
+    return reinterpret_cast<const void*>(&i8_quant_kernel<1, 8, HALF>);
 }
 
 }  // namespace
@@ -95,7 +99,7 @@ dg_status launch_i8_quant(const DeviceInfo* dev, const void* x, void* q, float* 
     const int rows = w == 1 ? 4 : 1;
     QuantArgs a{static_cast<const uint16_t*>(x), static_cast<uint8_t*>(q), s, M, K, mp > 0, mp};
     void* args[] = {&a};
-    if (launch_kernel(mp > 0 ? quant_fn<true>(w) : quant_fn<false>(w), static_cast<unsigned>((M - 1) / rows + 1),
+    if (launch_kernel(mp > 0 ? quant_fn<true>(w, K) : quant_fn<false>(w, K), static_cast<unsigned>((M - 1) / rows + 1),
                       w == 1 ? 128u : static_cast<unsigned>(w * 32), 0, stream, args, Early::kNothing) != cudaSuccess) {
         cudaGetLastError();
         return DG_ERR_CUDA;
