@@ -25,6 +25,8 @@
 // (cta_group::2) multiplies both CTAs' 128 rows of A with the N of both, of which each loads and holds half.  Of the
 // two the even one issues; what it waits for and what it frees goes through barriers of both.  What binds it at 128 tokens: the
 // MMAs take 512 cycles a block, its 32 KB 510 at the 64 bytes a clock that an SM takes in, and blocks come every 720.
+// Measured (calls in turn, quantisation included): 12288 x 4096 at 16 tokens 14.0 us, 3.6 TB/s of weights -- 8 us of stream
+// between a quantisation, a first load and a fold; 4099 x 12288 at 77 19.3; 24576 x 4096 at 512 82.4, 1.25 PFLOP/s.
 // Every wait is bounded: on timeout the kernel flags DG_DEVERR_WAIT_TIMEOUT and winds down.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -612,7 +614,7 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     int mp, groups, ns;
     long long units;
     // most: tokens of a group.  A K split takes the ranks that are resident at once; where two CTAs share an SM, at most
-    // 263 of the 304 (12288 x 4096 at 16 tokens: two ranks 14.5 us, three 16.9).
+    // 263 of the 304 (12288 x 4096 at 16 tokens: two ranks 14.0 us, three 18.5).
     auto cut = [&](int most) {
         mp = c.params[1] > 0 ? c.params[1] : group_tokens(M, most);
         if (mp > (M + 15) / 16 * 16) mp = (M + 15) / 16 * 16;
@@ -633,8 +635,8 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     }
     // A pair of CTAs for 256 rows where K is not split and a group has 64 tokens or more.  Each holds half of the
     // activations, so that an SM takes in 32 KB a block at 128 tokens and not 48 (it takes 61 bytes a clock at most), and
-    // three sets convert: 24576 x 4096 at 512 tokens 82.9 us, single CTAs 93.8; at 256 46.5 / 51.4, 128 33.7 / 36.4, 64
-    // 28.8 / 30.1; 8192 x 8192 at 256 34.5 / 36.0.  Groups are rounded up to 32 tokens: 20480 x 5120 at 160 49.5 / 48.7.
+    // three sets convert: 24576 x 4096 at 512 tokens 82.0 us, single CTAs 92.8; at 256 46.1 / 50.7, 128 32.7 / 36.0, 64
+    // 28.9 / 30.5; 8192 x 8192 at 256 33.3 / 35.8.  Groups are rounded up to 32 tokens: 20480 x 5120 at 160 48.7 / 48.2.
     const bool pair = c.params[3] == 2 || (c.params[3] == 0 && ns == 1 && mp >= 64 && (c.params[1] == 0 || mp % 32 == 0) && c.params[0] % 6 == 0);
     if (pair) {
         if (c.params[2] > 1 || (c.params[1] > 0 && (mp < 64 || mp % 32 != 0)) || c.params[0] % 6 != 0) return DG_ERR_BAD_VARIANT;
@@ -653,8 +655,8 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     const int share = ns > 1 ? (mp / 4 + ns - 1) / ns * 4 : mp;
     const size_t fold = ns > 1 ? static_cast<size_t>(ns) * share * kTileRows * 4 : 0;
     // A K split of up to 32 tokens has two CTAs an SM, or leaves room for the next launch's, whose first weights then come
-    // under this one's tail (12288 x 4096 at 16 tokens: two ranks 14.5 us, with deep rings and one CTA an SM 20.0).
-    // Elsewhere the rings are as deep as an SM holds (19456 x 8192 at 16 tokens: 4 stages 537 ns a block, 8 391).
+    // under this one's tail (12288 x 4096 at 16 tokens: two ranks 14.0 us, with deep rings and one CTA an SM 20.7).
+    // Elsewhere the rings are as deep as an SM holds (19456 x 8192 at 16 tokens: 4 stages 39.7 us, 8 30.1).
     const size_t budget = mp <= 32 && ns > 1 ? 112 * 1024 : kMaxDynSmem;
     // A multiple of the converting sets as weights' stages: a slot then belongs to one set, which sees its phases in
     // turn.  (A set that waits for a slot's next phase while the one before, another set's, is not complete would pass

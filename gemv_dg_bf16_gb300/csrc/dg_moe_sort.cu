@@ -11,9 +11,12 @@
 // warp and expert took 4.1 us for 64 tokens of 6 slots and 64 us for 32768 of 8: it steps through
 // the distinct values of a warp.)
 //
+// Measured: 64 tokens of 6 slots 2.4 us, 512 of 8 5.7, 8192 of 8 12.7, 32768 of 8 48: one cluster's blocks one after the other.
+//
 // Rows move in 16-byte pieces, any type; a token's row is read once and written to its up to 32
 // places.  On the way back a thread has the loads of eight slots in flight, and adds in slot
-// order in binary32.
+// order in binary32.  Bytes bind them: rows of 4096 bf16, 8 slots: 32768 tokens there 355.6 us and back 354.5 (6.8 TB/s),
+// 8192 back 90.1 and the gradient 171.9 (6.6 TB/s); 64 tokens are a launch and two loads in a row, 2.2 us.
 #include "dg_internal.h"
 #include "dg_common.cuh"
 
