@@ -26,7 +26,7 @@
 // two the even one issues; what it waits for and what it frees goes through barriers of both.  What binds it at 128 tokens: the
 // MMAs take 512 cycles a block, its 32 KB 510 at the 64 bytes a clock that an SM takes in, and blocks come every 720.
 // Measured (calls in turn, quantisation included): 12288 x 4096 at 16 tokens 14.0 us, 3.6 TB/s of weights -- 8 us of stream
-// between a quantisation, a first load and a fold; 4099 x 12288 at 77 19.3; 24576 x 4096 at 512 82.4, 1.25 PFLOP/s.
+// between a quantisation, a first load and a fold; 4099 x 12288 at 77 19.3; 24576 x 4096 at 512 81.2, 1.27 PFLOP/s.
 // Every wait is bounded: on timeout the kernel flags DG_DEVERR_WAIT_TIMEOUT and winds down.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -251,15 +251,17 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                 const uint64_t once = tc::policy_evict_first();
                 int s = 0, issued = 0;
                 uint32_t round = 0;
+                // A unit begins at a block of its tile's own, so that not all of them ask for the same activations at a time
+                // (24576 x 4096 at 512 tokens 82.0 -> 81.2 us; the order of blocks changes no sum).
                 for (int u = first; u < a.units && !*abort_flag; u += stride) {
-                    const int row = u / a.groups * kUnitRows + half * kTileRows;
-                    for (int i = 0; i < nk; ++i) {                      // weights: nothing to wait for
+                    const int tile = u / a.groups, row = tile * kUnitRows + half * kTileRows;
+                    for (int i = 0, kb = tile % nk; i < nk; ++i, kb = kb + 1 < nk ? kb + 1 : 0) {       // weights: nothing to wait for
                         if (round > 0 && !tc::bar_wait(wempty + 8 * s, (round - 1) & 1u, abort_flag)) break;
                         tc::bar_expect_tx(wfull + 8 * s, kWBox);
                         if (a.groups == 1)
-                            tc::tma_2d_hint(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, row, wfull + 8 * s, once);
+                            tc::tma_2d_hint(tc::su32(smem + s * kWBox), &tmW, (kb0 + kb) * kBlock, row, wfull + 8 * s, once);
                         else
-                            tc::tma_2d(tc::su32(smem + s * kWBox), &tmW, (kb0 + i) * kBlock, row, wfull + 8 * s);
+                            tc::tma_2d(tc::su32(smem + s * kWBox), &tmW, (kb0 + kb) * kBlock, row, wfull + 8 * s);
                         ++issued;
                         if (++s == SW) {
                             s = 0;
@@ -279,12 +281,12 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                 for (int u = first; u < a.units && !*abort_flag; u += stride) {
                     const int group = PAIR ? u % a.groups * 2 + half : u % a.groups;        // (PAIR: tiles of half a group)
                     const uint8_t* src = a.x + (static_cast<size_t>(group) * a.nkb + kb0) * xstage;
-                    for (int i = 0; i < nk; ++i, src += xstage) {
+                    for (int i = 0, kb = u / a.groups % nk; i < nk; ++i, kb = kb + 1 < nk ? kb + 1 : 0) {
                         const int before = issued - SX;                 // the block that had the slot
                         if (before >= 0 && !tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag)) break;
                         const uint32_t dst = tc::su32(xring + s * xstage);
                         tc::bar_expect_tx(xfull + 8 * s, static_cast<uint32_t>(xstage));
-                        tc::bulk_load(dst, src, static_cast<uint32_t>(xstage), xfull + 8 * s);
+                        tc::bulk_load(dst, src + static_cast<size_t>(kb) * xstage, static_cast<uint32_t>(xstage), xfull + 8 * s);
                         ++issued;
                         if (++s == SX) {
                             s = 0;
@@ -635,8 +637,8 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     }
     // A pair of CTAs for 256 rows where K is not split and a group has 64 tokens or more.  Each holds half of the
     // activations, so that an SM takes in 32 KB a block at 128 tokens and not 48 (it takes 61 bytes a clock at most), and
-    // three sets convert: 24576 x 4096 at 512 tokens 82.0 us, single CTAs 92.8; at 256 46.1 / 50.7, 128 32.7 / 36.0, 64
-    // 28.9 / 30.5; 8192 x 8192 at 256 33.3 / 35.8.  Groups are rounded up to 32 tokens: 20480 x 5120 at 160 48.7 / 48.2.
+    // three sets convert: 24576 x 4096 at 512 tokens 81.2 us, single CTAs 93.8; at 256 45.3 / 51.7, 128 32.7 / 36.6, 64
+    // 28.8 / 30.5; 8192 x 8192 at 256 32.5 / 36.6.  Groups are rounded up to 32 tokens: 20480 x 5120 at 160 47.4 / 48.1.
     const bool pair = c.params[3] == 2 || (c.params[3] == 0 && ns == 1 && mp >= 64 && (c.params[1] == 0 || mp % 32 == 0) && c.params[0] % 6 == 0);
     if (pair) {
         if (c.params[2] > 1 || (c.params[1] > 0 && (mp < 64 || mp % 32 != 0)) || c.params[0] % 6 != 0) return DG_ERR_BAD_VARIANT;
