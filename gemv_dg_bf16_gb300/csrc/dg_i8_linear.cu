@@ -626,6 +626,11 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
         if (c.params[2] == 0)
             for (int r = 2; r <= kMaxRanks && 2 * r <= nkb; ++r)
                 if (units <= tc_cluster_capacity(dev, mp <= 32, r) && (mp > 32 || units * r <= 2 * dev->sm_count * 13 / 15)) ns = r;
+        // A few more units than SMs, and long ones: thirds of K in clusters, and not a second round for some SMs (16 tokens, one
+        // rank / three: 20480 x 5120 32.3 / 25.5 us, 24576 x 8192 49.3 / 41.2, 20480 x 12288 71.5 / 49.5; 24576 x 4096 27.3 / 27.3
+        // and at 8 27.2 / 30.0, 26000 x 4096 28.6 / 34.9, 20480 x 2560 18.2 / 18.7; 64 tokens, 24576 x 4096 30.7 / 48.7).
+        const long long sms = dev->sm_count;
+        if (c.params[2] == 0 && ns == 1 && mp <= 32 && nkb >= 32 && units > sms && (nkb >= 48 ? units * 7 <= sms * 9 : units * 6 <= sms * 7)) ns = 3;
         if (ns > nkb) ns = nkb;
     };
     cut(128);

@@ -71,7 +71,7 @@ def test_linear_to_the_bit(M, N, K):
     _check(_x(M, K, M * 7 + N), *_w(N, K, N + K))
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (16, 4099, 2064), (5, 2050, 12288), (77, 4099, 1616), (200, 8208, 528), (512, 1283, 4096),
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (16, 4099, 2064), (5, 2050, 12288), (77, 4099, 1616), (200, 8208, 528), (512, 1283, 4096), (16, 20480, 4112), (31, 24576, 4096),
                                    (3, 17, 33008), (40, 260, 16384)])
 def test_linear_of_ragged_and_long_shapes(M, N, K):
     _check(_x(M, K, M), *_w(N, K, N + K))
