@@ -616,14 +616,15 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     int mp, groups, ns;
     long long units;
     // most: tokens of a group.  A K split takes the ranks that are resident at once; where two CTAs share an SM, at most
-    // 263 of the 304 (12288 x 4096 at 16 tokens: two ranks 14.0 us, three 18.5).
+    // 263 of the 304 (12288 x 4096 at 16 tokens: two ranks 14.0 us, three 18.5).  Up to 512 elements a launch of clusters and
+    // the fold cost more than the blocks (256 x 512, one rank / two: 16 tokens 4.65 / 4.9 us, 64 6.3 / 6.75, 300 8.05 / 9.35).
     auto cut = [&](int most) {
         mp = c.params[1] > 0 ? c.params[1] : group_tokens(M, most);
         if (mp > (M + 15) / 16 * 16) mp = (M + 15) / 16 * 16;
         groups = (M - 1) / mp + 1;
         units = static_cast<long long>(tiles) * groups;
         ns = c.params[2] > 0 ? c.params[2] : 1;
-        if (c.params[2] == 0)
+        if (c.params[2] == 0 && nkb > 4)
             for (int r = 2; r <= kMaxRanks && 2 * r <= nkb; ++r)
                 if (units <= tc_cluster_capacity(dev, mp <= 32, r) && (mp > 32 || units * r <= 2 * dev->sm_count * 13 / 15)) ns = r;
         // A few more units than SMs, and long ones: thirds of K in clusters, and not a second round for some SMs (16 tokens, one
