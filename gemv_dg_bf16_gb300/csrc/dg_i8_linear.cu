@@ -53,6 +53,7 @@ struct Roles {
 constexpr int kSegBlocks = i8::kSegment / kBlock;
 constexpr int kACols = kBlock / 2;                 // tensor-memory columns of a converted block
 constexpr int kMaxRanks = 8;
+constexpr int kFewTokens = 16;
 constexpr int kDone = 8;                           // blocks whose completion is told apart: more than are in flight
 
 struct I8Args {
@@ -598,6 +599,23 @@ int group_tokens(int M, int most)
     return ((M - 1) / groups + 16) / 16 * 16;
 }
 
+// What a call of `units` units of mp tokens takes in us with K in ns ranges, roughly, for a choice among them: a launch, an
+// epilogue that grows with the tokens, the fold, and 0.4 a block of K of an SM, one CTA after the other on it or (K
+// split, up to 32 tokens) two side by side.  Where hardly an SM is left over, the next launch's first loads come late.  Fitted
+// to 4.2 us for 64 x 256 at 24 tokens to 21 for 4096 x 4096 at 400: 66 shapes, cuts and counts of tokens within a fifth or so.
+float estimate(int sms, long long units, int nkb, int mp, int ns)
+{
+    const long long ctas = units * ns;
+    const int blocks = (nkb - 1) / ns + 1;
+    const bool two = ns > 1 && mp <= 32;
+    const float rounds = two ? (ctas > sms ? static_cast<float>(ctas) / sms : 1.0f) * (mp > 16 ? 1.3f : 1.0f)
+                             : static_cast<float>((ctas - 1) / sms + 1);
+    float t = 3.6f + (mp == 32 ? 0.7f : 0.031f * (mp - 16)) + 0.4f * blocks * rounds;
+    if (ns > 1) t += 1.0f + 0.05f * ns + 0.01f * mp;
+    if (mp > 32 ? ctas * 32 > sms * 27ll : ctas * 15 > sms * 26ll) t += 2.5f;
+    return t;
+}
+
 }  // namespace
 
 size_t i8_workspace_bytes(int M, int K)
@@ -641,11 +659,34 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
         else if (c.params[2] == 0)
             ns = 1;
     }
+    // More than 16 tokens: the groups and the ranks with the least estimate.  (With groups of up to 128 and all the ranks that
+    // fit instead, us before / now: 64 x 256 at 400 tokens 7.1 / 4.5, 1024 x 512 at 200 8.1 / 5.3, 2048 x 1024 at 100 9.6 /
+    // 7.0, 4096 x 1024 at 200 11.2 / 8.2.)
+    if (M > kFewTokens && c.params[1] == 0 && c.params[2] == 0 && c.params[3] != 2) {
+        float best = 0.0f;
+        int most_best = 0, ns_best = 1;
+        for (int most = 16; most <= 128; most += 16) {
+            const int m = group_tokens(M, most);
+            const long long u = static_cast<long long>(tiles) * ((M - 1) / m + 1);
+            for (int r = 1; r <= kMaxRanks; r += r < 4 ? 1 : 2) {
+                if (r > 1 && (nkb <= 4 || 2 * r > nkb || m > 112 || u > tc_cluster_capacity(dev, m <= 32, r))) break;
+                const float t = estimate(dev->sm_count, u, nkb, m, r);
+                if (most_best == 0 || t < best) {
+                    best = t;
+                    most_best = m;
+                    ns_best = r;
+                }
+            }
+        }
+        cut(most_best);
+        if (!(ns == 3 && ns_best == 1 && units > dev->sm_count)) ns = ns_best;     // (cut's thirds of K stay)
+    }
     // A pair of CTAs for 256 rows where K is not split and a group has 64 tokens or more.  Each holds half of the
     // activations, so that an SM takes in 32 KB a block at 128 tokens and not 48 (it takes 61 bytes a clock at most), and
     // three sets convert: 24576 x 4096 at 512 tokens 81.2 us, single CTAs 93.8; at 256 45.3 / 51.7, 128 32.7 / 36.6, 64
-    // 28.8 / 30.5; 8192 x 8192 at 256 32.5 / 36.6.  Groups are rounded up to 32 tokens: 20480 x 5120 at 160 47.4 / 48.1.
-    const bool pair = c.params[3] == 2 || (c.params[3] == 0 && ns == 1 && mp >= 64 && (c.params[1] == 0 || mp % 32 == 0) && c.params[0] % 6 == 0);
+    // 28.8 / 30.5; 8192 x 8192 at 256 32.5 / 36.6.  Groups are rounded up to 32 tokens: 20480 x 5120 at 160 47.4 / 48.1.  Not
+    // for few units or a short K: 4096 x 4096 at 200 19.1 / 18.0, 2048 x 1024 at 400 11.7 / 10.1.
+    const bool pair = c.params[3] == 2 || (c.params[3] == 0 && ns == 1 && mp >= 64 && nkb >= 16 && units * 8 >= 5ll * dev->sm_count && (c.params[1] == 0 || mp % 32 == 0) && c.params[0] % 6 == 0);
     if (pair) {
         if (c.params[2] > 1 || (c.params[1] > 0 && (mp < 64 || mp % 32 != 0)) || c.params[0] % 6 != 0) return DG_ERR_BAD_VARIANT;
         mp = mp <= 64 ? 64 : (mp + 31) / 32 * 32;
