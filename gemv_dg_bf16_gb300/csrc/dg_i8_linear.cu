@@ -21,7 +21,7 @@
 // Each rank of a K split folds a share of the tokens, and the others write their integers of these into its
 // shared memory.
 //
-// Groups of 64 tokens and more without a K split: a pair of CTAs has a unit of 256 weight rows, and one MMA
+// Groups of 64 tokens and more, many units and 16 blocks or more, K not split: a pair of CTAs has a unit of 256 weight rows, and one MMA
 // (cta_group::2) multiplies both CTAs' 128 rows of A with the N of both, of which each loads and holds half.  Of the
 // two the even one issues; what it waits for and what it frees goes through barriers of both.  What binds it at 128 tokens: the
 // MMAs take 512 cycles a block, its 32 KB 510 at the 64 bytes a clock that an SM takes in, and blocks come every 720.
