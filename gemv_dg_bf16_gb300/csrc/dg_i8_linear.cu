@@ -653,7 +653,7 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
         if (ns > nkb) ns = nkb;
     };
     cut(128);
-    if (ns > 1 && mp > 112) {                                       // no room for more tokens' integers
+    if (ns > 1 && mp > 112) {           // (beside more tokens' integers two stages of weights are left: by a choice only)
         if (c.params[1] == 0)
             cut(64);
         else if (c.params[2] == 0)
@@ -716,6 +716,9 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     while (c.params[0] == 0 && !pair && stw > 4 && smem_bytes(mp, xt, stw, stw < kDone ? stw : kDone - 1, fold) > budget) stw -= 2;
     while (stx > 2 && smem_bytes(mp, xt, stw, stx, fold) > budget) --stx;
     while (c.params[0] == 0 && !pair && stw > 2 && smem_bytes(mp, xt, stw, stx, fold) > budget) stw -= 2;
+    // A table's pick holds for every row count of its bucket, whose groups and ranks differ, and with them the stages
+    // that fit: as deep as this call's (two of each always do; depth changes no bits).
+    while (c.from_table && !pair && stw > 2 && smem_bytes(mp, xt, stw, stx, fold) > kMaxDynSmem) stw -= 2;
     size_t smem = smem_bytes(mp, xt, stw, stx, fold);
     // Never more CTAs on an SM than its 512 tensor-memory columns hold.
     const size_t least = mp <= 32 ? 77 * 1024 : 115 * 1024;

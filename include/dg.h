@@ -433,7 +433,9 @@ dg_status dg_quant_i8_rowscale(const void* x, int8_t* q, float* s, int M, int K,
  * rows whose codes fit in shared memory), and DG_VAR_TC: params[0] stages of the weights' ring (2, 4, 6 or
  * 8; 0 = derived), [1] tokens of a group (a multiple of 16 up to 128; 0 = derived), [2] ranges K is cut
  * into (1..8; 0 = derived), [3] CTAs that share 128 rows each of a tile of weights (1 or 2; 0 = derived; 2 goes with 6
- * stages, 64, 96 or 128 tokens and all of K, each or 0).  A token with a non-finite activation gets NaN outputs.  ws: the status
+ * stages, 64, 96 or 128 tokens and all of K, each or 0).  Stages of an explicit choice that have no room beside its
+ * tokens and ranges (8 beside 128 tokens, 4 where K is cut too) are DG_ERR_BAD_VARIANT; a table's pick serves every row
+ * count of its bucket, as deep as fits.  A token with a non-finite activation gets NaN outputs.  ws: the status
  * word, and the codes and scales of the activations. */
 dg_status dg_gemv_i8_rowscale(const void* x, const int8_t* Wq, const float* sw, void* y, int M, int N, int K, void* ws,
                               size_t ws_bytes, dg_stream_t stream, const dg_choice* choice);
