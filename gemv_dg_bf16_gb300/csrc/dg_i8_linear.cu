@@ -688,7 +688,8 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     // for few units or a short K: 4096 x 4096 at 200 19.1 / 18.0, 2048 x 1024 at 400 11.7 / 10.1.
     const bool pair = c.params[3] == 2 || (c.params[3] == 0 && ns == 1 && mp >= 64 && nkb >= 16 && units * 8 >= 5ll * dev->sm_count && (c.params[1] == 0 || mp % 32 == 0) && c.params[0] % 6 == 0);
     if (pair) {
-        if (c.params[2] > 1 || (c.params[1] > 0 && (mp < 64 || mp % 32 != 0)) || c.params[0] % 6 != 0) return DG_ERR_BAD_VARIANT;
+        // (a group that the rows do not fill is a smaller one, of 64 tokens at least)
+        if (c.params[2] > 1 || (c.params[1] > 0 && (c.params[1] < 64 || c.params[1] % 32 != 0)) || c.params[0] % 6 != 0) return DG_ERR_BAD_VARIANT;
         mp = mp <= 64 ? 64 : (mp + 31) / 32 * 32;
         groups = (M - 1) / mp + 1;
         units = static_cast<long long>((tiles + 1) / 2) * groups;

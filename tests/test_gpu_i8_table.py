@@ -1,5 +1,5 @@
-"""A shape table's pick for the 8-bit integer linear serves every row count of its bucket: depth is no
-condition of a call."""
+"""A shape table's pick for the 8-bit integer linear serves every row count of its bucket: neither depth nor
+the width of a group is a condition of a call."""
 import json
 
 import pytest
@@ -31,7 +31,8 @@ def _inputs(M, N, K):
 @pytest.mark.parametrize("N,K,bucket,first", [(4096, 4096, 128, 97), (4096, 4096, 256, 193), (4099, 12288, 128, 97), (2048, 8192, 96, 65),
                                               (1536, 7168, 384, 257), (24576, 4096, 512, 385), (300, 1040, 16, 13), (300, 1040, 6, 5),
                                               (20480, 5120, 48, 33)])
-@pytest.mark.parametrize("variant,params", [(TC, [2]), (TC, [4]), (TC, [6]), (TC, [8]), (TC, [8, 128]), (TC, [8, 128, 4]), (TC, [6, 96, 8]), (TC, [8, 16])])
+@pytest.mark.parametrize("variant,params", [(TC, [2]), (TC, [4]), (TC, [6]), (TC, [8]), (TC, [8, 128]), (TC, [8, 128, 4]), (TC, [6, 96, 8]), (TC, [8, 16]),
+                                            (TC, [0, 64, 0, 2]), (TC, [0, 96, 0, 2]), (TC, [6, 128, 1, 2])])
 def test_table_pick_serves_every_row_count(cuda_device, swept, tmp_path, N, K, bucket, first, variant, params):
     doc = dict(swept)
     doc["entries"] = [{**swept["entries"][0], "op": "gemv_i8", "M": bucket, "N": N, "K": K,
@@ -60,3 +61,13 @@ def test_explicit_depth_that_does_not_fit_is_refused(cuda_device):
         with pytest.raises(dg.DGError) as e:
             dg.dg_gemv_i8_rowscale(x, w, sw, choice=dg.Choice.make(*choice))
         assert e.value.status == dg.DG_ERR_BAD_VARIANT, choice
+
+
+@pytest.mark.parametrize("M", [1, 40, 65, 97])
+def test_a_pair_takes_groups_that_the_rows_do_not_fill(cuda_device, M):
+    N, K = 700, 2064
+    x, w, sw = _inputs(M, N, K)
+    want = dg.dg_gemv_i8_rowscale(x, w, sw)
+    for tokens in (64, 96, 128):
+        y = dg.dg_gemv_i8_rowscale(x, w, sw, choice=dg.Choice.make(TC, 0, tokens, 0, 2))
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16)), tokens
