@@ -829,6 +829,8 @@ dg_status dg_gemv_i8_rowscale(const void* x, const int8_t* Wq, const float* sw, 
     if (!dev) return s;
     dg_choice c;
     if ((s = resolve_choice(DG_OP_GEMV_I8, M, N, K, choice, &c)) != DG_OK) return s;
+    // (a table's pick that has no room for this call's tokens: what is derived without one, the same bits)
+    if (c.from_table && c.variant == DG_VAR_CC_WARP && !i8_cc_takes(M, K)) default_choice(DG_OP_GEMV_I8, M, N, K, &c);
     if (c.variant == DG_VAR_CC_WARP) return launch_i8_cc(dev, c, x, Wq, sw, y, M, N, K, reinterpret_cast<cudaStream_t>(stream));
     if (c.variant != DG_VAR_TC) return DG_ERR_BAD_VARIANT;
     return launch_i8_linear(dev, c, x, Wq, sw, y, M, N, K, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));

@@ -1,5 +1,5 @@
 """A shape table's pick for the 8-bit integer linear serves every row count of its bucket: neither depth nor
-the width of a group is a condition of a call."""
+the width of a group nor the tokens that the CUDA cores take is a condition of a call."""
 import json
 
 import pytest
@@ -9,7 +9,7 @@ import gemv_dg_bf16_gb300 as dg
 
 pytestmark = pytest.mark.gpu
 
-TC = dg.DG_VAR_TC
+CC, TC = dg.DG_VAR_CC_WARP, dg.DG_VAR_TC
 
 
 @pytest.fixture(scope="module")
@@ -32,7 +32,7 @@ def _inputs(M, N, K):
                                               (1536, 7168, 384, 257), (24576, 4096, 512, 385), (300, 1040, 16, 13), (300, 1040, 6, 5),
                                               (20480, 5120, 48, 33)])
 @pytest.mark.parametrize("variant,params", [(TC, [2]), (TC, [4]), (TC, [6]), (TC, [8]), (TC, [8, 128]), (TC, [8, 128, 4]), (TC, [6, 96, 8]), (TC, [8, 16]),
-                                            (TC, [0, 64, 0, 2]), (TC, [0, 96, 0, 2]), (TC, [6, 128, 1, 2])])
+                                            (TC, [0, 64, 0, 2]), (TC, [0, 96, 0, 2]), (TC, [6, 128, 1, 2]), (CC, [])])
 def test_table_pick_serves_every_row_count(cuda_device, swept, tmp_path, N, K, bucket, first, variant, params):
     doc = dict(swept)
     doc["entries"] = [{**swept["entries"][0], "op": "gemv_i8", "M": bucket, "N": N, "K": K,
