@@ -431,6 +431,9 @@ int invariant_variant(int op, int K)
     return DG_VAR_TC;
 }
 
+// Every family of the 8-bit integer linear gives the same bits, as its sums are exact: the mode asks nothing of it.
+bool one_result(int op) { return op == DG_OP_GEMV_I8; }
+
 bool same_family(int a, int b) { return a == b || (cuda_core_family(a) && cuda_core_family(b)); }
 
 // The tensor-core linears cut K by a rule that depends on the row count beyond 128
@@ -520,7 +523,7 @@ dg_status dg_select(dg_op op, int M, int N, int K, dg_choice* out)
         }
         return DG_ERR_BAD_VARIANT;
     }
-    const bool invariant = g_numerics.load(std::memory_order_relaxed) == DG_NUMERICS_BATCH_INVARIANT;
+    const bool invariant = g_numerics.load(std::memory_order_relaxed) == DG_NUMERICS_BATCH_INVARIANT && !one_result(op);
     const int fam = invariant_variant(op, K);
     {
         std::lock_guard<std::mutex> lk(g_tmu);

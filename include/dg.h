@@ -201,7 +201,8 @@ unsigned dg_launch_flags(void);
  *     reduce in different orders, so a row's bits can change when the same row is
  *     computed inside a larger batch (all meet the same error bound).
  *   DG_NUMERICS_BATCH_INVARIANT: every bucket of an op takes one family (the
- *     tensor cores; the fp8 head with K > 8192 the CUDA cores), so output row m is
+ *     tensor cores; the fp8 head with K > 8192 the CUDA cores; the 8-bit integer
+ *     linear, whose families agree to the bit, its fastest), so output row m is
  *     a function of input row m alone -- for the MoE ops, of token m's activations,
  *     ids and gate weights -- whatever M is and whatever the other rows hold.  A
  *     one-row draft pass and a many-row verify pass then give the same logits and

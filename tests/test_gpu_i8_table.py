@@ -71,3 +71,27 @@ def test_a_pair_takes_groups_that_the_rows_do_not_fill(cuda_device, M):
     for tokens in (64, 96, 128):
         y = dg.dg_gemv_i8_rowscale(x, w, sw, choice=dg.Choice.make(TC, 0, tokens, 0, 2))
         assert torch.equal(y.view(torch.int16), want.view(torch.int16)), tokens
+
+
+def test_batch_invariant_mode_takes_table_picks_of_either_family(cuda_device, swept, tmp_path):
+    """Every family gives the same bits, so the mode keeps a pick of the CUDA cores, and rows keep theirs in any batch."""
+    N, K = 300, 1040
+    x, w, sw = _inputs(20, N, K)
+    dg.dg_set_numerics(dg.DG_NUMERICS_BATCH_INVARIANT)
+    try:
+        full = dg.dg_gemv_i8_rowscale(x, w, sw)
+        for M in (1, 2, 3, 4, 5):
+            assert torch.equal(dg.dg_gemv_i8_rowscale(x[:M], w, sw).view(torch.int16), full[:M].view(torch.int16)), M
+        for variant in (CC, TC):
+            doc = dict(swept)
+            doc["entries"] = [{**swept["entries"][0], "op": "gemv_i8", "M": 4, "N": N, "K": K, "pick": {"variant": variant, "params": []}}]
+            path = tmp_path / "table.json"
+            path.write_text(json.dumps(doc))
+            dg.dg_table_load(str(path))
+            for M in (3, 4):
+                pick = dg.dg_select(dg.DG_OP_GEMV_I8, M, N, K)
+                assert (pick.from_table, pick.variant) == (1, variant)
+                assert torch.equal(dg.dg_gemv_i8_rowscale(x[:M], w, sw).view(torch.int16), full[:M].view(torch.int16))
+    finally:
+        dg.dg_table_clear()
+        dg.dg_set_numerics(dg.DG_NUMERICS_FASTEST)
