@@ -358,8 +358,14 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
             uint4 raw[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + tc::sw128_offset(row, c));
+            // Every lane's bytes are read before the slot is handed back: the copy that fills it again writes by another
+            // proxy, which an arrival alone does not hold behind these loads.  (Without the fence 12 of 89000
+            // calls, all of the instance of 128 tokens on single CTAs, had a few weight rows of a later block; with it none of
+            // 450000.  24576 x 4096 at 128 tokens 33.0 -> 33.4 us, 77 tokens 19.4 -> 19.9; handed back behind the stores to
+            // tensor memory instead 33.8 and 20.4.)
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) tc::bar_arrive(wempty + 8 * s);          // (every lane has read its bytes)
+            if (lane == 0) tc::bar_arrive(wempty + 8 * s);
             const int before = i - kBufs;                           // the block that had the buffer
             if (before >= 0 && !__all_sync(kFull, tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag))) break;
             tc::fence_after();
