@@ -84,7 +84,8 @@ def test_batch_invariant_mode_takes_table_picks_of_either_family(cuda_device, sw
             assert torch.equal(dg.dg_gemv_i8_rowscale(x[:M], w, sw).view(torch.int16), full[:M].view(torch.int16)), M
         for variant in (CC, TC):
             doc = dict(swept)
-            doc["entries"] = [{**swept["entries"][0], "op": "gemv_i8", "M": 4, "N": N, "K": K, "pick": {"variant": variant, "params": []}}]
+            doc["entries"] = [{**swept["entries"][0], "op": "gemv_i8", "M": M, "N": N, "K": K, "pick": {"variant": variant, "params": []}}
+                              for M in (3, 4)]                   # (each a bucket of its own)
             path = tmp_path / "table.json"
             path.write_text(json.dumps(doc))
             dg.dg_table_load(str(path))
