@@ -175,6 +175,9 @@ __global__ void __launch_bounds__(kBulkThreads, 1) cc_bulk_kernel(DenseArgs a, i
                     fma_vector<WT, MT, RW, MTP>(w, xs + k / 8, kv, p);
                 }
             }
+            // Every lane's vectors are read before the stage is handed back: the copies that fill it again write by
+            // another proxy, which an arrival alone does not hold behind these loads.
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(empty0 + 8 * s) : "memory");
             reduce_scatter<Q>(p, lane);
