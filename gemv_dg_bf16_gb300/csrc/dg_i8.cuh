@@ -3,9 +3,9 @@
 // A row of bf16 values with largest magnitude amax >= 0 becomes, in binary32 (every step one
 // correctly rounded operation, so that codes and scales are defined to the last bit):
 //   A = max(amax, 2^-100),  r = 127 * (1 / A),  s = A * fl(1 / 127),  q = round-to-nearest-even(x * r)
-// |q| <= 127: amax * r is within 2^-21 of 127 (1 / A may be subnormal, where it has 22 bits at least).  The
-// floor keeps r finite; an all-zero row has codes 0.  A row that holds an infinity or a NaN has codes 0
-// and scale NaN.
+// |q| <= 127: amax * r is 127 to a relative 2^-21, so within 2^-14 (1 / A may be subnormal, where it has 22 bits at
+// least).  The floor keeps r finite; an all-zero row has codes 0.  A row that holds an infinity or a NaN has
+// codes 0 and scale NaN.
 //
 // Products are exact.  An 8-bit integer is exact in binary16, a product of two in binary32, and a
 // sum of at most 1024 of them is at most 1024 * 127 * 128 < 2^24, so that a chain of f16 MMAs
