@@ -4,6 +4,10 @@ The functions carry the C ABI's names and only marshal arguments: every step of
 the computation runs in the library's CUDA kernels.  Importing this package does
 not load the library; the first call does, and it raises if the library is
 missing (there is no CPU fallback).
+
+No call records an autograd graph: what it returns is detached, whatever its inputs
+require.  Gradients are calls of their own (dg_moe_combine_grad, and dg_moe_combine
+without weights for dg_moe_gather), for a torch.autograd.Function to make.
 """
 from ._binding import (  # noqa: F401
     DG_OP_GATE_UP_SILU, DG_OP_GEMV_BF16, DG_OP_HEAD_FP8_ARGMAX, DG_OP_MOE_W1, DG_OP_MOE_W2, DG_OP_GEMV_A8W8, DG_OP_GEMV_A4W4,

@@ -607,7 +607,8 @@ def dg_logits_adjust(logits, tokens=None, lengths=None, prompt_lengths=None, rep
                      presence=None, bias_ids=None, bias=None, mask=None, out=None, stream=None):
     """logits [M, V] (bf16 or fp32, any row stride) with penalties for used tokens [M, L] int32 (the first
     prompt_lengths[m] of lengths[m] are the prompt's), biases [M, B] of the entries bias_ids [M, B], and -inf
-    where bit v of mask [M, ceil(V / 32)] int32 is 0.  Into out; None: in place."""
+    where bit v of mask [M, ceil(V / 32)] int32 is 0.  Into out; None: in place.  Time goes by L, whatever the lengths:
+    of a buffer wider than the longest list, pass a view of the columns in use."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return dg_logits_adjust(logits, tokens, lengths, prompt_lengths, repetition, frequency, presence, bias_ids,

@@ -543,7 +543,10 @@ typedef struct {
 
 /* out = logits with the edits; out == logits (and ld_out == ld) works in place, where only what changes
  * is written; otherwise the two do not overlap.  logits and out [M, V] of one type (ld, ld_out), on
- * their element's boundary.  1 <= V <= 2^24, M >= 1, 0 <= n_tokens <= 2^24, 0 <= n_bias <= 1024. */
+ * their element's boundary.  1 <= V <= 2^24, M >= 1, 0 <= n_tokens <= 2^24, 0 <= n_bias <= 1024.
+ * The lengths are on the device, so the kernels are chosen by n_tokens: of a buffer wider than the longest
+ * list, pass the width in use (ld_tokens keeps the buffer's rows apart).  256 rows of 248320 with lists of up
+ * to 1000 tokens take 126 us as 32768 columns and 54 us as 1000. */
 dg_status dg_logits_adjust(const void* logits, int logits_type, int64_t ld, void* out, int64_t ld_out,
                            const dg_logits_edits* edits, int M, int V, dg_stream_t stream);
 
