@@ -29,9 +29,6 @@
 // between a quantisation, a first load and a fold; 4099 x 12288 at 77 19.3; 24576 x 4096 at 512 81.2, 1.27 PFLOP/s.
 // Every wait is bounded: on timeout the kernel flags DG_DEVERR_WAIT_TIMEOUT and winds down.
 #include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
 
 #include "dg_i8.cuh"
 #include "dg_internal.h"
@@ -39,6 +36,10 @@
 
 namespace dg {
 namespace {
+
+using tc::cluster_rank;
+using tc::cluster_sync_all;
+using tc::map_to_rank;
 
 constexpr int kTileRows = 128;                     // MMA M
 constexpr int kBlock = 128;                        // K elements a stage: one swizzled row of bytes
@@ -68,26 +69,6 @@ struct I8Args {
     uint16_t* y;
     uint8_t* ws;
 };
-
-__device__ __forceinline__ void cluster_sync_all()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t local_addr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local_addr), "r"(rank));
-    return r;
-}
 
 // Four integers into the shared memory of a CTA of the cluster.
 __device__ __forceinline__ void st_cluster(uint32_t addr, int a, int b, int c, int d)
@@ -551,29 +532,6 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
 
 // ------------------------------------------------------------------------ host
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-// 2-D tiled map over bytes, 128-byte swizzle.
-bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer)
-{
-    std::call_once(g_encode_once, [] {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-        cudaGetLastError();
-    });
-    if (!g_encode) return false;
-    const cuuint64_t dims[2] = {inner, outer};
-    const cuuint64_t strides[1] = {inner};
-    const cuuint32_t box[2] = {box_inner, box_outer};
-    const cuuint32_t estr[2] = {1, 1};
-    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 const void* kernel_of(int mp, bool pair)
 {
     if (pair)
@@ -751,7 +709,7 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     a.y = static_cast<uint16_t*>(y);
     a.ws = static_cast<uint8_t*>(ws);
     CUtensorMap tmW;
-    if (!encode_2d(&tmW, Wq, static_cast<uint64_t>(K), static_cast<uint64_t>(N), kBlock, kTileRows)) return DG_ERR_CUDA;
+    if (!encode_2d(&tmW, Wq, static_cast<uint64_t>(K), static_cast<uint64_t>(N), kBlock, kTileRows, true)) return DG_ERR_CUDA;
     const dg_status st = launch_i8_quant(dev, x, qws, const_cast<float*>(a.sx), M, K, xt, stream);
     if (st != DG_OK) return st;
     void* args[] = {&tmW, &a};

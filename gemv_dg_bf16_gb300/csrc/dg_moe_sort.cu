@@ -18,7 +18,7 @@
 // order in binary32.  Bytes bind them: rows of 4096 bf16, 8 slots: 32768 tokens there 355.6 us and back 354.5 (6.8 TB/s),
 // 8192 back 90.1 and the gradient 171.9 (6.6 TB/s); 64 tokens are a launch and two loads in a row, 2.2 us.
 #include "dg_internal.h"
-#include "dg_common.cuh"
+#include "dg_tc_common.cuh"
 
 namespace dg {
 namespace {
@@ -36,26 +36,11 @@ struct SortArgs {
     uint64_t recip;                      // 2^32 / topk, rounded up
 };
 
-__device__ __forceinline__ uint32_t ctarank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
 __device__ __forceinline__ int ld_peer(const int* local, uint32_t rank)
 {
-    uint32_t at;
     int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(local))), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(tc::map_to_rank(tc::su32(local), rank)) : "memory");
     return v;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // The expert of slot i, or -1 where its id is outside [0, E) or an earlier slot of its token has it.
@@ -74,7 +59,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_sort_kernel(SortArgs a)
     extern __shared__ int sh[];
     __shared__ int again;                                  // some token of a block has an expert twice
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, words = a.block / 32;
-    const int rank = static_cast<int>(ctarank()), ctas = gridDim.x;
+    const int rank = static_cast<int>(tc::cluster_rank()), ctas = gridDim.x;
     uint32_t* bits = reinterpret_cast<uint32_t*>(sh);      // [words][E]
     int* front = sh + words * a.E;                         // [words][E]: bits of the words in front
     int* total = front + words * a.E;                      // [E]: this CTA's slots of each expert
@@ -130,7 +115,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_sort_kernel(SortArgs a)
     uint32_t live = 0;
     for (int b = 0; b < blocks; ++b) live = build(b, true);
     if (ctas > 1)
-        cluster_sync();
+        tc::cluster_sync_all();
     else
         __syncthreads();
     // Experts in runs of `per` a thread: slots of lower experts, and of this one in the CTAs in front.
@@ -161,7 +146,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) moe_sort_kernel(SortArgs a)
     }
     if (rank == 0 && threadIdx.x == 0) a.offsets[a.E] = all;
     if (ctas > 1)
-        cluster_sync();                            // (no CTA leaves while others read its totals)
+        tc::cluster_sync_all();                            // (no CTA leaves while others read its totals)
     else
         __syncthreads();
     for (int b = 0; b < blocks; ++b) {

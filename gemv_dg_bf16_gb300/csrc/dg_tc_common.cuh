@@ -293,6 +293,28 @@ __device__ __forceinline__ void split_chunk(const uint16_t* row, int k0, int K, 
     lo = make_uint4(lw[0], lw[1], lw[2], lw[3]);
 }
 
+// Every thread of every CTA of the cluster executes this, unconditionally.
+__device__ __forceinline__ void cluster_sync_all()
+{
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// The place in the shared memory of the cluster's CTA `rank` of what is at local_addr here.
+__device__ __forceinline__ uint32_t map_to_rank(uint32_t local_addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local_addr), "r"(rank));
+    return r;
+}
+
 // Byte offset of 16-byte chunk c of row r inside a 128-byte-swizzled K-major block
 // (8-row groups of 1024 bytes).
 __device__ __forceinline__ uint32_t sw128_offset(int r, int c)
@@ -301,4 +323,9 @@ __device__ __forceinline__ uint32_t sw128_offset(int r, int c)
 }
 
 }  // namespace tc
+
+// 2-D tiled map of rows of `inner` elements, 128-byte swizzle: bf16, or bytes when `u8` (dg_tc_dense.cu).
+bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
+               bool u8 = false);
+
 }  // namespace dg

@@ -114,12 +114,9 @@ __host__ __device__ inline size_t a8_extra_bytes(int xq_blocks, int mp)
     return static_cast<size_t>(xq_blocks) * mp * (kA8Block + 4);
 }
 
-// Every thread of every CTA of the cluster executes this, unconditionally.
-__device__ __forceinline__ void cluster_sync_all()
-{
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+using tc::cluster_rank;
+using tc::cluster_sync_all;
+using tc::map_to_rank;
 
 // The same barrier in two halves: every thread arrives once, and waits (once) before
 // its next arrival or its first access to a peer's shared memory.  The arrival is
@@ -137,20 +134,6 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // tokens 64 bytes apart modulo 128, so the fold's 16-byte reads of two tokens fall in
 // different bank halves (a stride of 128 rows sends every token to the same banks).
 constexpr int kPStride = 144;
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t local_addr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local_addr), "r"(rank));
-    return r;
-}
 
 // Rows [lo, hi) of a 128-row tile folded by rank r of an ns-rank cluster
 // (multiples of 4, so a (gate, up) row pair never straddles two ranks).
@@ -963,9 +946,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-// 2-D tiled map, 128-byte swizzle: bf16 elements, or bytes (e4m3 codes) when `u8`.
+}  // namespace
+
+// 2-D tiled map, 128-byte swizzle: bf16 elements, or bytes (e4m3 or integer codes) when `u8`.
 bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner,
-               uint32_t box_outer, bool u8 = false)
+               uint32_t box_outer, bool u8)
 {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
@@ -985,6 +970,8 @@ bool encode_2d(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, 
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 template <int MP, int EPI>
 const void* tc_fn()
