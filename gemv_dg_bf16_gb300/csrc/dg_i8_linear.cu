@@ -21,12 +21,14 @@
 // Each rank of a K split folds a share of the tokens, and the others write their integers of these into its
 // shared memory.
 //
-// Groups of 64 tokens and more, many units and 16 blocks or more, K not split: a pair of CTAs has a unit of 256 weight rows, and one MMA
-// (cta_group::2) multiplies both CTAs' 128 rows of A with the N of both, of which each loads and holds half.  Of the
-// two the even one issues; what it waits for and what it frees goes through barriers of both.  What binds it at 128 tokens: the
-// MMAs take 512 cycles a block, its 32 KB 510 at the 64 bytes a clock that an SM takes in, and blocks come every 720.
-// Measured (calls in turn, quantisation included): 12288 x 4096 at 16 tokens 14.0 us, 3.6 TB/s of weights -- 8 us of stream
-// between a quantisation, a first load and a fold; 4099 x 12288 at 77 19.3; 24576 x 4096 at 512 81.2, 1.27 PFLOP/s.
+// Groups of 64 tokens and more, many units and 16 blocks or more, K not split: a pair of CTAs has a unit of 256
+// weight rows, and one MMA (cta_group::2) multiplies both CTAs' 128 rows of A with the N of both, of which each loads
+// and holds half.  Of the two the even one issues; what it waits for and what it frees goes through barriers of both.
+// What binds it at 128 tokens: the MMAs take 512 cycles a block, its 32 KB 510 at the 64 bytes a clock that an SM takes
+// in, and blocks come every 720.
+// Measured (calls in turn, quantisation included): 12288 x 4096 at 16 tokens 14.1 us, 3.6 TB/s of weights -- 8 us of
+// stream between a quantisation, a first load and a fold; 4099 x 12288 at 77 19.9; 24576 x 4096 at 512 82.1, 1.26
+// PFLOP/s.
 // Every wait is bounded: on timeout the kernel flags DG_DEVERR_WAIT_TIMEOUT and winds down.
 #include <cuda.h>
 
@@ -73,7 +75,8 @@ struct I8Args {
 // Four integers into the shared memory of a CTA of the cluster.
 __device__ __forceinline__ void st_cluster(uint32_t addr, int a, int b, int c, int d)
 {
-    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+    asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
 }
 
 // Both barriers' phases complete (the two tests in flight at once; then the bounded waits).
@@ -114,8 +117,10 @@ template <bool PAIR>
 __device__ __forceinline__ void commit(uint32_t bar)
 {
     if constexpr (PAIR)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                     ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+            ::"r"(bar), "h"(static_cast<uint16_t>(3))
+            : "memory");
     else
         tc::commit(bar);
 }
@@ -125,6 +130,9 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+
+// The phase in which block i is told done.
+__device__ __forceinline__ uint32_t done_phase(int i) { return static_cast<uint32_t>(i / kDone) & 1u; }
 
 // Whether a condition holds in all of the 128 epilogue threads (a barrier for them).
 __device__ __forceinline__ bool all_of(bool p)
@@ -149,7 +157,8 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
     constexpr uint32_t kA0 = 2 * MP < 64 ? 64 : 2 * MP;             // first column of the converted blocks
     constexpr uint32_t kCols = MP <= 32 ? 256 : 512;               // two accumulators, kBufs converted blocks
     constexpr int kBufs = MP <= 32 ? 3 : 4;
-    constexpr int kSets = Roles<PAIR>::kSets, kConvert = Roles<PAIR>::kConvert, kEpilogue = Roles<PAIR>::kEpilogue, kStreamX = Roles<PAIR>::kStreamX;
+    constexpr int kSets = Roles<PAIR>::kSets, kConvert = Roles<PAIR>::kConvert;
+    constexpr int kEpilogue = Roles<PAIR>::kEpilogue, kStreamX = Roles<PAIR>::kStreamX;
     static_assert(kA0 + kBufs * kACols <= kCols, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -164,14 +173,17 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
     // done[i % kDone]: block i is multiplied, its activations' slot and its converted weights' buffer are free
     const uint32_t wfull = tc::su32(bars), wempty = wfull + 8 * SW, xfull = wempty + 8 * SW, done = xfull + 8 * SX;
     const uint32_t afull = done + 8 * kDone, dfull = afull + 8 * kBufs, dempty = dfull + 16;
-    int* fold = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + nbars * 8 + 16);   // [rank][share / 4][row][4]
+    // [rank][share / 4][row][4]
+    int* fold = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + nbars * 8 + 16);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool split = !PAIR && a.nsplit > 1;
     const int rank = split ? static_cast<int>(cluster_rank()) : 0, half = PAIR ? static_cast<int>(cluster_rank()) : 0;
     constexpr int kUnitRows = PAIR ? 2 * kTileRows : kTileRows;
-    // Units `first`, first + stride, ...; groups of one tile run side by side, so that its weights come from memory once.
-    const int first = static_cast<int>(blockIdx.x) / (PAIR ? 2 : a.nsplit), stride = split ? a.units : static_cast<int>(gridDim.x) / (PAIR ? 2 : 1);
+    // Units `first`, first + stride, ...; groups of one tile run side by side, so that its weights come from memory
+    // once.
+    const int first = static_cast<int>(blockIdx.x) / (PAIR ? 2 : a.nsplit);
+    const int stride = split ? a.units : static_cast<int>(gridDim.x) / (PAIR ? 2 : 1);
     const int kb0 = static_cast<int>(static_cast<long long>(rank) * a.nkb / a.nsplit);
     const int nk = static_cast<int>(static_cast<long long>(rank + 1) * a.nkb / a.nsplit) - kb0;     // blocks of a unit
 
@@ -195,12 +207,12 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
     }
     if (warp == 1) {
         if constexpr (PAIR) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tmem_holder)),
-                         "r"(kCols));
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(tc::su32(tmem_holder)), "r"(kCols));
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
         } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::su32(tmem_holder)),
-                         "r"(kCols));
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(tc::su32(tmem_holder)), "r"(kCols));
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         }
     }
@@ -211,8 +223,8 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
     const uint32_t tmem = *tmem_holder;
     pdl_launch_dependents();
     if (split) {
-        __syncwarp();
-        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // (waited for in front of the first remote access)
+        __syncwarp();                                               // (waited for in front of the first remote access)
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     }
 
     // After a wait that ran out: the copies in flight of a ring whose last `issued` loads went round
@@ -233,15 +245,17 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                 const uint64_t once = tc::policy_evict_first();
                 int s = 0, issued = 0;
                 uint32_t round = 0;
-                // A unit begins at a block of its tile's own, so that not all of them ask for the same activations at a time
-                // (24576 x 4096 at 512 tokens 82.0 -> 81.2 us; the order of blocks changes no sum).
+                // A unit begins at a block of its tile's own, so that not all of them ask for the same activations at
+                // a time (24576 x 4096 at 512 tokens 82.0 -> 81.2 us; the order of blocks changes no sum).  Weights
+                // have nothing to wait for.
                 for (int u = first; u < a.units && !*abort_flag; u += stride) {
                     const int tile = u / a.groups, row = tile * kUnitRows + half * kTileRows;
-                    for (int i = 0, kb = tile % nk; i < nk; ++i, kb = kb + 1 < nk ? kb + 1 : 0) {       // weights: nothing to wait for
+                    for (int i = 0, kb = tile % nk; i < nk; ++i, kb = kb + 1 < nk ? kb + 1 : 0) {
                         if (round > 0 && !tc::bar_wait(wempty + 8 * s, (round - 1) & 1u, abort_flag)) break;
                         tc::bar_expect_tx(wfull + 8 * s, kWBox);
                         if (a.groups == 1)
-                            tc::tma_2d_hint(tc::su32(smem + s * kWBox), &tmW, (kb0 + kb) * kBlock, row, wfull + 8 * s, once);
+                            tc::tma_2d_hint(tc::su32(smem + s * kWBox), &tmW, (kb0 + kb) * kBlock, row,
+                                            wfull + 8 * s, once);
                         else
                             tc::tma_2d(tc::su32(smem + s * kWBox), &tmW, (kb0 + kb) * kBlock, row, wfull + 8 * s);
                         ++issued;
@@ -253,7 +267,7 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                 }
                 if (*abort_flag) drain(wfull, issued, SW);
             }
-            __syncwarp();                                               // (a lane in pdl_wait() holds up the whole warp)
+            __syncwarp();                                           // (a lane in pdl_wait() holds up the whole warp)
             pdl_wait();
         } else if (warp == kStreamX) {
             pdl_wait();
@@ -261,14 +275,17 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                 int s = 0, issued = 0;
                 uint32_t round = 0;
                 for (int u = first; u < a.units && !*abort_flag; u += stride) {
-                    const int group = PAIR ? u % a.groups * 2 + half : u % a.groups;        // (PAIR: tiles of half a group)
+                    // (PAIR: tiles of half a group)
+                    const int group = PAIR ? u % a.groups * 2 + half : u % a.groups;
                     const uint8_t* src = a.x + (static_cast<size_t>(group) * a.nkb + kb0) * xstage;
                     for (int i = 0, kb = u / a.groups % nk; i < nk; ++i, kb = kb + 1 < nk ? kb + 1 : 0) {
-                        const int before = issued - SX;                 // the block that had the slot
-                        if (before >= 0 && !tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag)) break;
+                        const int before = issued - SX;             // the block that had the slot
+                        if (before >= 0 && !tc::bar_wait(done + 8 * (before % kDone), done_phase(before), abort_flag))
+                            break;
                         const uint32_t dst = tc::su32(xring + s * xstage);
                         tc::bar_expect_tx(xfull + 8 * s, static_cast<uint32_t>(xstage));
-                        tc::bulk_load(dst, src + static_cast<size_t>(kb) * xstage, static_cast<uint32_t>(xstage), xfull + 8 * s);
+                        tc::bulk_load(dst, src + static_cast<size_t>(kb) * xstage, static_cast<uint32_t>(xstage),
+                                      xfull + 8 * s);
                         ++issued;
                         if (++s == SX) {
                             s = 0;
@@ -287,19 +304,22 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                 for (int u = first; u < a.units && !*abort_flag; u += stride) {
                     for (int i = 0, in = 0; i < nk; ++i, ++block) {     // in: blocks of the segment so far
                         const int d = seg & 1;
-                        if constexpr (PAIR) {                           // (whoever converted has seen the activations too)
+                        if constexpr (PAIR) {                       // (whoever converted has seen the activations too)
                             if (!tc::bar_wait(afull + 8 * b, bround & 1u, abort_flag)) break;
-                            if (in == 0 && seg >= 2 && !tc::bar_wait(dempty + 8 * d, static_cast<uint32_t>(seg / 2 - 1) & 1u, abort_flag)) break;
                         } else {
                             if (!wait_both(xfull + 8 * s, round & 1u, afull + 8 * b, bround & 1u, abort_flag)) break;
-                            if (in == 0 && seg >= 2 && !tc::bar_wait(dempty + 8 * d, static_cast<uint32_t>(seg / 2 - 1) & 1u, abort_flag)) break;
                         }
+                        if (in == 0 && seg >= 2 &&
+                            !tc::bar_wait(dempty + 8 * d, static_cast<uint32_t>(seg / 2 - 1) & 1u, abort_flag))
+                            break;
                         tc::fence_after();
                         const uint64_t x0 = ring + static_cast<uint64_t>(s * (xstage / 16));
 #pragma unroll
                         for (int kk = 0; kk < kBlock / 16; ++kk)
-                            mma_f16_ta<PAIR>(tmem + static_cast<uint32_t>(d * MP), tmem + kA0 + static_cast<uint32_t>(b * kACols + kk * 8),
-                                             x0 + (kk < 4 ? 0 : box) + static_cast<uint64_t>((kk % 4) * 2), idesc, (in > 0 || kk > 0) ? 1u : 0u);
+                            mma_f16_ta<PAIR>(tmem + static_cast<uint32_t>(d * MP),
+                                             tmem + kA0 + static_cast<uint32_t>(b * kACols + kk * 8),
+                                             x0 + (kk < 4 ? 0 : box) + static_cast<uint64_t>((kk % 4) * 2), idesc,
+                                             (in > 0 || kk > 0) ? 1u : 0u);
                         commit<PAIR>(done + 8 * (block % kDone));
                         if (++in == kSegBlocks || i == nk - 1) {
                             commit<PAIR>(dfull + 8 * d);
@@ -339,16 +359,18 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
             uint4 raw[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) raw[c] = *reinterpret_cast<const uint4*>(src + tc::sw128_offset(row, c));
-            // Every lane's bytes are read before the slot is handed back: the copy that fills it again writes by another
-            // proxy, which an arrival alone does not hold behind these loads.  (Without the fence 12 of 89000
-            // calls, all of the instance of 128 tokens on single CTAs, had a few weight rows of a later block; with it none of
-            // 450000.  24576 x 4096 at 128 tokens 33.0 -> 33.4 us, 77 tokens 19.4 -> 19.9; handed back behind the stores to
-            // tensor memory instead 33.8 and 20.4.)
+            // Every lane's bytes are read before the slot is handed back: the copy that fills it again writes by
+            // another proxy, which an arrival alone does not hold behind these loads.  (Without the fence 12 of 89000
+            // calls, all of the instance of 128 tokens on single CTAs, had a few weight rows of a later block; with it
+            // none of 450000.  24576 x 4096 at 128 tokens 33.0 -> 33.4 us, 77 tokens 19.4 -> 19.9; handed back behind
+            // the stores to tensor memory instead 33.8 and 20.4.)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) tc::bar_arrive(wempty + 8 * s);
             const int before = i - kBufs;                           // the block that had the buffer
-            if (before >= 0 && !__all_sync(kFull, tc::bar_wait(done + 8 * (before % kDone), static_cast<uint32_t>(before / kDone) & 1u, abort_flag))) break;
+            if (before >= 0 &&
+                !__all_sync(kFull, tc::bar_wait(done + 8 * (before % kDone), done_phase(before), abort_flag)))
+                break;
             tc::fence_after();
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
@@ -390,7 +412,8 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
         bool good = true;
 #pragma unroll 1
         for (int u = first, k = 0; u < a.units && good; u += stride, ++k) {
-            const int t0 = u % a.groups * a.mp, rows_here = min(a.mp, a.M - t0), nrow = u / a.groups * kUnitRows + half * kTileRows + row;
+            const int t0 = u % a.groups * a.mp, rows_here = min(a.mp, a.M - t0);
+            const int nrow = u / a.groups * kUnitRows + half * kTileRows + row;
             const float sw = a.sw[min(nrow, a.N - 1)];
             float* sxt = sxs + (k & 1) * MP;
             for (int t = threadIdx.x - kEpilogue * 32; t < rows_here; t += 128) sxt[t] = ld_cg_f32(a.sx + t0 + t);
@@ -407,7 +430,7 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                 tc::fence_after();
 #pragma unroll
                 for (int c = 0; c < MP / 16; ++c) {
-                    if (c < MP / 16 - 1 || a.mp == MP) {            // (an instance serves mp = MP and, from 64 on, MP - 16)
+                    if (c < MP / 16 - 1 || a.mp == MP) {    // (an instance serves mp = MP and, from 64 on, MP - 16)
                         uint32_t v[16];
                         tc::tmem_ld16(tlane + static_cast<uint32_t>(d * MP + c * 16), v);
 #pragma unroll
@@ -423,7 +446,8 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                         tc::bar_arrive(dempty + 8 * d);
                 }
             }
-            // A wait that ran out ends the loop in all 128 threads or in none (they meet here, and the scales are there).
+            // A wait that ran out ends the loop in all 128 threads or in none (they meet here, and the scales are
+            // there).
             good = all_of(good && !*abort_flag);
             if (!good) break;
             if (split) {
@@ -439,17 +463,19 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                         at = rank * a.share;
                         peer = map_to_rank(tc::su32(fold), static_cast<uint32_t>(++to));
                     }
-                    st_cluster(peer + static_cast<uint32_t>((at * kTileRows + row * 4) * 4), tot[j], tot[j + 1], tot[j + 2], tot[j + 3]);
+                    st_cluster(peer + static_cast<uint32_t>((at * kTileRows + row * 4) * 4), tot[j], tot[j + 1],
+                               tot[j + 2], tot[j + 3]);
                     at += 4;
                 }
             } else if (a.N % 8 == 0 && nrow - row + kTileRows <= a.N) {
-                // Sixteen tokens at a time go through shared memory, [token][row] in turn in two places, and leave 16 bytes a
-                // lane, 256 of a token's outputs side by side.  (Straight from the lanes, 64 bytes a store, 128 tokens took 3.9 us.)
+                // Sixteen tokens at a time go through shared memory, [token][row] in turn in two places, and leave 16
+                // bytes a lane, 256 of a token's outputs side by side.  (Straight from the lanes, 64 bytes a store, 128
+                // tokens took 3.9 us.)
 #pragma unroll
                 for (int c = 0; c < MP / 16; ++c) {
                     if (c * 16 >= rows_here) break;
                     uint16_t* st = stage + (c & 1) * 16 * kTileRows;
-                    uint16_t v[16];                                 // (all read before the first is written: the compiler keeps their order)
+                    uint16_t v[16];         // (all read before the first is written: the compiler keeps their order)
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         const float4 sx = *reinterpret_cast<const float4*>(sxt + c * 16 + j);
@@ -465,7 +491,8 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                     for (int h = 0; h < 2; ++h) {
                         const int z = threadIdx.x - kEpilogue * 32 + h * 128, t = c * 16 + z / 16;
                         if (t < rows_here)
-                            *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(t0 + t) * a.N + (nrow - row) + z % 16 * 8) = *reinterpret_cast<const uint4*>(st + z * 8);
+                            *reinterpret_cast<uint4*>(a.y + static_cast<size_t>(t0 + t) * a.N + (nrow - row) +
+                                                      z % 16 * 8) = *reinterpret_cast<const uint4*>(st + z * 8);
                     }
                 }
             } else if (nrow < a.N) {
@@ -492,7 +519,7 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
             __syncwarp();
             asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");            // (the arrival at the start)
         }
-        cluster_sync_all();                                         // every rank's integers are in place; the last remote access
+        cluster_sync_all();                 // every rank's integers are in place; the last remote access
         if (warp >= kConvert && warp < kEpilogue + 4 && !*abort_flag) {
             // A warp takes 32 rows, the same ones of every third four tokens: a lane adds up a row's over the ranks.
             const int t0 = first % a.groups * a.mp, lo = rank * a.share, rows_here = min(a.mp, a.M - t0);
@@ -509,7 +536,8 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
                 if (nrow >= a.N) continue;
                 const int t = lo + z * 4;
                 const float4 sx = *reinterpret_cast<const float4*>(sxs + t);
-                const uint16_t out[4] = {i8::output(v.x, sx.x, sw), i8::output(v.y, sx.y, sw), i8::output(v.z, sx.z, sw), i8::output(v.w, sx.w, sw)};
+                const uint16_t out[4] = {i8::output(v.x, sx.x, sw), i8::output(v.y, sx.y, sw),
+                                         i8::output(v.z, sx.z, sw), i8::output(v.w, sx.w, sw)};
                 uint16_t* dst = a.y + static_cast<size_t>(t0 + t) * a.N + nrow;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -519,7 +547,7 @@ __global__ void __launch_bounds__(Roles<PAIR>::kThreads, MP <= 32 ? 2 : 1)
     }
     tc::fence_before();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync_all();                         // neither leaves while the other's MMAs or arrivals need it
+    if constexpr (PAIR) cluster_sync_all();         // neither leaves while the other's MMAs or arrivals need it
     if (*abort_flag && threadIdx.x == 0) set_status(a.ws, DG_DEVERR_WAIT_TIMEOUT);
     if (warp == 1) {
         tc::fence_after();
@@ -549,11 +577,16 @@ const void* kernel_of(int mp, bool pair)
 size_t smem_bytes(int mp, int xt, int sw, int sx, size_t fold)
 {
     const size_t most = mp <= 16 ? 16 : mp <= 32 ? 32 : mp <= 64 ? 64 : mp <= 96 ? 96 : 128;
-    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * xt * 256 + most * 8 + 2 * 16 * kTileRows * 2 + (2 * sw + sx + kDone + 10) * 8 + 16 + fold;
+    return 1024 + static_cast<size_t>(sw) * kWBox + static_cast<size_t>(sx) * xt * 256 + most * 8 +
+           2 * 16 * kTileRows * 2 + (2 * sw + sx + kDone + 10) * 8 + 16 + fold;
 }
 
 // Rows of the last group of up to 128 tokens and elements of the last block are there in full.
-size_t code_bytes(int M, int K) { return (static_cast<size_t>(M) + 127) * ((static_cast<size_t>(K) + kBlock - 1) / kBlock * kBlock) * 2; }
+size_t code_bytes(int M, int K)
+{
+    return (static_cast<size_t>(M) + 127) * ((static_cast<size_t>(K) + kBlock - 1) / kBlock * kBlock) * 2;
+}
+
 size_t scale_bytes(int M) { return (static_cast<size_t>(M) * 4 + 255) / 256 * 256; }
 
 // Tokens of a group: equal groups of up to `most`, rounded up to the MMA's 16.
@@ -563,10 +596,11 @@ int group_tokens(int M, int most)
     return ((M - 1) / groups + 16) / 16 * 16;
 }
 
-// What a call of `units` units of mp tokens takes in us with K in ns ranges, roughly, for a choice among them: a launch, an
-// epilogue that grows with the tokens, the fold, and 0.4 a block of K of an SM, one CTA after the other on it or (K
-// split, up to 32 tokens) two side by side.  Where hardly an SM is left over, the next launch's first loads come late.  Fitted
-// to 4.2 us for 64 x 256 at 24 tokens to 21 for 4096 x 4096 at 400: 66 shapes, cuts and counts of tokens within a fifth or so.
+// What a call of `units` units of mp tokens takes in us with K in ns ranges, roughly, for a choice among them: a
+// launch, an epilogue that grows with the tokens, the fold, and 0.4 a block of K of an SM, one CTA after the other on
+// it or (K split, up to 32 tokens) two side by side.  Where hardly an SM is left over, the next launch's first loads
+// come late.  Fitted to 4.2 us for 64 x 256 at 24 tokens to 21 for 4096 x 4096 at 400: 66 shapes, cuts and counts of
+// tokens within a fifth or so.
 float estimate(int sms, long long units, int nkb, int mp, int ns)
 {
     const long long ctas = units * ns;
@@ -587,46 +621,69 @@ size_t i8_workspace_bytes(int M, int K)
     return kWsData + code_bytes(M, K) + scale_bytes(M);
 }
 
-dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw, void* y,
-                           int M, int N, int K, void* ws, size_t ws_bytes, cudaStream_t stream)
+// How a call is cut, where its choice leaves that open.  Measured, both sides in us at the time:
+//   ranks       all that are resident at once; where two CTAs share an SM, at most 263 of the 304 (12288 x 4096 at 16
+//               tokens: two ranks 14.0, three 18.5).  None up to 512 elements, where a launch of clusters and the fold
+//               cost more than the blocks (256 x 512, one rank / two: 16 tokens 4.65 / 4.9, 64 6.3 / 6.75, 300 8.05 /
+//               9.35), nor for groups past 112 tokens, beside whose integers two stages of weights are left.
+//   thirds      up to 32 tokens, for a few more units than SMs and long ones: not a second round for some SMs (16
+//               tokens, one rank / three: 20480 x 5120 32.3 / 25.5, 24576 x 8192 49.3 / 41.2, 20480 x 12288 71.5 /
+//               49.5; not 24576 x 4096 27.3 / 27.3 and at 8 27.2 / 30.0, 26000 x 4096 28.6 / 34.9, 20480 x 2560 18.2 /
+//               18.7; at 64 tokens 24576 x 4096 30.7 / 48.7).
+//   groups      above 16 tokens the groups and ranks of least estimate (with groups of up to 128 and all the ranks
+//               that fit / so: 64 x 256 at 400 tokens 7.1 / 4.5, 1024 x 512 at 200 8.1 / 5.3, 2048 x 1024 at 100 9.6 /
+//               7.0, 4096 x 1024 at 200 11.2 / 8.2).
+//   pairs       of CTAs for 256 rows, where K is not split and a group has 64 tokens or more.  Each holds half of the
+//               activations, so that an SM takes in 32 KB a block at 128 tokens and not 48 (it takes 61 bytes a clock
+//               at most), and three sets convert (pair / single CTAs: 24576 x 4096 at 512 tokens 82.1 / 95.0, 256 45.3
+//               / 51.7, 128 33.4 / 37.3, 64 29.1 / 31.5; 8192 x 8192 at 256 32.6 / 36.6; groups rounded up to 32
+//               tokens: 20480 x 5120 at 160 47.4 / 48.1).  Not for few units or a short K (4096 x 4096 at 200 19.1 /
+//               18.0, 2048 x 1024 at 400 11.7 / 10.1).
+//   rings       a K split of up to 32 tokens has two CTAs an SM, or leaves room for the next launch's, whose first
+//               weights then come under this one's tail (12288 x 4096 at 16 tokens: two ranks 14.0, with deep rings
+//               and one CTA an SM 20.7).  Elsewhere they are as deep as an SM holds (19456 x 8192 at 16 tokens: 4
+//               stages 39.7, 8 30.1).  Activations wait behind the weights that are on their way: their ring is as
+//               long as the weights', or as there is room.
+dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void* x, const void* Wq, const float* sw,
+                           void* y, int M, int N, int K, void* ws, size_t ws_bytes, cudaStream_t stream)
 {
     if (ws_bytes < i8_workspace_bytes(M, K)) return DG_ERR_WORKSPACE_TOO_SMALL;
     for (int i = 0; i < 6; ++i)
         if (c.params[i] < 0 || (i > 3 && c.params[i] != 0)) return DG_ERR_BAD_VARIANT;
+    // A multiple of the converting sets as weights' stages: a slot then belongs to one set, which sees its phases in
+    // turn.  (A set that waits for a slot's next phase while the one before, another set's, is not complete would pass
+    // at once.)
+    const int want_stages = c.params[0], want_tokens = c.params[1], want_ranks = c.params[2], want_ctas = c.params[3];
+    if (want_stages > 8 || want_stages % 2 != 0 || want_tokens % 16 != 0 || want_tokens > 128 ||
+        want_ranks > kMaxRanks || want_ctas > 2)
+        return DG_ERR_BAD_VARIANT;
     const int tiles = (N - 1) / kTileRows + 1, nkb = (K - 1) / kBlock + 1;
-    if (c.params[1] % 16 != 0 || c.params[1] > 128 || c.params[2] > kMaxRanks) return DG_ERR_BAD_VARIANT;
+    const long long sms = dev->sm_count;
     int mp, groups, ns;
     long long units;
-    // most: tokens of a group.  A K split takes the ranks that are resident at once; where two CTAs share an SM, at most
-    // 263 of the 304 (12288 x 4096 at 16 tokens: two ranks 14.0 us, three 18.5).  Up to 512 elements a launch of clusters and
-    // the fold cost more than the blocks (256 x 512, one rank / two: 16 tokens 4.65 / 4.9 us, 64 6.3 / 6.75, 300 8.05 / 9.35).
-    auto cut = [&](int most) {
-        mp = c.params[1] > 0 ? c.params[1] : group_tokens(M, most);
+    auto cut = [&](int most) {                          // most: tokens of a group
+        mp = want_tokens > 0 ? want_tokens : group_tokens(M, most);
         if (mp > (M + 15) / 16 * 16) mp = (M + 15) / 16 * 16;
         groups = (M - 1) / mp + 1;
         units = static_cast<long long>(tiles) * groups;
-        ns = c.params[2] > 0 ? c.params[2] : 1;
-        if (c.params[2] == 0 && nkb > 4)
+        ns = want_ranks > 0 ? want_ranks : 1;
+        if (want_ranks == 0 && nkb > 4)
             for (int r = 2; r <= kMaxRanks && 2 * r <= nkb; ++r)
-                if (units <= tc_cluster_capacity(dev, mp <= 32, r) && (mp > 32 || units * r <= 2 * dev->sm_count * 13 / 15)) ns = r;
-        // A few more units than SMs, and long ones: thirds of K in clusters, and not a second round for some SMs (16 tokens, one
-        // rank / three: 20480 x 5120 32.3 / 25.5 us, 24576 x 8192 49.3 / 41.2, 20480 x 12288 71.5 / 49.5; 24576 x 4096 27.3 / 27.3
-        // and at 8 27.2 / 30.0, 26000 x 4096 28.6 / 34.9, 20480 x 2560 18.2 / 18.7; 64 tokens, 24576 x 4096 30.7 / 48.7).
-        const long long sms = dev->sm_count;
-        if (c.params[2] == 0 && ns == 1 && mp <= 32 && nkb >= 32 && units > sms && (nkb >= 48 ? units * 7 <= sms * 9 : units * 6 <= sms * 7)) ns = 3;
+                if (units <= tc_cluster_capacity(dev, mp <= 32, r) && (mp > 32 || units * r <= 2 * sms * 13 / 15))
+                    ns = r;
+        if (want_ranks == 0 && ns == 1 && mp <= 32 && nkb >= 32 && units > sms &&
+            (nkb >= 48 ? units * 7 <= sms * 9 : units * 6 <= sms * 7))
+            ns = 3;
         if (ns > nkb) ns = nkb;
     };
     cut(128);
-    if (ns > 1 && mp > 112) {           // (beside more tokens' integers two stages of weights are left: by a choice only)
-        if (c.params[1] == 0)
+    if (ns > 1 && mp > 112) {
+        if (want_tokens == 0)
             cut(64);
-        else if (c.params[2] == 0)
+        else if (want_ranks == 0)
             ns = 1;
     }
-    // More than 16 tokens: the groups and the ranks with the least estimate.  (With groups of up to 128 and all the ranks that
-    // fit instead, us before / now: 64 x 256 at 400 tokens 7.1 / 4.5, 1024 x 512 at 200 8.1 / 5.3, 2048 x 1024 at 100 9.6 /
-    // 7.0, 4096 x 1024 at 200 11.2 / 8.2.)
-    if (M > kFewTokens && c.params[1] == 0 && c.params[2] == 0 && c.params[3] != 2) {
+    if (M > kFewTokens && want_tokens == 0 && want_ranks == 0 && want_ctas != 2) {
         float best = 0.0f;
         int most_best = 0, ns_best = 1;
         for (int most = 16; most <= 128; most += 16) {
@@ -643,17 +700,15 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
             }
         }
         cut(most_best);
-        if (!(ns == 3 && ns_best == 1 && units > dev->sm_count)) ns = ns_best;     // (cut's thirds of K stay)
+        if (!(ns == 3 && ns_best == 1 && units > sms)) ns = ns_best;     // (thirds stay)
     }
-    // A pair of CTAs for 256 rows where K is not split and a group has 64 tokens or more.  Each holds half of the
-    // activations, so that an SM takes in 32 KB a block at 128 tokens and not 48 (it takes 61 bytes a clock at most), and
-    // three sets convert: 24576 x 4096 at 512 tokens 81.2 us, single CTAs 93.8; at 256 45.3 / 51.7, 128 32.7 / 36.6, 64
-    // 28.8 / 30.5; 8192 x 8192 at 256 32.5 / 36.6.  Groups are rounded up to 32 tokens: 20480 x 5120 at 160 47.4 / 48.1.  Not
-    // for few units or a short K: 4096 x 4096 at 200 19.1 / 18.0, 2048 x 1024 at 400 11.7 / 10.1.
-    const bool pair = c.params[3] == 2 || (c.params[3] == 0 && ns == 1 && mp >= 64 && nkb >= 16 && units * 8 >= 5ll * dev->sm_count && (c.params[1] == 0 || mp % 32 == 0) && c.params[0] % 6 == 0);
+    bool pair = want_ctas == 2;
+    if (want_ctas == 0 && ns == 1 && mp >= 64 && nkb >= 16 && units * 8 >= 5 * sms)
+        pair = (want_tokens == 0 || mp % 32 == 0) && want_stages % 6 == 0;
     if (pair) {
         // (a group that the rows do not fill is a smaller one, of 64 tokens at least)
-        if (c.params[2] > 1 || (c.params[1] > 0 && (c.params[1] < 64 || c.params[1] % 32 != 0)) || c.params[0] % 6 != 0) return DG_ERR_BAD_VARIANT;
+        if (want_ranks > 1 || (want_tokens > 0 && (want_tokens < 64 || want_tokens % 32 != 0)) || want_stages % 6 != 0)
+            return DG_ERR_BAD_VARIANT;
         mp = mp <= 64 ? 64 : (mp + 31) / 32 * 32;
         groups = (M - 1) / mp + 1;
         units = static_cast<long long>((tiles + 1) / 2) * groups;
@@ -662,28 +717,26 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     const int xt = pair ? mp / 2 : mp;
     const void* fn = kernel_of(mp, pair);
     const int threads = pair ? Roles<true>::kThreads : Roles<false>::kThreads;
-    if (units * ns > 0x7fffffffll || units * nkb / dev->sm_count > 0x3fffffff) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (units * ns > 0x7fffffffll || units * nkb / sms > 0x3fffffff) return DG_ERR_UNSUPPORTED_SHAPE;
     const int clusters = pair ? tc_cluster_capacity(dev, false, 2) : 0;
     if (pair && clusters < 1) return DG_ERR_UNSUPPORTED_SHAPE;
-    const long long grid = pair ? 2 * (units < clusters ? units : clusters) : ns > 1 || units < dev->sm_count ? units * ns : dev->sm_count;
+    const long long grid = pair                     ? 2 * (units < clusters ? units : clusters)
+                           : ns > 1 || units < sms ? units * ns
+                                                    : sms;
     const int share = ns > 1 ? (mp / 4 + ns - 1) / ns * 4 : mp;
     const size_t fold = ns > 1 ? static_cast<size_t>(ns) * share * kTileRows * 4 : 0;
-    // A K split of up to 32 tokens has two CTAs an SM, or leaves room for the next launch's, whose first weights then come
-    // under this one's tail (12288 x 4096 at 16 tokens: two ranks 14.0 us, with deep rings and one CTA an SM 20.7).
-    // Elsewhere the rings are as deep as an SM holds (19456 x 8192 at 16 tokens: 4 stages 39.7 us, 8 30.1).
     const size_t budget = mp <= 32 && ns > 1 ? 112 * 1024 : kMaxDynSmem;
-    // A multiple of the converting sets as weights' stages: a slot then belongs to one set, which sees its phases in
-    // turn.  (A set that waits for a slot's next phase while the one before, another set's, is not complete would pass
-    // at once.)
-    if (c.params[0] > 8 || c.params[0] % 2 != 0 || c.params[3] > 2) return DG_ERR_BAD_VARIANT;
-    // Activations wait behind the weights that are on their way: their ring is as long as the weights', or as there is room.
-    int stw = c.params[0] > 0 ? c.params[0] : mp <= 32 ? 8 : 6, stx = kDone - 1;
-    while (c.params[0] == 0 && !pair && stw > 4 && smem_bytes(mp, xt, stw, stw < kDone ? stw : kDone - 1, fold) > budget) stw -= 2;
-    while (stx > 2 && smem_bytes(mp, xt, stw, stx, fold) > budget) --stx;
-    while (c.params[0] == 0 && !pair && stw > 2 && smem_bytes(mp, xt, stw, stx, fold) > budget) stw -= 2;
+    int stw = want_stages > 0 ? want_stages : mp <= 32 ? 8 : 6, stx = kDone - 1;
+    const auto past = [&](size_t room, int x) { return smem_bytes(mp, xt, stw, x, fold) > room; };
+    if (want_stages == 0 && !pair)
+        while (stw > 4 && past(budget, stw < kDone ? stw : kDone - 1)) stw -= 2;
+    while (stx > 2 && past(budget, stx)) --stx;
+    if (want_stages == 0 && !pair)
+        while (stw > 2 && past(budget, stx)) stw -= 2;
     // A table's pick holds for every row count of its bucket, whose groups and ranks differ, and with them the stages
     // that fit: as deep as this call's (two of each always do; depth changes no bits).
-    while (c.from_table && !pair && stw > 2 && smem_bytes(mp, xt, stw, stx, fold) > kMaxDynSmem) stw -= 2;
+    if (c.from_table && !pair)
+        while (stw > 2 && past(kMaxDynSmem, stx)) stw -= 2;
     size_t smem = smem_bytes(mp, xt, stw, stx, fold);
     // Never more CTAs on an SM than its 512 tensor-memory columns hold.
     const size_t least = mp <= 32 ? 77 * 1024 : 115 * 1024;
@@ -709,7 +762,8 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     a.y = static_cast<uint16_t*>(y);
     a.ws = static_cast<uint8_t*>(ws);
     CUtensorMap tmW;
-    if (!encode_2d(&tmW, Wq, static_cast<uint64_t>(K), static_cast<uint64_t>(N), kBlock, kTileRows, true)) return DG_ERR_CUDA;
+    if (!encode_2d(&tmW, Wq, static_cast<uint64_t>(K), static_cast<uint64_t>(N), kBlock, kTileRows, true))
+        return DG_ERR_CUDA;
     const dg_status st = launch_i8_quant(dev, x, qws, const_cast<float*>(a.sx), M, K, xt, stream);
     if (st != DG_OK) return st;
     void* args[] = {&tmW, &a};

@@ -40,8 +40,8 @@
  *   their 8-bit codes (OCP 8-bit float E4M3, "fn" variant: no infinities,
  *   S.1111.111 is NaN, largest magnitude 448).
  * - Every pointer must be 16-byte aligned (what dg_moe_route, dg_logprobs and dg_logits_adjust take, and
- *   the sort's ids, positions and gate weights: on their element's boundary) and K must be a multiple of 8 (bf16 weights) or 16 (e4m3 and 8-bit
- *   integer weights); otherwise DG_ERR_ALIGNMENT /
+ *   the sort's ids, positions and gate weights: on their element's boundary) and K must be a multiple
+ *   of 8 (bf16 weights) or 16 (e4m3 and 8-bit integer weights); otherwise DG_ERR_ALIGNMENT /
  *   DG_ERR_UNSUPPORTED_SHAPE is returned before anything is launched.
  * - Calls are asynchronous on `stream` and make no host synchronisation.
  *   Argument errors are returned synchronously and launch nothing.
@@ -508,7 +508,8 @@ dg_status dg_moe_combine(const void* z, const int32_t* pos, const float* w, void
 /* The gradients of dg_moe_combine with respect to z and w, given that of y:
  *   dz[pos[m, k]] = bf16_rn( w[m, k] * dy[m] )      rows that no slot names stay as they are
  *   dw[m, k]      = sum_n dy[m, n] * z[pos[m, k], n]  in binary32, in a fixed order; 0 where pos is outside
- * The positions inside are distinct (of two slots with one position, either's dz may be there).  dy [M, N], z and dz [P, N] bf16, w and dw [M, topk] fp32.  N % 8 == 0, 1 <= topk <= 32, M and P >= 1. */
+ * The positions inside are distinct (of two slots with one position, either's dz may be there).  dy [M, N], z and
+ * dz [P, N] bf16, w and dw [M, topk] fp32.  N % 8 == 0, 1 <= topk <= 32, M and P >= 1. */
 dg_status dg_moe_combine_grad(const void* dy, const void* z, const int32_t* pos, const float* w, void* dz, float* dw,
                               int M, int topk, int P, int N, dg_stream_t stream);
 
@@ -613,15 +614,17 @@ dg_status dg_table_check(const char* path, const char* arch, int driver_version,
  * write a table that keeps every candidate's time and parameters beside the pick.
  * A candidate replaces the default only if it is bitwise equal and at least 2 %
  * faster, first in the sweep and then in the medians of three more timings of
- * each, taken alternately (pick_us / default_us are then those medians).  mstar PR #1104, "What changed" (the promotion rule, every candidate's
- * time kept beside the choice); Strata PR #1297, "Summary" (byte-compared
- * variants only) and "True-default baseline"; "Decode optimization round 3",
- * "Rejected paths" (re-measure every row against the incumbent in context).
+ * each, taken alternately (pick_us / default_us are then those medians).  mstar PR #1104,
+ * "What changed" (the promotion rule, every candidate's time kept beside the choice);
+ * Strata PR #1297, "Summary" (byte-compared variants only) and "True-default baseline";
+ * "Decode optimization round 3", "Rejected paths" (re-measure every row against the
+ * incumbent in context).
  * Each record names the op and its sizes as dg_workspace_bytes does (N = N_half
  * for gate/up, N = I and K = hidden for MoE W1, N = Nout and K = I for MoE W2);
  * E is the expert count (0 = 128); for A4W4 topk names the format (DG_FP4_*) that is
- * measured; the pick serves both, with fewer stages where a call has room for fewer.  The table is written to out_path as JSON with
- * this build's identity.  The sweep allocates and frees its own device buffers
+ * measured; the pick serves both, with fewer stages where a call has room for fewer, as the 8-bit
+ * integer linear's does at every row count of its bucket.  The table is written to out_path as JSON
+ * with this build's identity.  The sweep allocates and frees its own device buffers
  * (it is an offline tool, not a decode-loop call) and synchronises the device.
  * Returns the first error met; shapes after it are not measured. */
 typedef struct {
