@@ -738,10 +738,9 @@ dg_status launch_i8_linear(const DeviceInfo* dev, const dg_choice& c, const void
     if (c.from_table && !pair)
         while (stw > 2 && past(kMaxDynSmem, stx)) stw -= 2;
     size_t smem = smem_bytes(mp, xt, stw, stx, fold);
-    // Never more CTAs on an SM than its 512 tensor-memory columns hold.
-    const size_t least = mp <= 32 ? 77 * 1024 : 115 * 1024;
-    if (smem < least) smem = least;
     if (smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
+    const size_t least = tc::smem_floor(mp <= 32 ? 256 : 512);
+    if (smem < least) smem = least;
     if (occupancy(fn, threads, smem) < 1) return DG_ERR_UNSUPPORTED_SHAPE;
     uint8_t* qws = static_cast<uint8_t*>(ws) + kWsData;
     I8Args a{};

@@ -322,6 +322,33 @@ __device__ __forceinline__ uint32_t sw128_offset(int r, int c)
     return static_cast<uint32_t>((r / 8) * 1024 + (r % 8) * 128 + ((c ^ (r % 8)) * 16));
 }
 
+// Dynamic shared memory that a CTA with `cols` columns of tensor memory asks for at least, so that whatever CTAs share
+// an SM -- of one kernel, or of kernels on several streams -- never ask for more than its 512 columns.  A CTA that waits
+// in tcgen05.alloc for another's columns holds its cluster peers up; two kernels that wait so for each other on two SMs
+// would never end.
+constexpr size_t kSmSmem = 228 * 1024, kCtaReserve = 1024;       // an SM's shared memory, and the system's part of a CTA
+constexpr size_t smem_floor(int cols)
+{
+    return (cols >= 512 ? 195 : cols >= 256 ? 98 : cols >= 128 ? 59 : 34) * size_t{1024};
+}
+
+// The least shared memory of any CTAs with more than 512 columns together.
+constexpr size_t least_overdrawn()
+{
+    size_t least[33] = {};                                        // by columns / 32
+    size_t best = ~size_t{0};
+    for (int c = 1; c <= 32; ++c) {
+        least[c] = ~size_t{0};
+        for (int t = 1; t <= 16 && t <= c; t *= 2) {
+            const size_t v = least[c - t] + smem_floor(32 * t) + kCtaReserve;
+            if (v < least[c]) least[c] = v;
+        }
+        if (c > 16 && least[c] < best) best = least[c];
+    }
+    return best;
+}
+static_assert(least_overdrawn() > kSmSmem, "CTAs of an SM may ask for more tensor memory than it has");
+
 }  // namespace tc
 
 // 2-D tiled map of rows of `inner` elements, 128-byte swizzle: bf16, or bytes when `u8` (dg_tc_dense.cu).

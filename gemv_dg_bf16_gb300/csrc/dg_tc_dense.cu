@@ -1175,8 +1175,9 @@ dg_status launch_tc(bool gate_up, const DeviceInfo* dev, const dg_choice& c, con
     if (!fn) return DG_ERR_BAD_VARIANT;
     if (pair) {
         const int st = c.params[0] > 0 ? c.params[0] : kPairStages;
-        const size_t smem = smem_bytes_pair(st);
+        size_t smem = smem_bytes_pair(st);
         if (st < 2 || st > 8 || smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
+        if (smem < tc::smem_floor(512)) smem = tc::smem_floor(512);
         if (ws_bytes < tc_workspace_bytes(M, N, K)) return DG_ERR_WORKSPACE_TOO_SMALL;
         TcArgs a{};
         a.N = N;
@@ -1214,8 +1215,9 @@ dg_status launch_tc(bool gate_up, const DeviceInfo* dev, const dg_choice& c, con
     // The epilogue stages the tile (or parks the K-split partial) in the ring.
     if (static_cast<size_t>(stages) * stage_bytes(mp) < static_cast<size_t>(mp) * kTileRows * 4) return DG_ERR_BAD_VARIANT;
     if (recv > 0 && smem_bytes(mp, stages, recv) > (c.params[0] > 0 ? kMaxDynSmem : kCoResidentSmem)) recv = 0;
-    const size_t smem = smem_bytes(mp, stages, recv);
+    size_t smem = smem_bytes(mp, stages, recv);
     if (smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
+    if (smem < tc::smem_floor(mp)) smem = tc::smem_floor(mp);
     if (ws_bytes < tc_workspace_bytes(M, N, K)) return DG_ERR_WORKSPACE_TOO_SMALL;
     TcArgs a{};
     a.N = N;
@@ -1337,8 +1339,7 @@ dg_status launch_tc_a8(const DeviceInfo* dev, const dg_choice& c, const void* x,
     if (smem > kMaxDynSmem) return DG_ERR_UNSUPPORTED_SHAPE;
     // Never more co-resident CTAs than their TMEM columns (4 x MP each) fit in the SM's
     // 512: a CTA waiting in tcgen05.alloc while its cluster peers wait for it would hang.
-    const size_t per_sm = 228 * 1024;
-    const size_t min_smem = per_sm / (512 / (kA8Bufs * mp) + 1) + 1024;
+    const size_t min_smem = tc::smem_floor(kA8Bufs * mp);
     if (smem < min_smem) smem = min_smem;
     if (ws_bytes < (preq ? a8_workspace_bytes(M, K) : kWsData)) return DG_ERR_WORKSPACE_TOO_SMALL;
     uint8_t* qws = static_cast<uint8_t*>(ws) + kWsData;
@@ -1510,8 +1511,7 @@ dg_status launch_tc_a4(const DeviceInfo* dev, const dg_choice& c, bool nv, const
     size_t smem = smem_bytes_a4(mp, nv, stages, recv, xq);
     if (smem > kMaxDynSmem) return DG_ERR_BAD_VARIANT;
     // Never more co-resident CTAs than their TMEM columns fit in the SM's 512.
-    const size_t cols = mp <= 64 ? 128 : 256;
-    const size_t min_smem = 228 * 1024 / (512 / cols + 1) + 1024;
+    const size_t min_smem = tc::smem_floor(mp <= 64 ? 128 : 256);
     if (smem < min_smem) smem = min_smem;
     if (occupancy(fn, kThreads, smem) < 1) return DG_ERR_UNSUPPORTED_SHAPE;
     uint8_t* qws = static_cast<uint8_t*>(ws) + kWsData;

@@ -330,6 +330,7 @@ std::once_flag g_once;
 size_t tc_head_smem(int K, int stages)
 {
     const size_t nkb = (K + kKB - 1) / kKB;
+    static_assert(1024 + kXBlock + 2 * kWBox >= tc::smem_floor(32), "32 columns of tensor memory");
     return 1024 + nkb * kXBlock + static_cast<size_t>(stages) * kWBox + (2 * stages + 4) * 8 + 16;
 }
 

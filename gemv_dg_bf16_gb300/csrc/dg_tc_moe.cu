@@ -327,6 +327,7 @@ std::once_flag g_once;
 
 size_t smem_bytes(int nkb, int stages)
 {
+    static_assert(1024 + kXBlock + 2 * kWBox >= tc::smem_floor(32), "32 columns of tensor memory");
     return 1024 + static_cast<size_t>(nkb) * kXBlock + static_cast<size_t>(stages) * kWBox + (2 * stages + 5) * 8 + 16;
 }
 
