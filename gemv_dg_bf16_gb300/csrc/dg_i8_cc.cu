@@ -5,9 +5,10 @@
 // takes 23 at the rate that weights arrive, so that up to a few tokens nothing is converted.  A CTA owns a
 // contiguous range of weight rows; the ks warps of a slot take every ks-th chunk of 512 elements of four rows,
 // 16 a lane, and the tokens' codes at the same places serve all four (two: 4096 x 4096 4.97 us, four 4.45).  Sixteen
-// loads are in flight a lane: at 4096 x 4096 all that a warp reads.  Lanes are added up by redux.sync and warps by shared-memory
-// atomics, one sum for each row and token of the CTA: everything is an exact integer, so no order
-// matters, and no barrier holds the stream up before the last one (with one a round of rows 12288 x 4096 took 13.1 us).
+// loads are in flight a lane: at 4096 x 4096 all that a warp reads.  Lanes are added up by redux.sync and warps by
+// shared-memory atomics, one sum for each row and token of the CTA: everything is an exact integer, so no order
+// matters, and no barrier holds the stream up before the last one (with one a round of rows 12288 x 4096 took 13.1
+// us).
 // Measured, weights in turn from memory: 4096 x 4096 5.6 us for one token (from L2 4.5), 6.1 for two, 7.4 for four;
 // 12288 x 4096 10.0 (5.0 TB/s), 10.7 and 13.0 (on tensor cores 13.8; for eight 14.2).  A launch, a first load and the
 // tokens' quantisation bind the small ones.

@@ -8,7 +8,8 @@
 // Bytes bind many rows: 24576 x 4096 takes 44.8 us with outputs in turn over 400 MB, 6.74 TB/s of reads and writes
 // together (a copy's 6.69 are half writes, these a third).  128 KB of loads in flight an SM are best: a warp has 16 of
 // them in four CTAs of 104 registers (in five CTAs of 96 it took 48.8), or 8 where that is a row of 2048 (24576 x 2048:
-// 23.6 us in turn, into one output 19.3, most of which then stays in L2; with 16 27.5).  Few rows are a launch and a chain of latencies: 16 x 4096 1.8 us.
+// 23.6 us in turn, into one output 19.3, most of which then stays in L2; with 16 27.5).  Few rows are a launch and a
+// chain of latencies: 16 x 4096 1.8 us.
 #include "dg_i8.cuh"
 #include "dg_internal.h"
 

@@ -3,13 +3,14 @@
 //
 // Calls of 2^20 logits or more, and 2048 more for each entry that a row's lists have room for (the lengths are on the
 // device), of which there are up to 8192, take two kernels.  The first streams the logits under the mask, a batch of
-// 16-byte vectors a thread (in place it writes what the mask changes; without a mask it is left out).  The second edits the entries that the lists name, a CTA a row: it counts the row's tokens in a hash
-// table in shared memory -- how often the sequence has made each, whether its prompt has it, whether a bias is
-// given -- and then edits each entry once, from the logit as it came in.  The table has more slots than the lists have
-// entries, so it never fills up.  Smaller calls, and longer lists, take one kernel: a CTA a slice of a row's vocabulary,
-// which it streams under the mask, with a counter for every entry of the slice; every slice reads the whole
-// list.  Counters count whole numbers, so their order does not matter; the biases of one token are added in list
-// order, by the warp that has its first place.
+// 16-byte vectors a thread (in place it writes what the mask changes; without a mask it is left out).  The second
+// edits the entries that the lists name, a CTA a row: it counts the row's tokens in a hash table in shared memory --
+// how often the sequence has made each, whether its prompt has it, whether a bias is given -- and then edits each
+// entry once, from the logit as it came in.  The table has more slots than the lists have entries, so it never fills
+// up.  Smaller calls, and longer lists, take one kernel: a CTA a slice of a row's vocabulary, which it streams under
+// the mask, with a counter for every entry of the slice; every slice reads the whole list.  Counters count whole
+// numbers, so their order does not matter; the biases of one token are added in list order, by the warp that has its
+// first place.
 // Measured with rows of 248320 bf16, lists of up to 4096 tokens, 64 biases and a mask, one kernel / two: 1 row 5.6 /
 // 16.1 us, 8 rows 10.5 / 17.5, 32 rows 20.1 / 20.7, 64 rows 38.1 / 28.2, 256 rows 105 / 61; with 200 tokens 4 rows 4.8 /
 // 5.2, 8 rows 7.9 / 6.4; 64 rows of 64000 with 1000 tokens 12.9 / 10.8, 32 rows 9.7 / 10.2.  Of the 61 the stream is 41
